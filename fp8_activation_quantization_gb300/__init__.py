@@ -29,6 +29,11 @@ __all__ = [
     "tkq_swiglu_cast_t_clamp", "tkq_swiglu_cast_t_ex", "tkq_per_token_cast_f32", "tkq_swiglu_values", "swiglu_values",
     "use_checked_library", "tkq_checked_build", "tkq_read_check_address",
     "tkq_swiglu_backward_values", "swiglu_backward_values", "tkq_fp8_encode", "fp8_encode",
+    "tkq_route_topk", "tkq_route_topk_backward", "route_topk", "route_topk_backward",
+    "tkq_swiglu_cast_checkpoint", "tkq_swiglu_checkpoint_backward",
+    "tkq_swiglu_checkpoint_backward_cast", "swiglu_forward_cast_and_checkpoint",
+    "swiglu_backward_from_checkpoint", "tkq_residual_norm_cast", "tkq_residual_norm_workspace",
+    "tkq_residual_norm_backward", "residual_norm_and_cast", "residual_norm_backward",
 ]
 
 FMT_E4M3 = 0
@@ -135,6 +140,22 @@ def _open(path):
         lib.tkq_swiglu_backward_values.restype = i
         lib.tkq_fp8_encode.argtypes = [p, p, i64, i, p]
         lib.tkq_fp8_encode.restype = i
+        lib.tkq_route_topk.argtypes = [p, p, p, p, p, i64, i64, i64, i, i, i, i, i, u, f32, p]
+        lib.tkq_route_topk.restype = i
+        lib.tkq_route_topk_backward.argtypes = [p, p, p, p, i64, i64, i64, i, i, u, f32, p]
+        lib.tkq_route_topk_backward.restype = i
+        lib.tkq_swiglu_cast_checkpoint.argtypes = [p, p, p, p, p, p, i64, i64, i, i, i, u, p]
+        lib.tkq_swiglu_cast_checkpoint.restype = i
+        lib.tkq_swiglu_checkpoint_backward.argtypes = [p] * 7 + [i64, i64, i, i, p]
+        lib.tkq_swiglu_checkpoint_backward.restype = i
+        lib.tkq_swiglu_checkpoint_backward_cast.argtypes = [p] * 8 + [i64, i64, i, i, i, u, p]
+        lib.tkq_swiglu_checkpoint_backward_cast.restype = i
+        lib.tkq_residual_norm_cast.argtypes = [p] * 11 + [i64, i64, i, i, u, u, f32, f32, p]
+        lib.tkq_residual_norm_cast.restype = i
+        lib.tkq_residual_norm_workspace.argtypes = [i64, i64]
+        lib.tkq_residual_norm_workspace.restype = i64
+        lib.tkq_residual_norm_backward.argtypes = [p] * 15 + [i64, i64, u, f32, p]
+        lib.tkq_residual_norm_backward.restype = i
         lib.tkq_checked_build.argtypes = []
         lib.tkq_checked_build.restype = i
         lib.tkq_read_check_address.argtypes = [ctypes.POINTER(ctypes.c_uint64), i]
@@ -284,6 +305,67 @@ def tkq_swiglu_backward_cast_ex(x, dy, w, out, sf, T, H, group=GROUP, fmt=FMT_E4
                                 stream=None) -> int:
     return (_lib or load_library()).tkq_swiglu_backward_cast_ex(x, dy, w, out, sf, T, H, group, fmt,
                                                       sf_flags, stream)
+
+
+ROUTE_SIGMOID = 1
+ROUTE_RENORM = 2
+NORM_POST = 1
+NORM_PRE = 2
+NORM_RES_F32 = 4
+
+
+def tkq_route_topk(logits, bias, ids, weights, counts, T, E, ld, dtype, k, n_groups=1,
+                   topk_groups=1, group_top=2, route_flags=0, scale=1.0, stream=None) -> int:
+    return (_lib or load_library()).tkq_route_topk(logits, bias, ids, weights, counts, T, E, ld,
+                                                   dtype, k, n_groups, topk_groups, group_top,
+                                                   route_flags, scale, stream)
+
+
+def tkq_route_topk_backward(logits, ids, dweights, dlogits, T, E, ld, dtype, k, route_flags=0,
+                            scale=1.0, stream=None) -> int:
+    return (_lib or load_library()).tkq_route_topk_backward(logits, ids, dweights, dlogits, T, E,
+                                                            ld, dtype, k, route_flags, scale,
+                                                            stream)
+
+
+def tkq_swiglu_cast_checkpoint(x, w, out, sf, ckpt, ckpt_sf, T, H, group=GROUP, fmt=FMT_E4M3,
+                               ckpt_fmt=FMT_E4M3, sf_flags=0, stream=None) -> int:
+    return (_lib or load_library()).tkq_swiglu_cast_checkpoint(x, w, out, sf, ckpt, ckpt_sf, T, H,
+                                                               group, fmt, ckpt_fmt, sf_flags,
+                                                               stream)
+
+
+def tkq_swiglu_checkpoint_backward(ckpt, ckpt_sf, dy, w, dx, y, dw, T, H, group=GROUP,
+                                   ckpt_fmt=FMT_E4M3, stream=None) -> int:
+    return (_lib or load_library()).tkq_swiglu_checkpoint_backward(ckpt, ckpt_sf, dy, w, dx, y, dw,
+                                                                   T, H, group, ckpt_fmt, stream)
+
+
+def tkq_swiglu_checkpoint_backward_cast(ckpt, ckpt_sf, dy, w, dx, dx_sf, y, dw, T, H, group=GROUP,
+                                        ckpt_fmt=FMT_E4M3, fmt=FMT_E4M3, sf_flags=0,
+                                        stream=None) -> int:
+    return (_lib or load_library()).tkq_swiglu_checkpoint_backward_cast(
+        ckpt, ckpt_sf, dy, w, dx, dx_sf, y, dw, T, H, group, ckpt_fmt, fmt, sf_flags, stream)
+
+
+def tkq_residual_norm_cast(r, h, w_post, gate, w_pre, r_out, out, sf, x_out, rstd_post, rstd_pre,
+                           T, C, group=GROUP, fmt=FMT_E4M3, sf_flags=0, norm_flags=0,
+                           res_scale=1.0, eps=1e-6, stream=None) -> int:
+    return (_lib or load_library()).tkq_residual_norm_cast(
+        r, h, w_post, gate, w_pre, r_out, out, sf, x_out, rstd_post, rstd_pre, T, C, group, fmt,
+        sf_flags, norm_flags, res_scale, eps, stream)
+
+
+def tkq_residual_norm_workspace(T, C) -> int:
+    return (_lib or load_library()).tkq_residual_norm_workspace(T, C)
+
+
+def tkq_residual_norm_backward(dr, dx, r, h, w_post, gate, w_pre, rstd_post, rstd_pre, dr_out, dh,
+                               dgate, dw_post, dw_pre, workspace, T, C, norm_flags=0,
+                               res_scale=1.0, stream=None) -> int:
+    return (_lib or load_library()).tkq_residual_norm_backward(
+        dr, dx, r, h, w_post, gate, w_pre, rstd_post, rstd_pre, dr_out, dh, dgate, dw_post, dw_pre,
+        workspace, T, C, norm_flags, res_scale, stream)
 
 
 def _sf_shape(T: int, groups_per_row: int, sf_flags: int):
@@ -635,6 +717,318 @@ def cast_back(x, sf, fmt=None, group_size=(1, GROUP), out_dtype=None, out=None):
     if st:
         raise TkqError(st, "tkq_cast_back")
     return out
+
+
+def _check_like(t, name, shape, dtypes, device):
+    """A tensor operand: contiguous, of one of `dtypes` and of `shape`, on `device`."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.device != device or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous CUDA tensor on the inputs' device")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {', '.join(map(str, dtypes))}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}")
+
+
+def _check_logits(logits, scores):
+    """T, E, row stride, dtype code and score flag of the logits of a routing call."""
+    import torch
+    if (not isinstance(logits, torch.Tensor) or not logits.is_cuda or logits.dim() != 2
+            or logits.dtype not in (torch.bfloat16, torch.float32)):
+        raise TypeError("logits must be a 2-D bfloat16 or float32 CUDA tensor")
+    T, E = logits.shape
+    ld = logits.stride(0) if T > 1 else E
+    if E > 1 and logits.stride(1) != 1:
+        raise TypeError("logits must be contiguous along the experts")
+    if scores not in ("softmax", "sigmoid"):
+        raise ValueError(f"unknown scores {scores!r}: expected 'softmax' or 'sigmoid'")
+    return (T, E, ld, OUT_BF16 if logits.dtype == torch.bfloat16 else OUT_F32,
+            ROUTE_SIGMOID if scores == "sigmoid" else 0)
+
+
+def route_topk(logits, k: int, scores: str = "softmax", bias=None, num_groups: int = 1,
+               topk_groups: int = 1, num_topk_sum: int = 2, renormalize: bool = True,
+               scale: float = 1.0, counts=None, ids=None, weights=None):
+    """Route each of T tokens to k of E experts: logits bf16 or fp32 [T, E] (rows
+    may be strided) -> (ids int32 [T, k], weights fp32 [T, k]).
+
+    ``scores``: 'softmax' over the experts or the 'sigmoid' of each logit.
+    ``bias`` (fp32 [E]) is added for the choice only.  With ``num_groups`` > 1 the
+    ``topk_groups`` best groups of consecutive experts are searched, a group's
+    score being the sum of its ``num_topk_sum`` (1 or 2) largest keys.  Experts
+    come in falling order, ties to the lowest index; the weights are
+    ``scale`` times the scores, divided by their sum with ``renormalize``.
+    ``counts`` (int32 [E], zeroed by the caller) receives the tokens of each
+    expert by addition.  A logit of -inf or NaN takes its expert out of the
+    row; ids left over are -1 with weight 0."""
+    import torch
+    T, E, ld, dtype, flags = _check_logits(logits, scores)
+    dev = logits.device
+    if bias is not None:
+        _check_like(bias, "bias", (E,), (torch.float32,), dev)
+    if counts is not None:
+        _check_like(counts, "counts", (E,), (torch.int32,), dev)
+    if renormalize:
+        flags |= ROUTE_RENORM
+    k = int(k)
+    if ids is None:
+        ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev)
+    else:
+        _check_out(ids, "ids", logits, 4 * T * k, dtype=torch.int32)
+    if weights is None:
+        weights = torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev)
+    else:
+        _check_out(weights, "weights", logits, 4 * T * k, dtype=torch.float32)
+    with _device_ctx(dev):
+        st = tkq_route_topk(_ptr(logits), _ptr(bias), _ptr(ids), _ptr(weights), _ptr(counts), T, E,
+                            ld, dtype, k, num_groups, topk_groups, num_topk_sum, flags, scale,
+                            _stream_handle(dev))
+    if st:
+        raise TkqError(st, "tkq_route_topk")
+    return ids, weights
+
+
+def route_topk_backward(logits, ids, dweights, scores: str = "softmax", renormalize: bool = True,
+                        scale: float = 1.0, out=None):
+    """Gradient of ``route_topk``'s weights: (logits, its ids, dweights fp32
+    [T, k]) -> dlogits [T, E] in the logits' type.  ``scores``, ``renormalize``
+    and ``scale`` as given to the forward."""
+    import torch
+    T, E, ld, dtype, flags = _check_logits(logits, scores)
+    dev = logits.device
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise TypeError("ids must be an int32 [T, k] tensor")
+    k = ids.shape[1]
+    _check_like(ids, "ids", (T, k), (torch.int32,), dev)
+    _check_like(dweights, "dweights", (T, k), (torch.float32,), dev)
+    if renormalize:
+        flags |= ROUTE_RENORM
+    if out is None:
+        out = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    else:
+        _check_out(out, "out", logits, T * E * logits.element_size(), dtype=logits.dtype)
+    with _device_ctx(dev):
+        st = tkq_route_topk_backward(_ptr(logits), _ptr(ids), _ptr(dweights), _ptr(out), T, E, ld,
+                                     dtype, k, flags, scale, _stream_handle(dev))
+    if st:
+        raise TkqError(st, "tkq_route_topk_backward")
+    return out
+
+
+def swiglu_forward_cast_and_checkpoint(x, fmt="e4m3", num_per_channels: int = GROUP,
+                                       topk_weights=None, ckpt_fmt="e4m3", round_sf: bool = False,
+                                       use_packed_ue8m0: bool = False,
+                                       use_tma_aligned_col_major_sf: bool = False):
+    """``swiglu_forward_and_per_token_cast`` that also keeps its input in 8 bits
+    for the backward: bf16 [T, 2H] (gate | up) -> (codes [T, H], scales,
+    checkpoint codes [T, 2H], checkpoint scales fp32 [T, 2H/128]).  The
+    checkpoint is ``per_token_cast(x, ckpt_fmt)``, bit for bit; the scale-layout
+    options apply to the cast's scales."""
+    import torch
+    _check_input(x)
+    f, cf = _fmt_code(fmt), _fmt_code(ckpt_fmt)
+    T, H2 = x.shape
+    if H2 % 2:
+        raise ValueError("x must have an even number of columns (gate | up)")
+    H, dev = H2 // 2, x.device
+    g = max(num_per_channels, 1)
+    _check_weights(topk_weights, T, x)
+    flags = _sf_flags(round_sf, use_packed_ue8m0, use_tma_aligned_col_major_sf)
+    out = torch.empty((T, H), dtype=_fp8_dtype(f), device=dev)
+    out_sf = sf_tensor(T, H // g, flags, dev)
+    ckpt = torch.empty((T, H2), dtype=_fp8_dtype(cf), device=dev)
+    ckpt_sf = torch.empty((T, 2 * (H // g)), dtype=torch.float32, device=dev)
+    with _device_ctx(dev):
+        st = tkq_swiglu_cast_checkpoint(_ptr(x), _ptr(topk_weights), _ptr(out), _ptr(out_sf),
+                                        _ptr(ckpt), _ptr(ckpt_sf), T, H, num_per_channels, f, cf,
+                                        flags, _stream_handle(dev))
+    if st:
+        raise TkqError(st, "tkq_swiglu_cast_checkpoint")
+    return out, out_sf, ckpt, ckpt_sf
+
+
+def swiglu_backward_from_checkpoint(ckpt, ckpt_sf, dy, fmt=None, num_per_channels: int = GROUP,
+                                    topk_weights=None, ckpt_fmt=None,
+                                    with_weight_grad: bool = False, with_y: bool = False,
+                                    round_sf: bool = False, use_packed_ue8m0: bool = False,
+                                    use_tma_aligned_col_major_sf: bool = False):
+    """Backward of y = silu(gate) * up [* w] from its 8-bit checkpoint (codes
+    [T, 2H], scales fp32 [T, 2H/128]) and dy bf16 [T, H]
+    -> (dx, dx_sf, dw, y).
+
+    dx is [dg | du]: bf16 [T, 2H] with dx_sf None (``fmt`` None), or its
+    per-token cast in ``fmt`` with the scales dx_sf.  dw: with
+    ``with_weight_grad`` the gradient of the routing weights (fp32 [T]), else
+    None.  y: with ``with_y`` the forward's output again in bf16 [T, H], for the
+    weight gradient of the product that follows, else None."""
+    import torch
+    _check_input(dy, "dy")
+    T, H = dy.shape
+    dev = dy.device
+    if ckpt_fmt is None and isinstance(ckpt, torch.Tensor):
+        ckpt_fmt = {torch.float8_e4m3fn: "e4m3", torch.float8_e5m2: "e5m2"}.get(ckpt.dtype)
+        if ckpt_fmt is None:
+            raise ValueError("ckpt_fmt is required for codes that are not an FP8 dtype")
+    cf = _fmt_code(ckpt_fmt)
+    g = max(num_per_channels, 1)
+    _check_like(ckpt, "ckpt", (T, 2 * H), (_fp8_dtype(cf), torch.uint8), dev)
+    _check_like(ckpt_sf, "ckpt_sf", (T, 2 * (H // g)), (torch.float32,), dev)
+    _check_weights(topk_weights, T, dy)
+    flags = _sf_flags(round_sf, use_packed_ue8m0, use_tma_aligned_col_major_sf)
+    dw = torch.empty((T,), dtype=torch.float32, device=dev) if with_weight_grad else None
+    y = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if with_y else None
+    if fmt is None:
+        if flags:
+            raise ValueError("the scale-layout options need fmt")
+        dx, dx_sf = torch.empty((T, 2 * H), dtype=torch.bfloat16, device=dev), None
+    else:
+        f = _fmt_code(fmt)
+        dx = torch.empty((T, 2 * H), dtype=_fp8_dtype(f), device=dev)
+        dx_sf = sf_tensor(T, 2 * (H // g), flags, dev)
+    with _device_ctx(dev):
+        stream = _stream_handle(dev)
+        if fmt is None:
+            st = tkq_swiglu_checkpoint_backward(_ptr(ckpt), _ptr(ckpt_sf), _ptr(dy),
+                                                _ptr(topk_weights), _ptr(dx), _ptr(y), _ptr(dw), T,
+                                                H, num_per_channels, cf, stream)
+        else:
+            st = tkq_swiglu_checkpoint_backward_cast(_ptr(ckpt), _ptr(ckpt_sf), _ptr(dy),
+                                                     _ptr(topk_weights), _ptr(dx), _ptr(dx_sf),
+                                                     _ptr(y), _ptr(dw), T, H, num_per_channels, cf,
+                                                     f, flags, stream)
+    if st:
+        raise TkqError(st, "tkq_swiglu_checkpoint_backward")
+    return dx, dx_sf, dw, y
+
+
+def _check_stream(r, name):
+    """The residual stream: a contiguous bf16 or fp32 [T, C] tensor."""
+    _check_input(r, name, allow_f32=True)
+    return r.shape
+
+
+def residual_norm_and_cast(r, h=None, w_post=None, gate=None, w_pre=None, post_norm: bool = True,
+                           res_scale: float = 1.0, eps: float = 1e-6, fmt="e4m3",
+                           with_bf16: bool = False, num_per_channels: int = GROUP,
+                           round_sf: bool = False, use_packed_ue8m0: bool = False,
+                           use_tma_aligned_col_major_sf: bool = False):
+    """The norms around a block, its gate and its residual scale, ending in the
+    cast of the next product's input:
+
+        r' = r + res_scale * norm(h) * w_post * sigmoid(gate)
+        x  = norm(r') * w_pre
+
+    with norm(v) = v / sqrt(mean(v^2) + eps) over the channels.  r: the residual
+    stream, bf16 or fp32 [T, C]; h: the block's output, bf16 [T, C] (None before
+    the first block: r' is r); gate: bf16 [T, C] or None; w_post, w_pre: fp32
+    [C] or None; ``post_norm`` False leaves h as it is.
+    -> (r', codes, scales, x, rstd_post, rstd_pre): the FP8 cast of x unless
+    ``fmt`` is None, x in bf16 with ``with_bf16``, and the two norms' factors
+    (fp32 [T]) that the backward takes; what is not asked for is None, and
+    without ``fmt`` and ``with_bf16`` there is no second norm."""
+    import torch
+    T, C = _check_stream(r, "r")
+    dev = r.device
+    bf16, f32 = (torch.bfloat16,), (torch.float32,)
+    flags = NORM_RES_F32 if r.dtype == torch.float32 else 0
+    r_out = r
+    rstd_post = rstd_pre = out = sf = x = None
+    if h is not None:
+        _check_like(h, "h", (T, C), bf16, dev)
+        r_out = torch.empty_like(r)
+        if post_norm:
+            flags |= NORM_POST
+            rstd_post = torch.empty((T,), dtype=torch.float32, device=dev)
+    elif w_post is not None or gate is not None:
+        raise ValueError("w_post and gate need h")
+    if gate is not None:
+        _check_like(gate, "gate", (T, C), bf16, dev)
+    if w_post is not None:
+        _check_like(w_post, "w_post", (C,), f32, dev)
+    if w_pre is not None:
+        _check_like(w_pre, "w_pre", (C,), f32, dev)
+    f, sf_flags = FMT_E4M3, 0
+    if fmt is not None or with_bf16:
+        flags |= NORM_PRE
+        rstd_pre = torch.empty((T,), dtype=torch.float32, device=dev)
+        if fmt is not None:
+            f = _fmt_code(fmt)
+            sf_flags = _sf_flags(round_sf, use_packed_ue8m0, use_tma_aligned_col_major_sf)
+            out = torch.empty((T, C), dtype=_fp8_dtype(f), device=dev)
+            sf = sf_tensor(T, C // max(num_per_channels, 1), sf_flags, dev)
+        if with_bf16:
+            x = torch.empty((T, C), dtype=torch.bfloat16, device=dev)
+    elif w_pre is not None:
+        raise ValueError("w_pre needs fmt or with_bf16")
+    with _device_ctx(dev):
+        st = tkq_residual_norm_cast(_ptr(r), _ptr(h), _ptr(w_post), _ptr(gate), _ptr(w_pre),
+                                    None if h is None else _ptr(r_out), _ptr(out), _ptr(sf),
+                                    _ptr(x), _ptr(rstd_post), _ptr(rstd_pre), T, C,
+                                    num_per_channels, f, sf_flags, flags, res_scale, eps,
+                                    _stream_handle(dev))
+    if st:
+        raise TkqError(st, "tkq_residual_norm_cast")
+    return r_out, out, sf, x, rstd_post, rstd_pre
+
+
+def residual_norm_backward(dr, r, h=None, dx=None, w_post=None, gate=None, w_pre=None,
+                           rstd_post=None, rstd_pre=None, res_scale: float = 1.0):
+    """Gradients of ``residual_norm_and_cast``: dr (the stream's type, or None) and
+    dx (bf16, or None where the forward had no second norm) are the gradients of
+    its r' and x, r is its r', and h, gate, the weights, the factors and
+    ``res_scale`` are the forward's (rstd_post None: there was no post-norm).
+    -> (dr of the forward's r, dh, dgate, dw_post, dw_pre); None for what has no
+    counterpart.  The cast is passed through."""
+    import torch
+    lead = dr if dr is not None else r
+    T, C = _check_stream(lead, "dr" if dr is not None else "r")
+    dev = lead.device
+    bf16, f32 = (torch.bfloat16,), (torch.float32,)
+    flags = NORM_RES_F32 if lead.dtype == torch.float32 else 0
+    dh = dgate = dw_post = dw_pre = work = None
+    if dx is not None:
+        flags |= NORM_PRE
+        _check_like(dx, "dx", (T, C), bf16, dev)
+        _check_like(r, "r", (T, C), (lead.dtype,), dev)
+        _check_like(rstd_pre, "rstd_pre", (T,), f32, dev)
+        if w_pre is not None:
+            _check_like(w_pre, "w_pre", (C,), f32, dev)
+            dw_pre = torch.empty((C,), dtype=torch.float32, device=dev)
+    elif dr is None:
+        raise ValueError("dr or dx is needed")
+    elif w_pre is not None:
+        raise ValueError("w_pre needs dx")
+    if h is not None:
+        _check_like(h, "h", (T, C), bf16, dev)
+        dh = torch.empty_like(h)
+        if rstd_post is not None:
+            flags |= NORM_POST
+            _check_like(rstd_post, "rstd_post", (T,), f32, dev)
+        if gate is not None:
+            _check_like(gate, "gate", (T, C), bf16, dev)
+            dgate = torch.empty_like(gate)
+        if w_post is not None:
+            _check_like(w_post, "w_post", (C,), f32, dev)
+            dw_post = torch.empty((C,), dtype=torch.float32, device=dev)
+    elif w_post is not None or gate is not None or rstd_post is not None:
+        raise ValueError("w_post, gate and rstd_post need h")
+    dr_out = torch.empty_like(lead)
+    with _device_ctx(dev):
+        if T == 0:  # sums over no rows
+            for dw in (dw_post, dw_pre):
+                if dw is not None:
+                    dw.zero_()
+        elif dw_post is not None or dw_pre is not None:
+            work = torch.empty((max(tkq_residual_norm_workspace(T, C), 0),), dtype=torch.uint8,
+                               device=dev)
+        st = tkq_residual_norm_backward(_ptr(dr), _ptr(dx), _ptr(r) if dx is not None else None,
+                                        _ptr(h), _ptr(w_post), _ptr(gate), _ptr(w_pre),
+                                        _ptr(rstd_post), _ptr(rstd_pre), _ptr(dr_out), _ptr(dh),
+                                        _ptr(dgate), _ptr(dw_post), _ptr(dw_pre), _ptr(work), T, C,
+                                        flags, res_scale, _stream_handle(dev))
+    if st:
+        raise TkqError(st, "tkq_residual_norm_backward")
+    return dr_out, dh, dgate, dw_post, dw_pre
 
 
 def swiglu_values(x, topk_weights=None):

@@ -27,34 +27,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Two FP8 codes (low byte = first element) -> binary16x2 (low half = first).
-template <int FMT>
-__device__ __forceinline__ uint32_t fp8x2_to_f16x2(uint32_t two) {
-    uint32_t h;
-    const uint16_t b = static_cast<uint16_t>(two);
-    if constexpr (FMT == kFmtE4M3)
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(b));
-    else
-        asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"(b));
-    return h;
-}
-
-__device__ __forceinline__ void f16x2_to_f32(uint32_t h, float& lo, float& hi) {
-    asm("{ .reg .f16 l, u;\n\t"
-        "mov.b32 {l, u}, %2;\n\t"
-        "cvt.f32.f16 %0, l;\n\t"
-        "cvt.f32.f16 %1, u; }"
-        : "=f"(lo), "=f"(hi)
-        : "r"(h));
-}
-
-// Two floats -> bf16x2, round to nearest even (low half = a).
-__device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-    return r;
-}
-
 // Bulk-async store of `bytes` (a multiple of 16) from shared memory to global
 // memory, tracked as one bulk group of the issuing thread; checked like every
 // other store in the checked build.

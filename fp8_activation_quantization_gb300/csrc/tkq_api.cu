@@ -162,6 +162,24 @@ unsigned long long* bad_address_word() {
     return static_cast<unsigned long long*>(p);
 }
 
+#ifdef TKQ_CHECKED
+// Adds one buffer to the call's table.
+void register_one(Range r, bool output) {
+    CheckTable& t = host_check_table();
+    if (output) {
+        uint64_t withhold = 0;
+        if (const char* env = std::getenv("TKQ_CHECK_WITHHOLD"))
+            withhold = std::strtoull(env, nullptr, 10);
+        r.hi = r.hi - r.lo > withhold ? r.hi - withhold : r.lo;
+    }
+    if (r.hi <= r.lo || t.n >= kCheckMax) return;
+    t.lo[t.n] = r.lo;
+    t.hi[t.n] = r.hi;
+    if (output) t.writable |= 1u << t.n;
+    ++t.n;
+}
+#endif
+
 // The buffers of the call about to launch, for the checked build's access
 // checks (a no-op otherwise): inputs may be read, outputs read and written.
 // Empty ranges (an absent optional buffer) are skipped.  The environment
@@ -173,19 +191,8 @@ void register_call(std::initializer_list<Range> inputs, std::initializer_list<Ra
 #ifdef TKQ_CHECKED
     CheckTable& t = host_check_table();
     t = CheckTable{};
-    uint64_t withhold = 0;
-    if (const char* env = std::getenv("TKQ_CHECK_WITHHOLD"))
-        withhold = std::strtoull(env, nullptr, 10);
-    auto add = [&t](uintptr_t lo, uintptr_t hi, bool out) {
-        if (hi <= lo || t.n >= kCheckMax) return;
-        t.lo[t.n] = lo;
-        t.hi[t.n] = hi;
-        if (out) t.writable |= 1u << t.n;
-        ++t.n;
-    };
-    for (const Range& r : inputs) add(r.lo, r.hi, false);
-    for (const Range& r : outputs)
-        add(r.lo, r.hi - r.lo > withhold ? r.hi - withhold : r.lo, true);
+    for (const Range& r : inputs) register_one(r, false);
+    for (const Range& r : outputs) register_one(r, true);
     t.status = device_status_word();
     t.bad = bad_address_word();
 #else
@@ -253,6 +260,39 @@ tkq_status check_common(int64_t T, int64_t C, int group, int fmt) {
     if (fmt != TKQ_FMT_E4M3 && fmt != TKQ_FMT_E5M2) return TKQ_ERR_FMT;
     // TMA row coordinates are 32-bit; C beyond 2^30 is far beyond one GPU
     if (T > INT32_MAX || C > (int64_t{1} << 30)) return TKQ_ERR_SHAPE;
+    return TKQ_OK;
+}
+
+// One buffer of a call: its address, bytes and alignment.  Absent buffers
+// (NULL) take no part.
+struct Buffer {
+    const void* p;
+    int64_t bytes;
+    uintptr_t align;
+};
+
+// Alignment of all buffers, and overlap of every output with every other
+// buffer; then the call's table for the checked build.
+template <size_t NI, size_t NO>
+tkq_status check_buffers(const Buffer (&in)[NI], const Buffer (&out)[NO]) {
+    for (const Buffer& b : in)
+        if (b.p && !tkq::aligned(b.p, b.align)) return TKQ_ERR_ALIGN;
+    for (const Buffer& b : out)
+        if (b.p && !tkq::aligned(b.p, b.align)) return TKQ_ERR_ALIGN;
+    const auto range = [](const Buffer& b) {
+        return b.p ? tkq::span(b.p, b.bytes) : tkq::Range{0, 0};
+    };
+    for (size_t i = 0; i < NO; ++i) {
+        for (const Buffer& b : in)
+            if (tkq::overlap(range(out[i]), range(b))) return TKQ_ERR_ALIAS;
+        for (size_t k = i + 1; k < NO; ++k)
+            if (tkq::overlap(range(out[i]), range(out[k]))) return TKQ_ERR_ALIAS;
+    }
+#ifdef TKQ_CHECKED
+    tkq::register_call({}, {});
+    for (const Buffer& b : in) tkq::register_one(range(b), false);
+    for (const Buffer& b : out) tkq::register_one(range(b), true);
+#endif
     return TKQ_OK;
 }
 
@@ -534,6 +574,237 @@ tkq_status tkq_cast_back(const void* codes, const float* sf, void* out, int64_t 
     return launch_status(tkq::launch_cast_back(codes, sf, out, T, C, group_rows, group_cols, fmt,
                                                out_dtype == TKQ_OUT_BF16,
                                                static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+tkq_status check_route(int64_t T, int64_t E, int64_t ld, int dtype, int k, unsigned flags,
+                       float scale) {
+    if (T < 0 || T > INT32_MAX || E <= 0 || E > 1024 || ld < E || ld > (int64_t{1} << 28) ||
+        k <= 0 || k > 32 || k > E)
+        return TKQ_ERR_SHAPE;
+    if (dtype != TKQ_OUT_F32 && dtype != TKQ_OUT_BF16) return TKQ_ERR_FMT;
+    if (flags & ~(TKQ_ROUTE_SIGMOID | TKQ_ROUTE_RENORM)) return TKQ_ERR_FLAGS;
+    if (!std::isfinite(scale)) return TKQ_ERR_VALUE;
+    return TKQ_OK;
+}
+
+tkq::RouteShape route_shape(int64_t E, int dtype, int k, unsigned flags, float scale) {
+    tkq::RouteShape s = {};
+    s.E = static_cast<int>(E);
+    s.k = k;
+    s.groups = s.topk_groups = s.group_top = 1;
+    s.sigmoid = flags & TKQ_ROUTE_SIGMOID;
+    s.renorm = flags & TKQ_ROUTE_RENORM;
+    s.bf16 = dtype == TKQ_OUT_BF16;
+    s.scale = scale;
+    return s;
+}
+
+// Bytes of T rows of E elements with a row stride of ld elements.
+int64_t strided_bytes(int64_t T, int64_t E, int64_t ld, int64_t item) {
+    return ((T - 1) * ld + E) * item;
+}
+}  // namespace
+
+tkq_status tkq_route_topk(const void* logits, const float* bias, int32_t* ids, float* weights,
+                          int32_t* counts, int64_t T, int64_t E, int64_t ld, int dtype, int k,
+                          int n_groups, int topk_groups, int group_top, unsigned route_flags,
+                          float scale, tkq_stream_t stream) {
+    tkq_status st = check_route(T, E, ld, dtype, k, route_flags, scale);
+    if (st != TKQ_OK) return st;
+    if (n_groups <= 0 || n_groups > 32 || E % n_groups || topk_groups <= 0 ||
+        topk_groups > n_groups)
+        return TKQ_ERR_SHAPE;
+    if (group_top != 1 && group_top != 2) return TKQ_ERR_VALUE;
+    if (T == 0) return TKQ_OK;
+    if (!logits || !ids || !weights) return TKQ_ERR_NULL;
+    const int64_t item = dtype == TKQ_OUT_BF16 ? 2 : 4;
+    const Buffer in[] = {{logits, strided_bytes(T, E, ld, item), static_cast<uintptr_t>(item)},
+                         {bias, E * 4, 4}};
+    const Buffer out[] = {{ids, T * k * 4, 4}, {weights, T * k * 4, 4}, {counts, E * 4, 4}};
+    if ((st = check_buffers(in, out)) != TKQ_OK) return st;
+    tkq::RouteShape s = route_shape(E, dtype, k, route_flags, scale);
+    s.groups = n_groups;
+    s.topk_groups = topk_groups;
+    s.group_top = group_top;
+    return launch_status(tkq::launch_route_topk(logits, bias, ids, weights, counts, T, ld, s,
+                                                static_cast<cudaStream_t>(stream)));
+}
+
+tkq_status tkq_route_topk_backward(const void* logits, const int32_t* ids, const float* dweights,
+                                   void* dlogits, int64_t T, int64_t E, int64_t ld, int dtype,
+                                   int k, unsigned route_flags, float scale, tkq_stream_t stream) {
+    tkq_status st = check_route(T, E, ld, dtype, k, route_flags, scale);
+    if (st != TKQ_OK) return st;
+    if (T == 0) return TKQ_OK;
+    if (!logits || !ids || !dweights || !dlogits) return TKQ_ERR_NULL;
+    const int64_t item = dtype == TKQ_OUT_BF16 ? 2 : 4;
+    const uintptr_t al = static_cast<uintptr_t>(item);
+    const Buffer in[] = {{logits, strided_bytes(T, E, ld, item), al},
+                         {ids, T * k * 4, 4},
+                         {dweights, T * k * 4, 4}};
+    const Buffer out[] = {{dlogits, T * E * item, al}};
+    if ((st = check_buffers(in, out)) != TKQ_OK) return st;
+    return launch_status(tkq::launch_route_topk_backward(
+        logits, ids, dweights, dlogits, T, ld, route_shape(E, dtype, k, route_flags, scale),
+        static_cast<cudaStream_t>(stream)));
+}
+
+tkq_status tkq_swiglu_cast_checkpoint(const void* x, const float* w, void* out, void* sf,
+                                      void* ckpt, float* ckpt_sf, int64_t T, int64_t H, int group,
+                                      int fmt, int ckpt_fmt, unsigned sf_flags,
+                                      tkq_stream_t stream) {
+    tkq_status st = check_common(T, H, group, fmt);
+    if (st != TKQ_OK || (st = check_common(T, H, group, ckpt_fmt)) != TKQ_OK) return st;
+    if (sf_flags & ~kSfAllFlags) return TKQ_ERR_FLAGS;
+    if (T == 0) return TKQ_OK;
+    if (!x || !out || !sf || !ckpt || !ckpt_sf) return TKQ_ERR_NULL;
+    const Buffer ins[] = {{x, T * H * 4, 16}, {w, T * 4, 4}};
+    const Buffer outs[] = {
+        {out, T * H, 16},
+        {sf, tkq_sf_bytes(T, H / group, sf_flags), (sf_flags & TKQ_SF_COL_MAJOR) ? 16u : 4u},
+        {ckpt, T * 2 * H, 16},
+        {ckpt_sf, T * 2 * (H / group) * 4, 4}};
+    if ((st = check_buffers(ins, outs)) != TKQ_OK) return st;
+    return launch_status(tkq::launch_swiglu_save(x, w, out, sf, ckpt, ckpt_sf, T, H, fmt, ckpt_fmt,
+                                                 sf_flags, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+// fmt: an FP8 format, or 2 for bf16 gradients (no dx_sf).
+tkq_status swiglu_restore_impl(const void* ckpt, const float* ckpt_sf, const void* dy,
+                               const float* w, void* dx, void* dx_sf, void* y, float* dw,
+                               int64_t T, int64_t H, int group, int ckpt_fmt, int fmt,
+                               unsigned sf_flags, tkq_stream_t stream) {
+    const bool cast = fmt != 2;
+    tkq_status st = check_common(T, H, group, ckpt_fmt);
+    if (st != TKQ_OK) return st;
+    if (sf_flags & ~kSfAllFlags) return TKQ_ERR_FLAGS;
+    if (T == 0) return TKQ_OK;
+    if (!ckpt || !ckpt_sf || !dy || !dx || (cast && !dx_sf)) return TKQ_ERR_NULL;
+    const Buffer ins[] = {{ckpt, T * 2 * H, 16},
+                          {ckpt_sf, T * 2 * (H / group) * 4, 4},
+                          {dy, T * H * 2, 16},
+                          {w, T * 4, 4}};
+    const Buffer outs[] = {{dx, T * 2 * H * (cast ? 1 : 2), 16},
+                           {cast ? dx_sf : nullptr, tkq_sf_bytes(T, 2 * (H / group), sf_flags),
+                            (sf_flags & TKQ_SF_COL_MAJOR) ? 16u : 4u},
+                           {y, T * H * 2, 16},
+                           {dw, T * 4, 4}};
+    if ((st = check_buffers(ins, outs)) != TKQ_OK) return st;
+    return launch_status(tkq::launch_swiglu_restore(ckpt, ckpt_sf, dy, w, dx, dx_sf, y, dw, T, H,
+                                                    ckpt_fmt, fmt, sf_flags,
+                                                    static_cast<cudaStream_t>(stream)));
+}
+}  // namespace
+
+tkq_status tkq_swiglu_checkpoint_backward(const void* ckpt, const float* ckpt_sf, const void* dy,
+                                          const float* w, void* dx, void* y, float* dw, int64_t T,
+                                          int64_t H, int group, int ckpt_fmt, tkq_stream_t stream) {
+    return swiglu_restore_impl(ckpt, ckpt_sf, dy, w, dx, nullptr, y, dw, T, H, group, ckpt_fmt, 2,
+                               0u, stream);
+}
+
+tkq_status tkq_swiglu_checkpoint_backward_cast(const void* ckpt, const float* ckpt_sf,
+                                               const void* dy, const float* w, void* dx,
+                                               void* dx_sf, void* y, float* dw, int64_t T,
+                                               int64_t H, int group, int ckpt_fmt, int fmt,
+                                               unsigned sf_flags, tkq_stream_t stream) {
+    if (const tkq_status st = check_common(T, H, group, fmt)) return st;
+    return swiglu_restore_impl(ckpt, ckpt_sf, dy, w, dx, dx_sf, y, dw, T, H, group, ckpt_fmt, fmt,
+                               sf_flags, stream);
+}
+
+namespace {
+constexpr unsigned kNormAllFlags = TKQ_NORM_POST | TKQ_NORM_PRE | TKQ_NORM_RES_F32;
+constexpr int64_t kNormMaxChannels = 16384;
+
+tkq_status check_norm(int64_t T, int64_t C, unsigned norm_flags, float res_scale) {
+    if (T < 0 || T > INT32_MAX || C <= 0 || C > kNormMaxChannels || C % 128) return TKQ_ERR_SHAPE;
+    if (norm_flags & ~kNormAllFlags) return TKQ_ERR_FLAGS;
+    if (!std::isfinite(res_scale)) return TKQ_ERR_VALUE;
+    return TKQ_OK;
+}
+}  // namespace
+
+tkq_status tkq_residual_norm_cast(const void* r, const void* h, const float* w_post,
+                                  const void* gate, const float* w_pre, void* r_out, void* out,
+                                  void* sf, void* x_out, float* rstd_post, float* rstd_pre,
+                                  int64_t T, int64_t C, int group, int fmt, unsigned sf_flags,
+                                  unsigned norm_flags, float res_scale, float eps,
+                                  tkq_stream_t stream) {
+    tkq_status st = check_norm(T, C, norm_flags, res_scale);
+    if (st != TKQ_OK || (st = check_common(T, C, group, fmt)) != TKQ_OK) return st;
+    if (!(eps >= 0.0f && std::isfinite(eps))) return TKQ_ERR_VALUE;
+    const bool post = norm_flags & TKQ_NORM_POST, pre = norm_flags & TKQ_NORM_PRE;
+    if (sf_flags & ~kSfAllFlags) return TKQ_ERR_FLAGS;
+    if (T == 0) return TKQ_OK;
+    if ((!h && (post || w_post || gate || r_out)) || (!post && rstd_post) ||
+        (!pre && (w_pre || out || x_out || rstd_pre)) || (!h && !pre))
+        return TKQ_ERR_FLAGS;
+    if (!r || (h && !r_out) || (pre && !out && !x_out) || !out != !sf) return TKQ_ERR_NULL;
+    const int64_t n = T * C, rb = norm_flags & TKQ_NORM_RES_F32 ? 4 : 2;
+    const Buffer ins[] = {{r, n * rb, 16},
+                          {h, n * 2, 16},
+                          {w_post, C * 4, 16},
+                          {gate, n * 2, 16},
+                          {w_pre, C * 4, 16}};
+    const Buffer outs[] = {
+        {r_out, n * rb, 16},
+        {out, n, 16},
+        {sf, tkq_sf_bytes(T, C / group, sf_flags), (sf_flags & TKQ_SF_COL_MAJOR) ? 16u : 4u},
+        {x_out, n * 2, 16},
+        {rstd_post, T * 4, 4},
+        {rstd_pre, T * 4, 4}};
+    if ((st = check_buffers(ins, outs)) != TKQ_OK) return st;
+    const tkq::ResidualNorm a = {r,  h,   gate,  w_post,    w_pre,    r_out, out, sf,
+                                 x_out, rstd_post, rstd_pre, T, C, res_scale, eps, post,
+                                 pre, rb == 4};
+    return launch_status(
+        tkq::launch_residual_norm(a, fmt, sf_flags, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t tkq_residual_norm_workspace(int64_t T, int64_t C) {
+    if (check_norm(T, C, 0u, 0.0f) != TKQ_OK) return -1;
+    return tkq::residual_norm_parts(T, C) * 2 * C * 4;
+}
+
+tkq_status tkq_residual_norm_backward(const void* dr, const void* dx, const void* r, const void* h,
+                                      const float* w_post, const void* gate, const float* w_pre,
+                                      const float* rstd_post, const float* rstd_pre, void* dr_out,
+                                      void* dh, void* dgate, float* dw_post, float* dw_pre,
+                                      void* workspace, int64_t T, int64_t C, unsigned norm_flags,
+                                      float res_scale, tkq_stream_t stream) {
+    tkq_status st = check_norm(T, C, norm_flags, res_scale);
+    if (st != TKQ_OK) return st;
+    const bool post = norm_flags & TKQ_NORM_POST, pre = norm_flags & TKQ_NORM_PRE;
+    if (T == 0) return TKQ_OK;
+    if ((!h && (post || w_post || gate || dh || dgate || dw_post)) || (!gate && dgate) ||
+        (!pre && (dx || w_pre || dw_pre)))
+        return TKQ_ERR_FLAGS;
+    if (!dr_out || (!dr && !dx) || (h && !dh) || (gate && !dgate) || (post && !rstd_post) ||
+        (pre && (!dx || !r || !rstd_pre)) || ((dw_post || dw_pre) && !workspace))
+        return TKQ_ERR_NULL;
+    const int64_t n = T * C, rb = norm_flags & TKQ_NORM_RES_F32 ? 4 : 2;
+    const Buffer ins[] = {{dr, n * rb, 16},
+                          {dx, n * 2, 16},
+                          {pre ? r : nullptr, n * rb, 16},
+                          {h, n * 2, 16},
+                          {w_post, C * 4, 16},
+                          {gate, n * 2, 16},
+                          {w_pre, C * 4, 16},
+                          {post ? rstd_post : nullptr, T * 4, 4},
+                          {pre ? rstd_pre : nullptr, T * 4, 4}};
+    const Buffer outs[] = {{dr_out, n * rb, 16}, {dh, n * 2, 16},
+                           {dgate, n * 2, 16},   {dw_post, C * 4, 16},
+                           {dw_pre, C * 4, 16},  {dw_post || dw_pre ? workspace : nullptr,
+                                                  tkq_residual_norm_workspace(T, C), 16}};
+    if ((st = check_buffers(ins, outs)) != TKQ_OK) return st;
+    const tkq::ResidualNormGrad a = {dx,     dr, r,     h,       gate,   w_post,    w_pre,
+                                     rstd_post, rstd_pre, dr_out, dh, dgate, dw_post, dw_pre,
+                                     workspace, T, C, res_scale, post, rb == 4};
+    return launch_status(
+        tkq::launch_residual_norm_backward(a, static_cast<cudaStream_t>(stream)));
 }
 
 tkq_status tkq_swiglu_values(const void* x, const float* w, float* y, int64_t T, int64_t H,

@@ -131,6 +131,13 @@ __device__ __forceinline__ float4 ld_ro(const float4* p) {
     return access_ok(p, 16, false) ? __ldg(p) : make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
+__device__ __forceinline__ int32_t ld_ro(const int32_t* p) {
+    return access_ok(p, 4, false) ? __ldg(p) : 0;
+}
+__device__ __forceinline__ uint16_t ld_ro(const uint16_t* p) {
+    return access_ok(p, 2, false) ? __ldg(p) : uint16_t{0};
+}
+
 // Streaming stores (.cs: the output is not read again by this kernel).
 __device__ __forceinline__ void st_stream(uint2* p, uint2 v) {
     if (!access_ok(p, 8, true)) return;
@@ -161,8 +168,17 @@ __device__ __forceinline__ void st_plain(float* p, float v) {
 __device__ __forceinline__ void st_plain(float4* p, float4 v) {
     if (access_ok(p, 16, true)) *p = v;
 }
+__device__ __forceinline__ void st_plain(int32_t* p, int32_t v) {
+    if (access_ok(p, 4, true)) *p = v;
+}
+__device__ __forceinline__ void st_plain(uint16_t* p, uint16_t v) {
+    if (access_ok(p, 2, true)) *p = v;
+}
 __device__ __forceinline__ void atomic_add_count(unsigned long long* p, unsigned long long v) {
     if (access_ok(p, 8, true)) atomicAdd(p, v);
+}
+__device__ __forceinline__ void atomic_add_count(int32_t* p, int32_t v) {
+    if (access_ok(p, 4, true)) atomicAdd(p, v);
 }
 
 // ---------------------------------------------------------------------------
@@ -178,6 +194,51 @@ __device__ __forceinline__ void unpack8(const uint4& q, float* v) {
     v[2] = bf16_lo(q.y); v[3] = bf16_hi(q.y);
     v[4] = bf16_lo(q.z); v[5] = bf16_hi(q.z);
     v[6] = bf16_lo(q.w); v[7] = bf16_hi(q.w);
+}
+
+// ---------------------------------------------------------------------------
+// FP8 -> fp32 (exact: every E4M3 and E5M2 value is a binary16 value), fp32 -> bf16
+// ---------------------------------------------------------------------------
+
+// Two FP8 codes (low byte = first element) -> binary16x2 (low half = first).
+template <int FMT>
+__device__ __forceinline__ uint32_t fp8x2_to_f16x2(uint32_t two) {
+    uint32_t h;
+    const uint16_t b = static_cast<uint16_t>(two);
+    if constexpr (FMT == kFmtE4M3)
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(b));
+    else
+        asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"(b));
+    return h;
+}
+
+__device__ __forceinline__ void f16x2_to_f32(uint32_t h, float& lo, float& hi) {
+    asm("{ .reg .f16 l, u;\n\t"
+        "mov.b32 {l, u}, %2;\n\t"
+        "cvt.f32.f16 %0, l;\n\t"
+        "cvt.f32.f16 %1, u; }"
+        : "=f"(lo), "=f"(hi)
+        : "r"(h));
+}
+
+// Two floats -> bf16x2, round to nearest even (low half = a).
+__device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+
+// Four FP8 codes packed in a word -> four floats, element order preserved.
+template <int FMT>
+__device__ __forceinline__ void decode4(uint32_t w, float* v) {
+    f16x2_to_f32(fp8x2_to_f16x2<FMT>(w & 0xFFFFu), v[0], v[1]);
+    f16x2_to_f32(fp8x2_to_f16x2<FMT>(w >> 16), v[2], v[3]);
+}
+
+// Eight floats -> eight bf16 in a uint4, round to nearest even.
+__device__ __forceinline__ uint4 pack8_bf16(const float* v) {
+    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                      pack_bf16x2(v[6], v[7]));
 }
 
 // ---------------------------------------------------------------------------

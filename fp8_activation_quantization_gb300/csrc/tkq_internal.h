@@ -28,7 +28,7 @@ unsigned int* device_status_word();
 // Access checking of the checked build (-DTKQ_CHECKED; see tkq_device.cuh):
 // the buffers of the current call, inputs and outputs, as address ranges.
 constexpr uint32_t kDeviceOutOfBounds = 2u;  // status-word bit: an access was refused
-constexpr int kCheckMax = 8;
+constexpr int kCheckMax = 16;
 
 struct CheckTable {
     unsigned long long lo[kCheckMax], hi[kCheckMax];  // [lo, hi) per buffer
@@ -158,5 +158,57 @@ cudaError_t launch_per_block_cast(const void* x, void* out, float* sf, int64_t T
 // scales of gr x gc groups (1x128, 128x1 or 128x128).
 cudaError_t launch_cast_back(const void* codes, const float* sf, void* out, int64_t T, int64_t C,
                              int gr, int gc, int fmt, bool out_bf16, cudaStream_t stream);
+
+// Routing to experts (route.cu).  `ld`: row stride of the logits in elements.
+struct RouteShape {
+    int E, k;                      // experts, chosen per token
+    int groups, topk_groups;       // groups of E / groups experts, of which topk_groups are searched
+    int group_top;                 // 1 or 2 largest keys make a group's score
+    bool sigmoid, renorm, bf16;
+    float scale;
+};
+cudaError_t launch_route_topk(const void* logits, const float* bias, int32_t* ids, float* weights,
+                              int32_t* counts, int64_t T, int64_t ld, const RouteShape& shape,
+                              cudaStream_t stream);
+cudaError_t launch_route_topk_backward(const void* logits, const int32_t* ids,
+                                       const float* dweights, void* dlogits, int64_t T, int64_t ld,
+                                       const RouteShape& shape, cudaStream_t stream);
+
+// The SwiGLU cast with an 8-bit checkpoint of its input, and its backward from
+// that checkpoint (swiglu_ckpt.cu).  out_kind: an FP8 format, or 2 for bf16
+// gradients (dx_sf unused); y and dw may be null.
+cudaError_t launch_swiglu_save(const void* x, const float* w, void* out, void* sf, void* ckpt,
+                               float* ckpt_sf, int64_t T, int64_t H, int fmt, int ckpt_fmt,
+                               unsigned sf_flags, cudaStream_t stream);
+cudaError_t launch_swiglu_restore(const void* ckpt, const float* ckpt_sf, const void* dy,
+                                  const float* w, void* dx, void* dx_sf, void* y, float* dw,
+                                  int64_t T, int64_t H, int ckpt_fmt, int out_kind,
+                                  unsigned sf_flags, cudaStream_t stream);
+
+// The norms around a block (residual_norm.cu); optional pointers may be null.
+struct ResidualNorm {
+    const void *r, *h, *gate;       // [T, C]: residual stream, block output, gate logits
+    const float *w_post, *w_pre;    // [C]
+    void *r_out, *out, *sf, *x_out;
+    float *rstd_post, *rstd_pre;    // [T]
+    int64_t T, C;
+    float res_scale, eps;
+    bool post, pre, r_f32;
+};
+cudaError_t launch_residual_norm(const ResidualNorm& a, int fmt, unsigned sf_flags,
+                                 cudaStream_t stream);
+
+struct ResidualNormGrad {
+    const void *dx, *dr, *r, *h, *gate;
+    const float *w_post, *w_pre, *rstd_post, *rstd_pre;
+    void *dr_out, *dh, *dgate;
+    float *dw_post, *dw_pre;
+    void* workspace;                // fp32 [residual_norm_parts, 2, C]
+    int64_t T, C;
+    float res_scale;
+    bool post, r_f32;
+};
+int64_t residual_norm_parts(int64_t T, int64_t C);
+cudaError_t launch_residual_norm_backward(const ResidualNormGrad& a, cudaStream_t stream);
 
 }  // namespace tkq

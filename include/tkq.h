@@ -324,6 +324,152 @@ tkq_status tkq_swiglu_cast_t_clamp(const void* x, const float* w, void* out, voi
                                    uint64_t* clamp_count, tkq_stream_t stream);
 
 /*
+ * Routing of tokens to experts (what gives the routing weight w of the SwiGLU
+ * casts; [P1] §2 names the operators, the formulas are the textbook ones).
+ * For every token t, with x = logits[t, :]:
+ *   score[e] = 1 / (1 + exp(-x[e]))               (TKQ_ROUTE_SIGMOID), or
+ *   score[e] = exp(x[e] - m) / sum_j exp(x[j] - m)  the softmax (default)
+ *   key[e]   = score[e] + bias[e]                 (score[e] without a bias)
+ * With n_groups > 1 the experts are n_groups runs of E / n_groups; a group's
+ * score is the sum of its group_top (1 or 2) largest keys, and only the
+ * topk_groups best groups are searched.  The k largest keys of what is left
+ * are chosen, in falling order; ties, of groups too, go to the lowest index.
+ *   ids[t, i]     the i-th chosen expert
+ *   weights[t, i] = scale * score[ids[t, i]], divided by the sum of the chosen
+ *                   scores with TKQ_ROUTE_RENORM (0 where that sum is 0); the
+ *                   bias moves the choice only
+ *   counts[e]     the number of tokens that chose e is ADDED (the caller
+ *                   zeroes; NULL: not counted)
+ * An expert whose logit is -inf or NaN is absent from that token: no share of
+ * the softmax, never chosen; one whose bias is -inf or NaN is never chosen.
+ * Where fewer than k experts can be chosen, the remaining ids are -1 and their
+ * weights 0.  A logit of +inf counts as the largest finite number.
+ *   logits : [T, E], dtype TKQ_OUT_F32 or TKQ_OUT_BF16, rows ld elements apart
+ *            (E <= ld <= 2^28), aligned to its element
+ *   bias : fp32 [E] or NULL;  ids : int32 [T, k];  weights : fp32 [T, k];
+ *   counts : int32 [E] or NULL
+ * T >= 0; 0 < E <= 1024; 0 < k <= 32, k <= E; 0 < n_groups <= 32,
+ * E % n_groups == 0; 0 < topk_groups <= n_groups; else TKQ_ERR_SHAPE.
+ * TKQ_ERR_VALUE: group_top not 1 or 2, scale not finite.  TKQ_ERR_FMT: dtype.
+ */
+#define TKQ_ROUTE_SIGMOID 1u
+#define TKQ_ROUTE_RENORM 2u
+tkq_status tkq_route_topk(const void* logits, const float* bias, int32_t* ids, float* weights,
+                          int32_t* counts, int64_t T, int64_t E, int64_t ld, int dtype, int k,
+                          int n_groups, int topk_groups, int group_top, unsigned route_flags,
+                          float scale, tkq_stream_t stream);
+
+/*
+ * Gradient of the routing weights with respect to the logits, for the ids a
+ * tkq_route_topk call gave (the choice itself has no gradient).  With
+ * a_i = scale * dweights[t, i], p_i the chosen scores and S their sum,
+ *   ds_i = a_i, or with TKQ_ROUTE_RENORM (a_i - sum_j a_j p_j / S) / S  (0 if S = 0)
+ *   dlogits = ds s (1 - s)  (sigmoid)   or   s (ds - sum_j ds_j s_j)  (softmax)
+ * and 0 for absent experts.  An id outside [0, E) is an empty slot.
+ *   logits : [T, E] as above;  ids : int32 [T, k];  dweights : fp32 [T, k];
+ *   dlogits : [T, E], contiguous, of the logits' type
+ */
+tkq_status tkq_route_topk_backward(const void* logits, const int32_t* ids, const float* dweights,
+                                   void* dlogits, int64_t T, int64_t E, int64_t ld, int dtype,
+                                   int k, unsigned route_flags, float scale, tkq_stream_t stream);
+
+/*
+ * tkq_swiglu_cast_ex that also writes an 8-bit checkpoint of its input from
+ * the same read: ckpt / ckpt_sf are what tkq_per_token_cast gives for x as a
+ * [T, 2H] matrix in ckpt_fmt, bit for bit; out / sf are those of
+ * tkq_swiglu_cast_ex, bit for bit.
+ *   ckpt : FP8 codes [T, 2H];  ckpt_sf : fp32 [T, 2H/128]
+ */
+tkq_status tkq_swiglu_cast_checkpoint(const void* x, const float* w, void* out, void* sf,
+                                      void* ckpt, float* ckpt_sf, int64_t T, int64_t H, int group,
+                                      int fmt, int ckpt_fmt, unsigned sf_flags,
+                                      tkq_stream_t stream);
+
+/*
+ * Backward of y = silu(g) * u [* w] from that checkpoint: with g and u the
+ * values fl32(code * scale) and the formulas of tkq_swiglu_backward_cast,
+ *   dx    [dg | du], bf16 [T, 2H] (rounded to nearest even), or for the _cast
+ *         form its per-token cast in fmt (codes [T, 2H], dx_sf as sf_flags say;
+ *         codes of the product by the reciprocal scale)
+ *   y     bf16 [T, H], the forward's y again, or NULL
+ *   dw    fp32 [T], the gradient of the routing weight, sum_c dy silu(g) u
+ *         (summed in fp32 in a fixed order), or NULL
+ *   dy    bf16 [T, H];  w : fp32 [T] or NULL
+ * T >= 0; H > 0, H % 128 == 0.  Alignment: ckpt, dy, dx, y 16 bytes, else 4.
+ */
+tkq_status tkq_swiglu_checkpoint_backward(const void* ckpt, const float* ckpt_sf, const void* dy,
+                                          const float* w, void* dx, void* y, float* dw, int64_t T,
+                                          int64_t H, int group, int ckpt_fmt, tkq_stream_t stream);
+tkq_status tkq_swiglu_checkpoint_backward_cast(const void* ckpt, const float* ckpt_sf,
+                                               const void* dy, const float* w, void* dx,
+                                               void* dx_sf, void* y, float* dw, int64_t T,
+                                               int64_t H, int group, int ckpt_fmt, int fmt,
+                                               unsigned sf_flags, tkq_stream_t stream);
+
+/*
+ * The norms before and after a block, with its gate and residual scale, in one
+ * pass ending in the per-token cast of the next product's input.  For every
+ * row, with h the block's output and r the residual stream:
+ *   p  = 1 / sqrt(mean(h^2) + eps)                     (TKQ_NORM_POST)
+ *   r' = r + res_scale * h [* p] [* w_post] [* sigmoid(gate)]
+ *   q  = 1 / sqrt(mean(r'^2) + eps)                    (TKQ_NORM_PRE)
+ *   x  = r' * q [* w_pre]
+ * in binary32; r' is rounded to the stream's type where it is stored, x is
+ * taken of the value before that rounding.
+ *   r, r_out : [T, C], bf16, or fp32 with TKQ_NORM_RES_F32
+ *   h        : bf16 [T, C], or NULL: no block, r' = r (r_out, w_post, gate and
+ *              TKQ_NORM_POST are then not given either)
+ *   w_post, w_pre : fp32 [C] or NULL (ones)
+ *   gate     : bf16 [T, C] or NULL
+ *   out, sf  : the per-token cast of x (exact quotient; sf as sf_flags say), or
+ *              both NULL
+ *   x_out    : bf16 [T, C], x rounded to nearest even, or NULL
+ *   rstd_post, rstd_pre : fp32 [T], p and q for the backward, or NULL
+ * With TKQ_NORM_PRE at least one of out and x_out is given, without it none.
+ * T >= 0; 0 < C <= 16384, C % 128 == 0.  Alignment: 16 bytes for matrices and
+ * [C] weights, 4 for the rest.  eps: finite, >= 0; res_scale: finite, else
+ * TKQ_ERR_VALUE.  Options that contradict each other: TKQ_ERR_FLAGS.
+ */
+#define TKQ_NORM_POST 1u
+#define TKQ_NORM_PRE 2u
+#define TKQ_NORM_RES_F32 4u
+tkq_status tkq_residual_norm_cast(const void* r, const void* h, const float* w_post,
+                                  const void* gate, const float* w_pre, void* r_out, void* out,
+                                  void* sf, void* x_out, float* rstd_post, float* rstd_pre,
+                                  int64_t T, int64_t C, int group, int fmt, unsigned sf_flags,
+                                  unsigned norm_flags, float res_scale, float eps,
+                                  tkq_stream_t stream);
+
+/*
+ * Gradients of tkq_residual_norm_cast.  With m = h [* p], n = r' * q and
+ * s = sigmoid(gate) (1 without a gate), given dr = dL/dr' and dx = dL/dx:
+ *   dr_out  = dr + q * (dx * w_pre - n * mean(dx * w_pre * n))
+ *   e       = res_scale * dr_out
+ *   dgate   = e * m * w_post * s * (1 - s)
+ *   dh      = p * (e * s * w_post - m * mean(e * s * w_post * m)) with
+ *             TKQ_NORM_POST, else e * s * w_post
+ *   dw_pre  = sum_t dx * n          dw_post = sum_t e * s * m
+ * The cast is passed through: dx is the gradient of the x that was cast.
+ *   dr      : [T, C] of the stream's type, or NULL (zero);  dx : bf16 [T, C],
+ *             given with TKQ_NORM_PRE;  r : the forward's r_out (its r without
+ *             h), needed with TKQ_NORM_PRE
+ *   h, gate, w_post, w_pre, rstd_post, rstd_pre : as in the forward
+ *   dr_out  : [T, C] of the stream's type;  dh, dgate : bf16 [T, C], given
+ *             exactly with h and gate;  dw_post, dw_pre : fp32 [C] or NULL
+ *   workspace : tkq_residual_norm_workspace(T, C) bytes, 16-byte aligned
+ *             (NULL when no weight gradient is asked for)
+ * Sums over rows are taken in a fixed order: results repeat bit for bit on one
+ * kind of GPU.  T == 0 launches nothing (the weight gradients are not written).
+ */
+int64_t tkq_residual_norm_workspace(int64_t T, int64_t C);
+tkq_status tkq_residual_norm_backward(const void* dr, const void* dx, const void* r, const void* h,
+                                      const float* w_post, const void* gate, const float* w_pre,
+                                      const float* rstd_post, const float* rstd_pre, void* dr_out,
+                                      void* dh, void* dgate, float* dw_post, float* dw_pre,
+                                      void* workspace, int64_t T, int64_t C, unsigned norm_flags,
+                                      float res_scale, tkq_stream_t stream);
+
+/*
  * Diagnostic (not an operation of the source pages): the fp32 SwiGLU values
  *   y[t, c] = silu(x[t, c]) * x[t, H + c] [* w[t]]
  * computed exactly as tkq_swiglu_cast and tkq_swiglu_cast_t compute them
