@@ -14,15 +14,17 @@
 //   dgate  = e m w_post s (1 - s)                         dw_post = sum_t e s m
 //   dh     = p (e s w_post - m mean(e s w_post m)),  or e s w_post without p
 //
-// One CTA per row, the row in registers between its reads and its writes, so
-// each tensor is read and written once; both are bound by memory (bf16
-// stream, with gate: 9 bytes a channel forward, 16 backward).  The stream r' is
-// rounded to its type where it is stored; the norm that follows is taken of
-// the binary32 value before that rounding.
+// One CTA per row, each thread with the same channels of every row: each tensor
+// is read and written once.  A thread keeps its next rows in flight as
+// 16-byte asynchronous copies into its own slots of shared memory (`Fifo`), so
+// loads go on across the reductions' barriers and no other thread waits for
+// them.  The stream r' is rounded to its type where it is stored; the norm that
+// follows is taken of the binary32 value before that rounding.
 #include <type_traits>
 
 #include <cuda_runtime.h>
 
+#include "tkq_async.cuh"
 #include "tkq_device.cuh"
 #include "tkq_internal.h"
 
@@ -31,7 +33,6 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kMaxThreads = 512;
-constexpr int kNoCast = 2;  // in the place of an FP8 format: no codes wanted
 
 // Sums of N values over the CTA, in the same order each time.  Two buffers in
 // turn: a thread past the barrier of one sum has read the sum before.
@@ -57,128 +58,241 @@ __device__ __forceinline__ void cta_sum(float (&v)[N], float (*buf)[N][32], int&
     turn ^= 1;
 }
 
-// Eight channels of a stream in bf16 or binary32.
-template <bool F32>
-struct Chunk {
-    uint4 q[F32 ? 2 : 1];
+// ---------------------------------------------------------------------------
+// a thread's rows in flight
+// ---------------------------------------------------------------------------
+// Shared memory holds `depth` rows; of each row a thread copies, and later
+// reads, only its own 16-byte pieces, so its wait for its own copies is all
+// the ordering there is.  Piece `slot` of vector `vec` of a stage:
+// (stage * slots + slot) * vecs + vec.
+__device__ __forceinline__ void cp_async16(uint4* dst, const void* src) {
+    if (!access_ok(src, 16, false)) return;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// All but the newest depth - 1 groups have arrived.
+__device__ __forceinline__ void cp_async_wait(int depth) {
+    switch (depth) {
+        case 1: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+        case 2: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+        case 3: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+        default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    }
+}
+constexpr int kMaxDepth = 4;
 
-    __device__ __forceinline__ void load(const void* base, int64_t vec) {
-        const uint4* p = static_cast<const uint4*>(base) + vec * (F32 ? 2 : 1);
-#pragma unroll
-        for (int i = 0; i < (F32 ? 2 : 1); ++i) q[i] = ld_stream(p + i);
-    }
-    __device__ __forceinline__ void values(float* v) const {
-        if constexpr (F32) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                v[4 * i] = __uint_as_float(q[i].x);
-                v[4 * i + 1] = __uint_as_float(q[i].y);
-                v[4 * i + 2] = __uint_as_float(q[i].z);
-                v[4 * i + 3] = __uint_as_float(q[i].w);
-            }
-        } else {
-            unpack8(q[0], v);
-        }
-    }
-    static __device__ __forceinline__ void store(void* base, int64_t vec, const float* v) {
-        uint4* p = static_cast<uint4*>(base) + vec * (F32 ? 2 : 1);
-        if constexpr (F32) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                st_stream(p + i,
-                          make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
-                                     __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])));
-        } else {
-            st_stream(p, pack8_bf16(v));
-        }
-    }
+struct Fifo {
+    int depth, slots;  // rows, 16-byte pieces of a vector of one row
 };
 
-// Eight weights of a row vector, ones when there is none.
-__device__ __forceinline__ void weights8(const float* w, int64_t vec, float* v) {
+// Copies vector `vec` of a row into consecutive slots from `slot` on.
+template <bool F32>
+__device__ __forceinline__ void fetch(uint4* stage, int slot, int vecs, int vec, const void* base,
+                                      int64_t row) {
+    const uint4* p = static_cast<const uint4*>(base) + (row * vecs + vec) * (F32 ? 2 : 1);
+    cp_async16(stage + slot * vecs + vec, p);
+    if constexpr (F32) cp_async16(stage + (slot + 1) * vecs + vec, p + 1);
+}
+// Its eight values.
+template <bool F32>
+__device__ __forceinline__ void values8(const uint4* stage, int slot, int vecs, int vec, float* v) {
+    const uint4 a = stage[slot * vecs + vec];
+    if constexpr (F32) {
+        const uint4 b = stage[(slot + 1) * vecs + vec];
+        v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y);
+        v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
+        v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y);
+        v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
+    } else {
+        unpack8(a, v);
+    }
+}
+template <bool F32>
+__device__ __forceinline__ void store8(void* base, int64_t vec, const float* v) {
+    uint4* p = static_cast<uint4*>(base) + vec * (F32 ? 2 : 1);
+    if constexpr (F32) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            st_stream(p + i,
+                      make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                                 __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])));
+    } else {
+        st_stream(p, pack8_bf16(v));
+    }
+}
+
+// Eight weights of a row vector times `scale`, ones in the place of an absent vector.
+__device__ __forceinline__ void weights8(const float* w, int vec, float scale, float* v) {
     float4 a = make_float4(1.f, 1.f, 1.f, 1.f), b = a;
     if (w) {
         a = ld_ro(reinterpret_cast<const float4*>(w) + vec * 2);
         b = ld_ro(reinterpret_cast<const float4*>(w) + vec * 2 + 1);
     }
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    v[0] = a.x * scale; v[1] = a.y * scale; v[2] = a.z * scale; v[3] = a.w * scale;
+    v[4] = b.x * scale; v[5] = b.y * scale; v[6] = b.z * scale; v[7] = b.w * scale;
 }
 
-__device__ __forceinline__ float sigmoid(float x) {
-    return rcp_approx(1.0f + ex2_approx(x * -1.4426950408889634f));
+// A thread's weights: kept in registers for all its rows where they fit (up to
+// two vectors a thread), else read again for each row.
+template <int NV>
+struct Weights {
+    static constexpr bool kKept = NV <= 2;
+    float kept[kKept ? NV : 1][8];
+    const float* w;
+    float scale;
+
+    __device__ __forceinline__ void init(const float* weights, float s, int vecs) {
+        w = weights;
+        scale = s;
+        if constexpr (kKept) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int vec = threadIdx.x + i * blockDim.x;
+                if (vec < vecs) weights8(w, vec, scale, kept[i]);
+            }
+        }
+    }
+    __device__ __forceinline__ void get(int i, int vec, float* v) const {
+        if constexpr (kKept) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = kept[i][e];
+        } else {
+            weights8(w, vec, scale, v);
+        }
+    }
+};
+
+// sigmoid(x) and 1 - sigmoid(x) = exp(-x) sigmoid(x), for two values.  Where
+// exp(-x) overflows the first is 0 and the product NaN, which fminf makes 1.
+__device__ __forceinline__ float2 sigmoid2(float2 x, float2& rest) {
+    const float2 t = mul2(x, make_float2(-1.4426950408889634f, -1.4426950408889634f));
+    const float2 e = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+    const float2 den = add2(make_float2(1.0f, 1.0f), e);
+    const float2 s = make_float2(rcp_approx(den.x), rcp_approx(den.y));
+    const float2 r = mul2(e, s);
+    rest = make_float2(fminf(r.x, 1.0f), fminf(r.y, 1.0f));
+    return s;
+}
+__device__ __forceinline__ float2 two(float a) { return make_float2(a, a); }
+__device__ __forceinline__ float2 at2(const float* v, int e) { return make_float2(v[e], v[e + 1]); }
+__device__ __forceinline__ void put2(float* v, int e, float2 a) {
+    v[e] = a.x;
+    v[e + 1] = a.y;
 }
 
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
-template <int NV, bool F32, int FMT>
+// Codes of a vector's eight values; a group is half a warp's vectors.
+template <int FMT>
+__device__ __forceinline__ void cast8(const ResidualNorm& a, const SfLayout& lay, int64_t t,
+                                      int vecs, int vec, const float* v) {
+    float m = absmax8(v);
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+    float sc, inv;
+    group_scale<FMT>(m, sc, inv);
+    if (lay.flags & (kSfRoundPow2 | kSfPacked)) pow2_scale(sc, inv);
+    if (vec < vecs) {
+        st_stream(static_cast<uint2*>(a.out) + t * vecs + vec, quantize8<FMT>(v, sc, inv));
+        if ((threadIdx.x & 15) == 0) store_scale(a.sf, lay, t, true, vec / 16, sc);
+    }
+}
+
+template <int NV, bool F32, bool POST, bool GATE>
 __global__ void __launch_bounds__(kMaxThreads)
-    residual_norm_kernel(const ResidualNorm a, const SfLayout lay, int64_t rows_walk) {
+    residual_norm_kernel(const ResidualNorm a, const SfLayout lay, int64_t rows_walk, int fmt,
+                         Fifo q8) {
+    extern __shared__ uint4 fifo[];
     __shared__ float buf[2][1][32];
     grid_dependency_launch();
+    constexpr int kR = F32 ? 2 : 1;   // slots of r; then h, gate
     int turn = 0;
     const int tid = threadIdx.x, vecs = static_cast<int>(a.C / 8);
     const float inv_c = 1.0f / static_cast<float>(a.C);
+    const int stage_size = q8.slots * vecs;
+    const auto fetch_row = [&](int64_t t, int stage) {
+        if (t < a.T)
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int vec = tid + i * blockDim.x;
+                if (vec >= vecs) continue;
+                uint4* s = fifo + stage * stage_size;
+                if (a.h) fetch<false>(s, kR, vecs, vec, a.h, t);
+                fetch<F32>(s, 0, vecs, vec, a.r, t);
+                if constexpr (GATE) fetch<false>(s, kR + 1, vecs, vec, a.gate, t);
+            }
+        cp_async_commit();
+    };
     grid_dependency_wait();
+    for (int d = 0; d < q8.depth - 1; ++d)
+        fetch_row(blockIdx.x + static_cast<int64_t>(d) * gridDim.x, d);
+    Weights<NV> w_post, w_pre;
+    w_post.init(a.w_post, a.res_scale, vecs);
+    w_pre.init(a.w_pre, 1.0f, vecs);
+    int stage = 0, ahead = q8.depth - 1;
     for (int64_t t = blockIdx.x; t < rows_walk; t += gridDim.x) {
+        fetch_row(t + static_cast<int64_t>(q8.depth - 1) * gridDim.x, ahead);
         if (t >= a.T) {  // the padding rows of the column-major scale layouts
             for (int j = tid; j < lay.groups; j += blockDim.x)
                 store_scale(a.sf, lay, t, false, j, 0.0f);
             continue;
         }
-        float v[NV][8];
+        const uint4* s = fifo + stage * stage_size;
+        cp_async_wait(q8.depth);
+        stage = stage + 1 == q8.depth ? 0 : stage + 1;
+        ahead = ahead + 1 == q8.depth ? 0 : ahead + 1;
         float sum[1] = {0.0f};
+        float p = 1.0f;
+        if constexpr (POST) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int vec = tid + i * blockDim.x;
+                if (vec >= vecs) continue;
+                float h[8];
+                values8<false>(s, kR, vecs, vec, h);
+                float2 c = two(0.0f);
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) c = fma2(at2(h, e), at2(h, e), c);
+                sum[0] += c.x + c.y;
+            }
+            cta_sum<1>(sum, buf, turn);
+            p = __frsqrt_rn(sum[0] * inv_c + a.eps);
+            if (tid == 0 && a.rstd_post) st_plain(a.rstd_post + t, p);
+            sum[0] = 0.0f;
+        }
+        float v[NV][8];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int vec = tid + i * blockDim.x;
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
-            if (vec < vecs && a.h) {
-                Chunk<false> c;
-                c.load(a.h, t * vecs + vec);
-                c.values(v[i]);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) sum[0] += v[i][e] * v[i][e];
-            }
-        }
-        float p = 1.0f;
-        if (a.post) {
-            cta_sum<1>(sum, buf, turn);
-            p = __frsqrt_rn(sum[0] * inv_c + a.eps);
-            if (tid == 0 && a.rstd_post) st_plain(a.rstd_post + t, p);
-        }
-        sum[0] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int vec = tid + i * blockDim.x;
             if (vec >= vecs) continue;
-            Chunk<F32> c;
-            c.load(a.r, t * vecs + vec);
-            float r[8];
-            c.values(r);
+            values8<F32>(s, 0, vecs, vec, v[i]);
             if (a.h) {
-                float w[8];
-                weights8(a.w_post, vec, w);
+                float h[8], w[8], g[8];
+                values8<false>(s, kR, vecs, vec, h);
+                if constexpr (GATE) values8<false>(s, kR + 1, vecs, vec, g);
+                w_post.get(i, vec, w);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] *= p * v[i][e];
-                if (a.gate) {
-                    Chunk<false> g;
-                    g.load(a.gate, t * vecs + vec);
-                    float s[8];
-                    g.values(s);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) w[e] *= sigmoid(s[e]);
+                for (int e = 0; e < 8; e += 2) {
+                    float2 b = mul2(at2(w, e), at2(h, e));
+                    if constexpr (POST) b = mul2(b, two(p));
+                    if constexpr (GATE) {
+                        float2 rest;
+                        b = mul2(b, sigmoid2(at2(g, e), rest));
+                    }
+                    put2(v[i], e, add2(b, at2(v[i], e)));
                 }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) r[e] = fmaf(a.res_scale, w[e], r[e]);
-                Chunk<F32>::store(a.r_out, t * vecs + vec, r);
+                store8<F32>(a.r_out, t * vecs + vec, v[i]);
             }
+            float2 c = two(0.0f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                v[i][e] = r[e];
-                sum[0] += r[e] * r[e];
-            }
+            for (int e = 0; e < 8; e += 2) c = fma2(at2(v[i], e), at2(v[i], e), c);
+            sum[0] += c.x + c.y;
         }
         if (!a.pre) continue;
         cta_sum<1>(sum, buf, turn);
@@ -187,27 +301,18 @@ __global__ void __launch_bounds__(kMaxThreads)
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int vec = tid + i * blockDim.x;
-            const bool live = vec < vecs;
-            float w[8];
-            if (live) weights8(a.w_pre, vec, w);
+            float w[8] = {};
+            if (vec < vecs) w_pre.get(i, vec, w);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[i][e] = live ? v[i][e] * q * w[e] : 0.0f;
-            if (live && a.x_out)
+            for (int e = 0; e < 8; e += 2)
+                put2(v[i], e, mul2(mul2(at2(v[i], e), two(q)), at2(w, e)));
+            if (a.x_out && vec < vecs)
                 st_stream(static_cast<uint4*>(a.x_out) + t * vecs + vec, pack8_bf16(v[i]));
-            if constexpr (FMT != kNoCast) {
-                // a group is half a warp's vectors
-                float m = absmax8(v[i]);
-#pragma unroll
-                for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
-                float sc, inv;
-                group_scale<FMT>(m, sc, inv);
-                if (lay.flags & (kSfRoundPow2 | kSfPacked)) pow2_scale(sc, inv);
-                if (live) {
-                    st_stream(static_cast<uint2*>(a.out) + t * vecs + vec,
-                              quantize8<FMT>(v[i], sc, inv));
-                    if ((tid & 15) == 0) store_scale(a.sf, lay, t, true, vec / 16, sc);
-                }
-            }
+            if (!a.out) continue;
+            if (fmt == kFmtE4M3)
+                cast8<kFmtE4M3>(a, lay, t, vecs, vec, v[i]);
+            else
+                cast8<kFmtE5M2>(a, lay, t, vecs, vec, v[i]);
         }
     }
 }
@@ -215,101 +320,155 @@ __global__ void __launch_bounds__(kMaxThreads)
 // ---------------------------------------------------------------------------
 // backward
 // ---------------------------------------------------------------------------
-// One reduction a row: with f = w_post s, the sum that dh needs,
-// sum e f m, is linear in the first mean and so follows from
-//   S1 = sum dx w_pre n,  S2 = sum f m (dr' + q dx w_pre),  S3 = sum f m n:
-//   sum f m dr = S2 - q (S1 / C) S3.
-// The weight gradients are summed over a CTA's rows in registers and written
-// as one partial row a CTA; sum_parts_kernel adds them up in order.
-template <int NV, bool F32>
+// One reduction a row.  With G = dr' + q dx w_pre, so that dr = G - q^2 m1 r'
+// for the first mean m1 = S1 / C, and f = a w_post s, the sum that dh needs is
+// linear in m1 and follows from sums over what the row brings along:
+//   S1 = q sum dx w_pre r',  S2 = p sum f h G,  S3 = p sum f h r':
+//   sum e w_post s m = S2 - q^2 m1 S3.
+// G and r' stay in registers between the two passes (up to two vectors a
+// thread), h and the gate are read from shared memory again.  The weight
+// gradients are summed over a CTA's rows in registers and written as one
+// partial row a CTA; sum_parts_kernel adds them up in order.
+template <int NV, bool F32, bool POST, bool GATE>
 __global__ void __launch_bounds__(kMaxThreads)
-    residual_norm_backward_kernel(const ResidualNormGrad a) {
-    __shared__ float buf[2][3][32];
+    residual_norm_backward_kernel(const ResidualNormGrad a, Fifo q8) {
+    extern __shared__ uint4 fifo[];
+    __shared__ float buf[2][POST ? 3 : 1][32];
     grid_dependency_launch();
+    constexpr int kS = F32 ? 2 : 1;   // slots of a stream: h, gate, dr, dx, r
+    constexpr bool kKept = Weights<NV>::kKept;
+    constexpr int kH = 0, kGate = 1;
+    const int at_dr = (a.h ? 1 : 0) + (GATE ? 1 : 0), at_dx = at_dr + (a.dr ? kS : 0);
     int turn = 0;
     const int tid = threadIdx.x, vecs = static_cast<int>(a.C / 8);
     const float inv_c = 1.0f / static_cast<float>(a.C);
+    const int stage_size = q8.slots * vecs;
+    const auto fetch_row = [&](int64_t t, int stage) {
+        if (t < a.T)
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int vec = tid + i * blockDim.x;
+                if (vec >= vecs) continue;
+                uint4* s = fifo + stage * stage_size;
+                if (a.dr) fetch<F32>(s, at_dr, vecs, vec, a.dr, t);
+                if (a.dx) {
+                    fetch<false>(s, at_dx, vecs, vec, a.dx, t);
+                    fetch<F32>(s, at_dx + 1, vecs, vec, a.r, t);
+                }
+                if (a.h) fetch<false>(s, kH, vecs, vec, a.h, t);
+                if constexpr (GATE) fetch<false>(s, kGate, vecs, vec, a.gate, t);
+            }
+        cp_async_commit();
+    };
+    // dr', dx and r' of one vector, zeros for what is absent
+    const auto stream = [&](const uint4* s, int vec, float* g, float* d, float* r) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] = d[e] = r[e] = 0.0f;
+        if (a.dr) values8<F32>(s, at_dr, vecs, vec, g);
+        if (a.dx) {
+            values8<false>(s, at_dx, vecs, vec, d);
+            values8<F32>(s, at_dx + 1, vecs, vec, r);
+        }
+    };
     float acc_pre[NV][8] = {}, acc_post[NV][8] = {};
     grid_dependency_wait();
+    for (int d = 0; d < q8.depth - 1; ++d)
+        fetch_row(blockIdx.x + static_cast<int64_t>(d) * gridDim.x, d);
+    Weights<NV> w_post, w_pre;
+    w_post.init(a.w_post, a.res_scale, vecs);
+    w_pre.init(a.w_pre, 1.0f, vecs);
+    int stage = 0, ahead = q8.depth - 1;
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-        const float p = a.post ? ld_ro(a.rstd_post + t) : 1.0f;
+        fetch_row(t + static_cast<int64_t>(q8.depth - 1) * gridDim.x, ahead);
+        const float p = POST ? ld_ro(a.rstd_post + t) : 1.0f;
         const float q = a.dx ? ld_ro(a.rstd_pre + t) : 0.0f;
-        Chunk<false> dx[NV], h[NV], gate[NV];
-        Chunk<F32> dr[NV], r[NV];
-        float sum[3] = {0.0f, 0.0f, 0.0f};
+        const uint4* s = fifo + stage * stage_size;
+        cp_async_wait(q8.depth);
+        stage = stage + 1 == q8.depth ? 0 : stage + 1;
+        ahead = ahead + 1 == q8.depth ? 0 : ahead + 1;
+        float g[kKept ? NV : 1][8], r[kKept ? NV : 1][8];
+        float sum[POST ? 3 : 1] = {};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int vec = tid + i * blockDim.x;
-            dx[i] = {};
-            h[i] = {};
-            gate[i] = {};
-            dr[i] = {};
-            r[i] = {};
             if (vec >= vecs) continue;
-            const int64_t at = t * vecs + vec;
+            float* gi = g[kKept ? i : 0];
+            float* ri = r[kKept ? i : 0];
+            float d[8], w[8];
+            stream(s, vec, gi, d, ri);
+            float2 s1 = two(0.0f);
             if (a.dx) {
-                dx[i].load(a.dx, at);
-                r[i].load(a.r, at);
-            }
-            if (a.dr) dr[i].load(a.dr, at);
-            if (a.h) h[i].load(a.h, at);
-            if (a.gate) gate[i].load(a.gate, at);
-        }
+                w_pre.get(i, vec, w);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int vec = tid + i * blockDim.x;
-            if (vec >= vecs) continue;
-            float d[8], n[8], g[8], m[8], s[8], wq[8], wp[8];
-            dx[i].values(d);
-            r[i].values(n);
-            dr[i].values(g);
-            h[i].values(m);
-            gate[i].values(s);
-            weights8(a.w_pre, vec, wq);
-            weights8(a.w_post, vec, wp);
+                for (int e = 0; e < 8; e += 2) {
+                    const float2 dq = mul2(at2(d, e), two(q));
+                    put2(acc_pre[i], e, fma2(dq, at2(ri, e), at2(acc_pre[i], e)));
+                    const float2 dw = mul2(dq, at2(w, e));
+                    s1 = fma2(dw, at2(ri, e), s1);
+                    put2(gi, e, add2(dw, at2(gi, e)));
+                }
+            }
+            sum[0] += s1.x + s1.y;
+            if constexpr (POST) {
+                float2 s2 = two(0.0f), s3 = s2;
+                float h[8], gt[8];
+                values8<false>(s, kH, vecs, vec, h);
+                if constexpr (GATE) values8<false>(s, kGate, vecs, vec, gt);
+                w_post.get(i, vec, w);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float nn = n[e] * q;
-                acc_pre[i][e] += d[e] * nn;
-                const float dw = d[e] * wq[e];
-                sum[0] += dw * nn;
-                const float f = wp[e] * (a.gate ? sigmoid(s[e]) : 1.0f) * m[e] * p;
-                sum[1] += f * (g[e] + q * dw);
-                sum[2] += f * nn;
+                for (int e = 0; e < 8; e += 2) {
+                    float2 f = mul2(at2(w, e), at2(h, e));
+                    float2 rest;
+                    if constexpr (GATE) f = mul2(f, sigmoid2(at2(gt, e), rest));
+                    s2 = fma2(f, at2(gi, e), s2);
+                    s3 = fma2(f, at2(ri, e), s3);
+                }
+                sum[1] += s2.x + s2.y;
+                sum[2] += s3.x + s3.y;
             }
         }
-        if (a.dx || a.post) cta_sum<3>(sum, buf, turn);
-        const float m1 = sum[0] * inv_c;
-        const float m2 = a.post ? (sum[1] - q * m1 * sum[2]) * inv_c : 0.0f;
+        if (POST || a.dx) cta_sum<POST ? 3 : 1>(sum, buf, turn);
+        const float c1 = -q * q * inv_c * sum[0];              // dr = G + c1 r'
+        float c2 = 0.0f;                                       // dh = p (..) + c2 h
+        if constexpr (POST) c2 = -p * p * p * inv_c * (sum[1] + c1 * sum[2]);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int vec = tid + i * blockDim.x;
             if (vec >= vecs) continue;
             const int64_t at = t * vecs + vec;
-            float d[8], n[8], g[8], m[8], s[8], w[8];
-            dx[i].values(d);
-            r[i].values(n);
-            dr[i].values(g);
-            weights8(a.w_pre, vec, w);
+            float* gi = g[kKept ? i : 0];
+            float* ri = r[kKept ? i : 0];
+            float w[8];
+            if constexpr (!kKept) {
+                float d[8];
+                stream(s, vec, gi, d, ri);
+                w_pre.get(i, vec, w);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) g[e] += q * (d[e] * w[e] - n[e] * q * m1);
-            Chunk<F32>::store(a.dr_out, at, g);
-            if (!a.h) continue;
-            h[i].values(m);
-            gate[i].values(s);
-            weights8(a.w_post, vec, w);
-            float dg[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float mm = m[e] * p, err = a.res_scale * g[e];
-                const float sg = a.gate ? sigmoid(s[e]) : 1.0f;
-                // 1 - sigmoid(x) = sigmoid(-x), without cancellation
-                if (a.gate) dg[e] = err * mm * w[e] * sg * sigmoid(-s[e]);
-                acc_post[i][e] += err * sg * mm;
-                m[e] = p * (err * sg * w[e] - mm * (a.res_scale * m2));
+                for (int e = 0; e < 8; e += 2)
+                    put2(gi, e, fma2(mul2(at2(d, e), two(q)), at2(w, e), at2(gi, e)));
             }
-            Chunk<false>::store(a.dh, at, m);
-            if (a.gate) Chunk<false>::store(a.dgate, at, dg);
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) put2(gi, e, fma2(at2(ri, e), two(c1), at2(gi, e)));
+            store8<F32>(a.dr_out, at, gi);
+            if (!a.h) continue;
+            float h[8], gt[8], dh[8], dgate[8];
+            values8<false>(s, kH, vecs, vec, h);
+            if constexpr (GATE) values8<false>(s, kGate, vecs, vec, gt);
+            w_post.get(i, vec, w);
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                float2 x = at2(gi, e), rest;
+                float2 m = at2(h, e);
+                if constexpr (POST) m = mul2(m, two(p));
+                if constexpr (GATE) x = mul2(x, sigmoid2(at2(gt, e), rest));
+                // acc_post leaves out the residual scale, which w holds
+                put2(acc_post[i], e, fma2(x, m, at2(acc_post[i], e)));
+                const float2 xw = mul2(x, at2(w, e));
+                if constexpr (GATE) put2(dgate, e, mul2(mul2(xw, rest), m));
+                put2(dh, e, POST ? fma2(xw, two(p), mul2(at2(h, e), two(c2))) : xw);
+            }
+            store8<false>(a.dh, at, dh);
+            if constexpr (GATE) store8<false>(a.dgate, at, dgate);
         }
     }
     // partial rows [gridDim.x, 2, C]: dw_pre, dw_post
@@ -326,6 +485,8 @@ __global__ void __launch_bounds__(kMaxThreads)
         }
         if (a.dw_post) {
             part += 2 * vecs;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc_post[i][e] *= a.res_scale;
             st_plain(part,
                      make_float4(acc_post[i][0], acc_post[i][1], acc_post[i][2], acc_post[i][3]));
             st_plain(part + 1,
@@ -334,58 +495,88 @@ __global__ void __launch_bounds__(kMaxThreads)
     }
 }
 
-// dw[c] = the sum of `parts` partial rows, in slices of eight interleaved
-// rows that are then added in order.  Block: 32 float4 columns x 8 slices.
-__global__ void __launch_bounds__(256)
+// dw[c] = the sum of `parts` partial rows, in 32 interleaved slices that are
+// then added pairwise, always in the same order.  Block: 16 float4 columns x 32 slices.
+constexpr int kSumCols = 16, kSumSlices = 32;
+__global__ void __launch_bounds__(kSumCols* kSumSlices)
     sum_parts_kernel(const float* __restrict__ workspace, float* __restrict__ dw_pre,
                      float* __restrict__ dw_post, int64_t C, int parts) {
-    __shared__ float4 slice[8][32];
+    __shared__ float4 slice[kSumSlices][kSumCols];
     grid_dependency_launch();
-    const int col = threadIdx.x & 31, part = threadIdx.x >> 5;
-    const int64_t c4 = static_cast<int64_t>(blockIdx.x) * 32 + col;  // < 2 C / 4
+    const int col = threadIdx.x % kSumCols, part = threadIdx.x / kSumCols;
+    const int64_t c4 = static_cast<int64_t>(blockIdx.x) * kSumCols + col;  // < 2 C / 4
     const bool post = c4 >= C / 4;
     float* out = post ? dw_post : dw_pre;
     grid_dependency_wait();
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (out)
-        for (int i = part; i < parts; i += 8) {
+    if (out) {
+#pragma unroll 8
+        for (int i = part; i < parts; i += kSumSlices) {
             const float4 v = ld_ro(reinterpret_cast<const float4*>(workspace) + i * (C / 2) + c4);
             s.x += v.x;
             s.y += v.y;
             s.z += v.z;
             s.w += v.w;
         }
-    slice[part][col] = s;
-    __syncthreads();
-    if (part || !out) return;
-    for (int i = 1; i < 8; ++i) {
-        s.x += slice[i][col].x;
-        s.y += slice[i][col].y;
-        s.z += slice[i][col].z;
-        s.w += slice[i][col].w;
     }
-    st_plain(reinterpret_cast<float4*>(out) + (c4 - (post ? C / 4 : 0)), s);
+    slice[part][col] = s;
+#pragma unroll
+    for (int n = kSumSlices / 2; n > 0; n /= 2) {
+        __syncthreads();
+        if (part >= n) continue;
+        const float4 v = slice[part + n][col];
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
+        slice[part][col] = s;
+    }
+    if (part == 0 && out)
+        st_plain(reinterpret_cast<float4*>(out) + (c4 - (post ? C / 4 : 0)), s);
 }
 
-// Vectors a thread holds and threads a CTA for rows of C channels.
+// Vectors a thread holds, threads a CTA and rows in flight for rows of C
+// channels of `slots` 16-byte pieces a vector: CTAs of at most 512 threads (128
+// registers), about 768 threads an SM, which share 224 KB of shared memory for
+// up to four rows each.
 struct Shape {
     int nv, threads;
+    size_t smem;
+    Fifo fifo;
 };
-Shape shape_of(int64_t C) {
+constexpr size_t kSmemPerSm = 224 * 1024;
+constexpr int kThreadsPerSm = 768;
+Shape shape_of(int64_t C, int slots) {
+    Shape s;
     const int vecs = static_cast<int>(C / 8);
-    const int nv = vecs <= kMaxThreads ? 1 : vecs <= 2 * kMaxThreads ? 2 : 4;
-    return {nv, ((vecs + nv - 1) / nv + 31) / 32 * 32};
+    s.nv = vecs <= kMaxThreads ? 1 : vecs <= 2 * kMaxThreads ? 2 : 4;
+    s.threads = ((vecs + s.nv - 1) / s.nv + 31) / 32 * 32;
+    const size_t row = static_cast<size_t>(slots) * vecs * 16;
+    const size_t ctas = kThreadsPerSm / s.threads < 16 ? kThreadsPerSm / s.threads : 16;
+    size_t depth = kSmemPerSm / (row * ctas);
+    if (depth < 2) depth = kSmemPerSm / row >= 2 ? 2 : 1;
+    if (depth > kMaxDepth) depth = kMaxDepth;
+    s.fifo = {static_cast<int>(depth), slots};
+    s.smem = depth * row;
+    return s;
 }
 
+// The instance for the vectors a thread, the stream's type, and whether there
+// are a post-norm and a gate.
 template <typename F>
-cudaError_t with_nv(int nv, F&& f) {
-    if (nv == 1) return f(std::integral_constant<int, 1>());
-    if (nv == 2) return f(std::integral_constant<int, 2>());
-    return f(std::integral_constant<int, 4>());
-}
-template <typename F>
-cudaError_t with_bool(bool b, F&& f) {
-    return b ? f(std::true_type()) : f(std::false_type());
+cudaError_t with_instance(int nv, bool f32, bool post, bool gate, F&& f) {
+    const auto flag = [](bool b, auto&& g) {
+        return b ? g(std::true_type()) : g(std::false_type());
+    };
+    return flag(f32, [&](auto f32_) {
+        return flag(post, [&](auto post_) {
+            return flag(gate, [&](auto gate_) {
+                if (nv == 1) return f(std::integral_constant<int, 1>(), f32_, post_, gate_);
+                if (nv == 2) return f(std::integral_constant<int, 2>(), f32_, post_, gate_);
+                return f(std::integral_constant<int, 4>(), f32_, post_, gate_);
+            });
+        });
+    });
 }
 
 }  // namespace
@@ -398,47 +589,39 @@ cudaError_t launch_residual_norm(const ResidualNorm& a, int fmt, unsigned sf_fla
     lay.words = (lay.groups + 3) / 4;
     lay.rows4 = (a.T + 3) / 4 * 4;
     const int64_t rows = a.out && (sf_flags & kSfColMajor) ? lay.rows4 : a.T;
-    const Shape s = shape_of(a.C);
-    return with_nv(s.nv, [&](auto nv) {
-        return with_bool(a.r_f32, [&](auto f32) {
-            auto go = [&](auto f) {
-                auto* k = &residual_norm_kernel<decltype(nv)::value, decltype(f32)::value,
-                                                decltype(f)::value>;
-                const int grid =
-                    persistent_grid(reinterpret_cast<const void*>(k), s.threads, 0, rows);
-                if (const cudaError_t e = upload_checks(stream)) return e;
-                return launch_pdl(k, grid, s.threads, 0, stream, true, a, lay, rows);
-            };
-            if (!a.out) return go(std::integral_constant<int, kNoCast>());
-            if (fmt == kFmtE4M3) return go(std::integral_constant<int, kFmtE4M3>());
-            return go(std::integral_constant<int, kFmtE5M2>());
-        });
+    const Shape s = shape_of(a.C, (a.r_f32 ? 2 : 1) + (a.h ? 1 : 0) + (a.gate ? 1 : 0));
+    return with_instance(s.nv, a.r_f32, a.post, a.gate, [&](auto nv, auto f32, auto post, auto gate) {
+        auto* k = &residual_norm_kernel<nv(), f32(), post(), gate()>;
+        const int grid = persistent_grid(reinterpret_cast<const void*>(k), s.threads, s.smem, rows);
+        if (const cudaError_t e = upload_checks(stream)) return e;
+        return launch_pdl(k, grid, s.threads, s.smem, stream, true, a, lay, rows, fmt, s.fifo);
     });
 }
 
-// Partial rows a backward launch writes at most: the SMs times the CTAs of the
-// smallest row that fit one, no more than rows.
+// Partial rows a backward launch writes at most: one a CTA, as many CTAs an SM
+// as its threads allow, no more than rows.
 int64_t residual_norm_parts(int64_t T, int64_t C) {
-    const int64_t per_sm = 2048 / shape_of(C).threads;
+    const int64_t per_sm = 2 * kMaxThreads / shape_of(C, 1).threads;
     const int64_t most = num_sms() * (per_sm < 16 ? per_sm : 16);
     return T < most ? T : most;
 }
 
 cudaError_t launch_residual_norm_backward(const ResidualNormGrad& a, cudaStream_t stream) {
-    const Shape s = shape_of(a.C);
+    const int slot = a.r_f32 ? 2 : 1;
+    const Shape s = shape_of(a.C, (a.dr ? slot : 0) + (a.dx ? 1 + slot : 0) + (a.h ? 1 : 0) +
+                                      (a.gate ? 1 : 0));
     int parts = 0;
-    const cudaError_t e = with_nv(s.nv, [&](auto nv) {
-        return with_bool(a.r_f32, [&](auto f32) {
-            auto* k =
-                &residual_norm_backward_kernel<decltype(nv)::value, decltype(f32)::value>;
-            parts = persistent_grid(reinterpret_cast<const void*>(k), s.threads, 0,
+    const cudaError_t e =
+        with_instance(s.nv, a.r_f32, a.post, a.gate, [&](auto nv, auto f32, auto post, auto gate) {
+            auto* k = &residual_norm_backward_kernel<nv(), f32(), post(), gate()>;
+            parts = persistent_grid(reinterpret_cast<const void*>(k), s.threads, s.smem,
                                     residual_norm_parts(a.T, a.C));
             if (const cudaError_t e = upload_checks(stream)) return e;
-            return launch_pdl(k, parts, s.threads, 0, stream, true, a);
+            return launch_pdl(k, parts, s.threads, s.smem, stream, true, a, s.fifo);
         });
-    });
     if (e != cudaSuccess || (!a.dw_pre && !a.dw_post)) return e;
-    return launch_pdl(&sum_parts_kernel, static_cast<int>(a.C / 64), 256, 0, stream, true,
+    return launch_pdl(&sum_parts_kernel, static_cast<int>(a.C / (2 * kSumCols)),
+                      kSumCols * kSumSlices, 0, stream, true,
                       static_cast<const float*>(a.workspace), a.dw_pre, a.dw_post, a.C, parts);
 }
 

@@ -221,6 +221,7 @@ struct OccKeyHash {
 };
 std::mutex g_occ_mutex;
 std::unordered_map<OccKey, int, OccKeyHash> g_occ;
+std::unordered_map<OccKey, size_t, OccKeyHash> g_smem_limit;  // by kernel and device
 }  // namespace
 
 int persistent_grid(const void* kernel, int threads, size_t smem, int64_t blocks_needed) {
@@ -234,9 +235,16 @@ int persistent_grid(const void* kernel, int threads, size_t smem, int64_t blocks
         if (it != g_occ.end()) per_sm = it->second;
     }
     if (per_sm == 0) {
-        if (smem > 48 * 1024)
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(smem));
+        if (smem > 48 * 1024) {
+            // the limit only goes up: a kernel may be launched with several sizes
+            std::lock_guard<std::mutex> lock(g_occ_mutex);
+            size_t& limit = g_smem_limit[OccKey{kernel, dev, 0, 0}];
+            if (smem > limit) {
+                cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     static_cast<int>(smem));
+                limit = smem;
+            }
+        }
         if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) !=
                 cudaSuccess ||
             per_sm <= 0)
