@@ -34,29 +34,51 @@ namespace {
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kMaxThreads = 512;
 
-// Sums of N values over the CTA, in the same order each time.  Two buffers in
-// turn: a thread past the barrier of one sum has read the sum before.
+constexpr int kMaxWarps = kMaxThreads / 32;
+
+// Sums of N values over the CTA, in the same order each time.  The lanes first
+// split the values among them (half of a pair to each half of the warp), so
+// that N values take log2(N) steps more than one, not N times as many.  Two
+// buffers in turn: a thread past the barrier of one sum has read the sum before.
 template <int N>
-__device__ __forceinline__ void cta_sum(float (&v)[N], float (*buf)[N][32], int& turn) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+struct CtaSum {
+    static constexpr int kPad = N == 1 ? 1 : N == 2 ? 2 : 4;  // values, lanes of one: 32 / kPad
+    static constexpr int kLanes = 32 / kPad;
+    float buf[2][kPad][kMaxWarps];
+
+    __device__ __forceinline__ void operator()(float (&v)[N], int& turn) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+        float s;
+        if constexpr (kPad == 1) {
+            s = v[0];
+        } else if constexpr (kPad == 2) {
+            const bool hi = lane & 16;
+            s = (hi ? v[1] : v[0]) + __shfl_xor_sync(kAll, hi ? v[0] : v[1], 16);
+        } else {
+            static_assert(N == 3);
+            const bool hi = lane & 16, up = lane & 8;
+            const float a = (hi ? v[2] : v[0]) + __shfl_xor_sync(kAll, hi ? v[0] : v[2], 16);
+            const float b = (hi ? 0.0f : v[1]) + __shfl_xor_sync(kAll, hi ? v[1] : 0.0f, 16);
+            s = (up ? b : a) + __shfl_xor_sync(kAll, up ? a : b, 8);
+        }
 #pragma unroll
-    for (int i = 0; i < N; ++i)
+        for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+        const int mine = lane / kLanes, j = lane % kLanes;
+        if (warps > 1) {
+            if (j == 0) buf[turn][mine][warp] = s;
+            __syncthreads();
+            s = 0.0f;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(kAll, v[i], o);
-    if (warps == 1) return;
-    if (lane == 0)
+            for (int k = 0; k < kMaxWarps; k += kLanes)
+                if (j + k < warps) s += buf[turn][mine][j + k];
 #pragma unroll
-        for (int i = 0; i < N; ++i) buf[turn][i][warp] = v[i];
-    __syncthreads();
+            for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+            turn ^= 1;
+        }
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        float s = lane < warps ? buf[turn][i][lane] : 0.0f;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
-        v[i] = s;
+        for (int i = 0; i < N; ++i) v[i] = kPad == 1 ? s : __shfl_sync(kAll, s, i * kLanes);
     }
-    turn ^= 1;
-}
+};
 
 // ---------------------------------------------------------------------------
 // a thread's rows in flight
@@ -85,23 +107,23 @@ __device__ __forceinline__ void cp_async_wait(int depth) {
 constexpr int kMaxDepth = 4;
 
 struct Fifo {
-    int depth, slots;  // rows, 16-byte pieces of a vector of one row
+    int depth, slots;  // stages, 16-byte pieces of a vector of one row
 };
 
-// Copies vector `vec` of a row into consecutive slots from `slot` on.
+// Copies the vector at `at` (in vectors of eight) of a tensor to `dst`; a
+// binary32 vector's second half goes `vecs` pieces further.
 template <bool F32>
-__device__ __forceinline__ void fetch(uint4* stage, int slot, int vecs, int vec, const void* base,
-                                      int64_t row) {
-    const uint4* p = static_cast<const uint4*>(base) + (row * vecs + vec) * (F32 ? 2 : 1);
-    cp_async16(stage + slot * vecs + vec, p);
-    if constexpr (F32) cp_async16(stage + (slot + 1) * vecs + vec, p + 1);
+__device__ __forceinline__ void fetch(uint4* dst, int vecs, const void* base, int64_t at) {
+    const uint4* p = static_cast<const uint4*>(base) + at * (F32 ? 2 : 1);
+    cp_async16(dst, p);
+    if constexpr (F32) cp_async16(dst + vecs, p + 1);
 }
 // Its eight values.
 template <bool F32>
-__device__ __forceinline__ void values8(const uint4* stage, int slot, int vecs, int vec, float* v) {
-    const uint4 a = stage[slot * vecs + vec];
+__device__ __forceinline__ void values8(const uint4* src, int vecs, float* v) {
+    const uint4 a = *src;
     if constexpr (F32) {
-        const uint4 b = stage[(slot + 1) * vecs + vec];
+        const uint4 b = src[vecs];
         v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y);
         v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
         v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y);
@@ -111,8 +133,8 @@ __device__ __forceinline__ void values8(const uint4* stage, int slot, int vecs, 
     }
 }
 template <bool F32>
-__device__ __forceinline__ void store8(void* base, int64_t vec, const float* v) {
-    uint4* p = static_cast<uint4*>(base) + vec * (F32 ? 2 : 1);
+__device__ __forceinline__ void store8(void* base, int64_t at, const float* v) {
+    uint4* p = static_cast<uint4*>(base) + at * (F32 ? 2 : 1);
     if constexpr (F32) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -202,117 +224,146 @@ __device__ __forceinline__ void cast8(const ResidualNorm& a, const SfLayout& lay
     }
 }
 
-template <int NV, bool F32, bool POST, bool GATE>
+// ROWS consecutive rows are taken at a time, so that their reductions share the
+// barriers and the shuffles, and one row's arithmetic covers the other's
+// latencies.  WHOLE: there is a block and a pre-norm, and the row is exactly
+// the CTA's vectors, so nothing of that is asked again for each vector.
+template <int NV, bool F32, bool POST, bool GATE, int ROWS, bool WHOLE>
 __global__ void __launch_bounds__(kMaxThreads)
     residual_norm_kernel(const ResidualNorm a, const SfLayout lay, int64_t rows_walk, int fmt,
                          Fifo q8) {
     extern __shared__ uint4 fifo[];
-    __shared__ float buf[2][1][32];
+    __shared__ CtaSum<ROWS> cta_sum;
     grid_dependency_launch();
     constexpr int kR = F32 ? 2 : 1;   // slots of r; then h, gate
     int turn = 0;
     const int tid = threadIdx.x, vecs = static_cast<int>(a.C / 8);
     const float inv_c = 1.0f / static_cast<float>(a.C);
-    const int stage_size = q8.slots * vecs;
-    const auto fetch_row = [&](int64_t t, int stage) {
-        if (t < a.T)
+    const int row_size = q8.slots * vecs;
+    const bool has_h = WHOLE || a.h, pre = WHOLE || a.pre;
+    const auto inside = [&](int vec) { return WHOLE || vec < vecs; };
+    const auto fetch_rows = [&](int64_t t0, int stage) {
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k) {
+            if (t0 + k >= a.T) break;
+            uint4* s = fifo + (stage * ROWS + k) * row_size;
+            const int64_t row = (t0 + k) * vecs;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int vec = tid + i * blockDim.x;
-                if (vec >= vecs) continue;
-                uint4* s = fifo + stage * stage_size;
-                if (a.h) fetch<false>(s, kR, vecs, vec, a.h, t);
-                fetch<F32>(s, 0, vecs, vec, a.r, t);
-                if constexpr (GATE) fetch<false>(s, kR + 1, vecs, vec, a.gate, t);
+                if (!inside(vec)) continue;
+                if (has_h) fetch<false>(s + kR * vecs + vec, vecs, a.h, row + vec);
+                fetch<F32>(s + vec, vecs, a.r, row + vec);
+                if constexpr (GATE) fetch<false>(s + (kR + 1) * vecs + vec, vecs, a.gate, row + vec);
             }
+        }
         cp_async_commit();
     };
+    const int64_t step = static_cast<int64_t>(gridDim.x) * ROWS;
+    const int64_t start = static_cast<int64_t>(blockIdx.x) * ROWS;
     grid_dependency_wait();
-    for (int d = 0; d < q8.depth - 1; ++d)
-        fetch_row(blockIdx.x + static_cast<int64_t>(d) * gridDim.x, d);
+    for (int d = 0; d < q8.depth - 1; ++d) fetch_rows(start + d * step, d);
     Weights<NV> w_post, w_pre;
     w_post.init(a.w_post, a.res_scale, vecs);
     w_pre.init(a.w_pre, 1.0f, vecs);
     int stage = 0, ahead = q8.depth - 1;
-    for (int64_t t = blockIdx.x; t < rows_walk; t += gridDim.x) {
-        fetch_row(t + static_cast<int64_t>(q8.depth - 1) * gridDim.x, ahead);
-        if (t >= a.T) {  // the padding rows of the column-major scale layouts
-            for (int j = tid; j < lay.groups; j += blockDim.x)
-                store_scale(a.sf, lay, t, false, j, 0.0f);
-            continue;
-        }
-        const uint4* s = fifo + stage * stage_size;
+    for (int64_t t = start; t < rows_walk; t += step) {
+        fetch_rows(t + (q8.depth - 1) * step, ahead);
+        if (t + ROWS > a.T)  // the padding rows of the column-major scale layouts
+            for (int64_t row = t < a.T ? a.T : t; row < rows_walk && row < t + ROWS; ++row)
+                for (int j = tid; j < lay.groups; j += blockDim.x)
+                    store_scale(a.sf, lay, row, false, j, 0.0f);
+        if (t >= a.T) continue;
+        const uint4* s = fifo + stage * ROWS * row_size;
         cp_async_wait(q8.depth);
         stage = stage + 1 == q8.depth ? 0 : stage + 1;
         ahead = ahead + 1 == q8.depth ? 0 : ahead + 1;
-        float sum[1] = {0.0f};
-        float p = 1.0f;
+        // a row past the last one computes on what its slots hold and stores nothing
+        float v[ROWS][NV][8];
+        float sum[ROWS], p[ROWS];
         if constexpr (POST) {
+#pragma unroll
+            for (int k = 0; k < ROWS; ++k) {
+                float2 c = two(0.0f);
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int vec = tid + i * blockDim.x;
+                    if (!inside(vec)) continue;
+                    values8<false>(s + k * row_size + kR * vecs + vec, vecs, v[k][i]);
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) c = fma2(at2(v[k][i], e), at2(v[k][i], e), c);
+                }
+                sum[k] = c.x + c.y;
+            }
+            cta_sum(sum, turn);
+#pragma unroll
+            for (int k = 0; k < ROWS; ++k) {
+                p[k] = rsqrtf(sum[k] * inv_c + a.eps);
+                if (tid == 0 && a.rstd_post && t + k < a.T) st_plain(a.rstd_post + t + k, p[k]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k) {
+            float2 c = two(0.0f);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int vec = tid + i * blockDim.x;
-                if (vec >= vecs) continue;
-                float h[8];
-                values8<false>(s, kR, vecs, vec, h);
-                float2 c = two(0.0f);
+                float* vi = v[k][i];
+                if (!inside(vec)) {
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) c = fma2(at2(h, e), at2(h, e), c);
-                sum[0] += c.x + c.y;
-            }
-            cta_sum<1>(sum, buf, turn);
-            p = __frsqrt_rn(sum[0] * inv_c + a.eps);
-            if (tid == 0 && a.rstd_post) st_plain(a.rstd_post + t, p);
-            sum[0] = 0.0f;
-        }
-        float v[NV][8];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int vec = tid + i * blockDim.x;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
-            if (vec >= vecs) continue;
-            values8<F32>(s, 0, vecs, vec, v[i]);
-            if (a.h) {
-                float h[8], w[8], g[8];
-                values8<false>(s, kR, vecs, vec, h);
-                if constexpr (GATE) values8<false>(s, kR + 1, vecs, vec, g);
-                w_post.get(i, vec, w);
-#pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    float2 b = mul2(at2(w, e), at2(h, e));
-                    if constexpr (POST) b = mul2(b, two(p));
-                    if constexpr (GATE) {
-                        float2 rest;
-                        b = mul2(b, sigmoid2(at2(g, e), rest));
-                    }
-                    put2(v[i], e, add2(b, at2(v[i], e)));
+                    for (int e = 0; e < 8; ++e) vi[e] = 0.0f;
+                    continue;
                 }
-                store8<F32>(a.r_out, t * vecs + vec, v[i]);
+                const uint4* at = s + k * row_size + vec;
+                float r[8];
+                values8<F32>(at, vecs, r);
+                if (has_h) {
+                    float w[8], g[8];
+                    if constexpr (!POST) values8<false>(at + kR * vecs, vecs, vi);
+                    if constexpr (GATE) values8<false>(at + (kR + 1) * vecs, vecs, g);
+                    w_post.get(i, vec, w);
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) {
+                        float2 b = mul2(at2(w, e), at2(vi, e));
+                        if constexpr (GATE) {
+                            float2 rest;
+                            b = mul2(b, sigmoid2(at2(g, e), rest));
+                        }
+                        put2(vi, e, POST ? fma2(b, two(p[k]), at2(r, e)) : add2(b, at2(r, e)));
+                    }
+                    if (ROWS == 1 || t + k < a.T) store8<F32>(a.r_out, (t + k) * vecs + vec, vi);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) vi[e] = r[e];
+                }
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) c = fma2(at2(vi, e), at2(vi, e), c);
             }
-            float2 c = two(0.0f);
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) c = fma2(at2(v[i], e), at2(v[i], e), c);
-            sum[0] += c.x + c.y;
+            sum[k] = c.x + c.y;
         }
-        if (!a.pre) continue;
-        cta_sum<1>(sum, buf, turn);
-        const float q = __frsqrt_rn(sum[0] * inv_c + a.eps);
-        if (tid == 0 && a.rstd_pre) st_plain(a.rstd_pre + t, q);
+        if (!pre) continue;
+        cta_sum(sum, turn);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int vec = tid + i * blockDim.x;
-            float w[8] = {};
-            if (vec < vecs) w_pre.get(i, vec, w);
+        for (int k = 0; k < ROWS; ++k) {
+            if (ROWS > 1 && t + k >= a.T) break;
+            const float q = rsqrtf(sum[k] * inv_c + a.eps);
+            if (tid == 0 && a.rstd_pre) st_plain(a.rstd_pre + t + k, q);
 #pragma unroll
-            for (int e = 0; e < 8; e += 2)
-                put2(v[i], e, mul2(mul2(at2(v[i], e), two(q)), at2(w, e)));
-            if (a.x_out && vec < vecs)
-                st_stream(static_cast<uint4*>(a.x_out) + t * vecs + vec, pack8_bf16(v[i]));
-            if (!a.out) continue;
-            if (fmt == kFmtE4M3)
-                cast8<kFmtE4M3>(a, lay, t, vecs, vec, v[i]);
-            else
-                cast8<kFmtE5M2>(a, lay, t, vecs, vec, v[i]);
+            for (int i = 0; i < NV; ++i) {
+                const int vec = tid + i * blockDim.x;
+                float* vi = v[k][i];
+                float w[8] = {};
+                if (inside(vec)) w_pre.get(i, vec, w);
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) put2(vi, e, mul2(mul2(at2(vi, e), two(q)), at2(w, e)));
+                if (a.x_out && inside(vec))
+                    st_stream(static_cast<uint4*>(a.x_out) + (t + k) * vecs + vec, pack8_bf16(vi));
+                if (!a.out) continue;
+                if (fmt == kFmtE4M3)
+                    cast8<kFmtE4M3>(a, lay, t + k, vecs, vec, vi);
+                else
+                    cast8<kFmtE5M2>(a, lay, t + k, vecs, vec, vi);
+            }
         }
     }
 }
@@ -329,45 +380,51 @@ __global__ void __launch_bounds__(kMaxThreads)
 // thread), h and the gate are read from shared memory again.  The weight
 // gradients are summed over a CTA's rows in registers and written as one
 // partial row a CTA; sum_parts_kernel adds them up in order.
-template <int NV, bool F32, bool POST, bool GATE>
+// WHOLE: dr', dx and h are given and the row is exactly the CTA's vectors.
+template <int NV, bool F32, bool POST, bool GATE, bool WHOLE>
 __global__ void __launch_bounds__(kMaxThreads)
     residual_norm_backward_kernel(const ResidualNormGrad a, Fifo q8) {
     extern __shared__ uint4 fifo[];
-    __shared__ float buf[2][POST ? 3 : 1][32];
+    __shared__ CtaSum<POST ? 3 : 1> cta_sum;
     grid_dependency_launch();
     constexpr int kS = F32 ? 2 : 1;   // slots of a stream: h, gate, dr, dx, r
     constexpr bool kKept = Weights<NV>::kKept;
-    constexpr int kH = 0, kGate = 1;
-    const int at_dr = (a.h ? 1 : 0) + (GATE ? 1 : 0), at_dx = at_dr + (a.dr ? kS : 0);
+    const bool has_dr = WHOLE || a.dr, has_dx = WHOLE || a.dx, has_h = WHOLE || a.h;
     int turn = 0;
     const int tid = threadIdx.x, vecs = static_cast<int>(a.C / 8);
+    const int at_gate = vecs;
+    const int at_dr = ((has_h ? 1 : 0) + (GATE ? 1 : 0)) * vecs;
+    const int at_dx = at_dr + (has_dr ? kS : 0) * vecs;
+    const int at_r = at_dx + vecs;
     const float inv_c = 1.0f / static_cast<float>(a.C);
     const int stage_size = q8.slots * vecs;
+    const auto inside = [&](int vec) { return WHOLE || vec < vecs; };
     const auto fetch_row = [&](int64_t t, int stage) {
         if (t < a.T)
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int vec = tid + i * blockDim.x;
-                if (vec >= vecs) continue;
-                uint4* s = fifo + stage * stage_size;
-                if (a.dr) fetch<F32>(s, at_dr, vecs, vec, a.dr, t);
-                if (a.dx) {
-                    fetch<false>(s, at_dx, vecs, vec, a.dx, t);
-                    fetch<F32>(s, at_dx + 1, vecs, vec, a.r, t);
+                if (!inside(vec)) continue;
+                uint4* s = fifo + stage * stage_size + vec;
+                const int64_t at = t * vecs + vec;
+                if (has_dr) fetch<F32>(s + at_dr, vecs, a.dr, at);
+                if (has_dx) {
+                    fetch<false>(s + at_dx, vecs, a.dx, at);
+                    fetch<F32>(s + at_r, vecs, a.r, at);
                 }
-                if (a.h) fetch<false>(s, kH, vecs, vec, a.h, t);
-                if constexpr (GATE) fetch<false>(s, kGate, vecs, vec, a.gate, t);
+                if (has_h) fetch<false>(s, vecs, a.h, at);
+                if constexpr (GATE) fetch<false>(s + at_gate, vecs, a.gate, at);
             }
         cp_async_commit();
     };
     // dr', dx and r' of one vector, zeros for what is absent
-    const auto stream = [&](const uint4* s, int vec, float* g, float* d, float* r) {
+    const auto stream = [&](const uint4* s, float* g, float* d, float* r) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) g[e] = d[e] = r[e] = 0.0f;
-        if (a.dr) values8<F32>(s, at_dr, vecs, vec, g);
-        if (a.dx) {
-            values8<false>(s, at_dx, vecs, vec, d);
-            values8<F32>(s, at_dx + 1, vecs, vec, r);
+        if (has_dr) values8<F32>(s + at_dr, vecs, g);
+        if (has_dx) {
+            values8<false>(s + at_dx, vecs, d);
+            values8<F32>(s + at_r, vecs, r);
         }
     };
     float acc_pre[NV][8] = {}, acc_post[NV][8] = {};
@@ -377,11 +434,18 @@ __global__ void __launch_bounds__(kMaxThreads)
     Weights<NV> w_post, w_pre;
     w_post.init(a.w_post, a.res_scale, vecs);
     w_pre.init(a.w_pre, 1.0f, vecs);
+    float p_next = 1.0f, q_next = 0.0f;
+    const auto load_factors = [&](int64_t t) {
+        if (POST && t < a.T) p_next = ld_ro(a.rstd_post + t);
+        if (has_dx && t < a.T) q_next = ld_ro(a.rstd_pre + t);
+    };
+    load_factors(blockIdx.x);
     int stage = 0, ahead = q8.depth - 1;
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
         fetch_row(t + static_cast<int64_t>(q8.depth - 1) * gridDim.x, ahead);
-        const float p = POST ? ld_ro(a.rstd_post + t) : 1.0f;
-        const float q = a.dx ? ld_ro(a.rstd_pre + t) : 0.0f;
+        // the row's factors were loaded a row ago
+        const float p = p_next, q = q_next;
+        load_factors(t + gridDim.x);
         const uint4* s = fifo + stage * stage_size;
         cp_async_wait(q8.depth);
         stage = stage + 1 == q8.depth ? 0 : stage + 1;
@@ -391,13 +455,13 @@ __global__ void __launch_bounds__(kMaxThreads)
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int vec = tid + i * blockDim.x;
-            if (vec >= vecs) continue;
+            if (!inside(vec)) continue;
             float* gi = g[kKept ? i : 0];
             float* ri = r[kKept ? i : 0];
             float d[8], w[8];
-            stream(s, vec, gi, d, ri);
+            stream(s + vec, gi, d, ri);
             float2 s1 = two(0.0f);
-            if (a.dx) {
+            if (has_dx) {
                 w_pre.get(i, vec, w);
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) {
@@ -412,8 +476,8 @@ __global__ void __launch_bounds__(kMaxThreads)
             if constexpr (POST) {
                 float2 s2 = two(0.0f), s3 = s2;
                 float h[8], gt[8];
-                values8<false>(s, kH, vecs, vec, h);
-                if constexpr (GATE) values8<false>(s, kGate, vecs, vec, gt);
+                values8<false>(s + vec, vecs, h);
+                if constexpr (GATE) values8<false>(s + vec + at_gate, vecs, gt);
                 w_post.get(i, vec, w);
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) {
@@ -427,21 +491,21 @@ __global__ void __launch_bounds__(kMaxThreads)
                 sum[2] += s3.x + s3.y;
             }
         }
-        if (POST || a.dx) cta_sum<POST ? 3 : 1>(sum, buf, turn);
+        if (POST || has_dx) cta_sum(sum, turn);
         const float c1 = -q * q * inv_c * sum[0];              // dr = G + c1 r'
         float c2 = 0.0f;                                       // dh = p (..) + c2 h
         if constexpr (POST) c2 = -p * p * p * inv_c * (sum[1] + c1 * sum[2]);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int vec = tid + i * blockDim.x;
-            if (vec >= vecs) continue;
+            if (!inside(vec)) continue;
             const int64_t at = t * vecs + vec;
             float* gi = g[kKept ? i : 0];
             float* ri = r[kKept ? i : 0];
             float w[8];
             if constexpr (!kKept) {
                 float d[8];
-                stream(s, vec, gi, d, ri);
+                stream(s + vec, gi, d, ri);
                 w_pre.get(i, vec, w);
 #pragma unroll
                 for (int e = 0; e < 8; e += 2)
@@ -450,10 +514,10 @@ __global__ void __launch_bounds__(kMaxThreads)
 #pragma unroll
             for (int e = 0; e < 8; e += 2) put2(gi, e, fma2(at2(ri, e), two(c1), at2(gi, e)));
             store8<F32>(a.dr_out, at, gi);
-            if (!a.h) continue;
+            if (!has_h) continue;
             float h[8], gt[8], dh[8], dgate[8];
-            values8<false>(s, kH, vecs, vec, h);
-            if constexpr (GATE) values8<false>(s, kGate, vecs, vec, gt);
+            values8<false>(s + vec, vecs, h);
+            if constexpr (GATE) values8<false>(s + vec + at_gate, vecs, gt);
             w_post.get(i, vec, w);
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
@@ -535,25 +599,27 @@ __global__ void __launch_bounds__(kSumCols* kSumSlices)
         st_plain(reinterpret_cast<float4*>(out) + (c4 - (post ? C / 4 : 0)), s);
 }
 
-// Vectors a thread holds, threads a CTA and rows in flight for rows of C
-// channels of `slots` 16-byte pieces a vector: CTAs of at most 512 threads (128
-// registers), about 768 threads an SM, which share 224 KB of shared memory for
-// up to four rows each.
+// Vectors a thread holds, threads a CTA and stages in flight for rows of C
+// channels of `slots` 16-byte pieces a vector, `rows` at a time: CTAs of at most
+// 512 threads (128 registers), about 768 threads an SM, which share 224 KB of
+// shared memory for up to four stages each.
 struct Shape {
     int nv, threads;
+    bool exact;  // the row is exactly the CTA's vectors
     size_t smem;
     Fifo fifo;
 };
 constexpr size_t kSmemPerSm = 224 * 1024;
 constexpr int kThreadsPerSm = 768;
-Shape shape_of(int64_t C, int slots) {
+Shape shape_of(int64_t C, int slots, int rows) {
     Shape s;
     const int vecs = static_cast<int>(C / 8);
     s.nv = vecs <= kMaxThreads ? 1 : vecs <= 2 * kMaxThreads ? 2 : 4;
     s.threads = ((vecs + s.nv - 1) / s.nv + 31) / 32 * 32;
-    const size_t row = static_cast<size_t>(slots) * vecs * 16;
+    s.exact = vecs == s.nv * s.threads;
+    const size_t row = static_cast<size_t>(slots) * vecs * 16 * rows;
     const size_t ctas = kThreadsPerSm / s.threads < 16 ? kThreadsPerSm / s.threads : 16;
-    size_t depth = kSmemPerSm / (row * ctas);
+    size_t depth = ctas ? kSmemPerSm / (row * ctas) : 0;
     if (depth < 2) depth = kSmemPerSm / row >= 2 ? 2 : 1;
     if (depth > kMaxDepth) depth = kMaxDepth;
     s.fifo = {static_cast<int>(depth), slots};
@@ -589,19 +655,32 @@ cudaError_t launch_residual_norm(const ResidualNorm& a, int fmt, unsigned sf_fla
     lay.words = (lay.groups + 3) / 4;
     lay.rows4 = (a.T + 3) / 4 * 4;
     const int64_t rows = a.out && (sf_flags & kSfColMajor) ? lay.rows4 : a.T;
-    const Shape s = shape_of(a.C, (a.r_f32 ? 2 : 1) + (a.h ? 1 : 0) + (a.gate ? 1 : 0));
-    return with_instance(s.nv, a.r_f32, a.post, a.gate, [&](auto nv, auto f32, auto post, auto gate) {
-        auto* k = &residual_norm_kernel<nv(), f32(), post(), gate()>;
-        const int grid = persistent_grid(reinterpret_cast<const void*>(k), s.threads, s.smem, rows);
+    const int slots = (a.r_f32 ? 2 : 1) + (a.h ? 1 : 0) + (a.gate ? 1 : 0);
+    const auto launch = [&](auto* k, int rows_at_once) {
+        const Shape s = shape_of(a.C, slots, rows_at_once);
+        const int grid = persistent_grid(reinterpret_cast<const void*>(k), s.threads, s.smem,
+                                         (rows + rows_at_once - 1) / rows_at_once);
         if (const cudaError_t e = upload_checks(stream)) return e;
         return launch_pdl(k, grid, s.threads, s.smem, stream, true, a, lay, rows, fmt, s.fifo);
+    };
+    const Shape s = shape_of(a.C, slots, 1);
+    return with_instance(s.nv, a.r_f32, a.post, a.gate, [&](auto nv, auto f32, auto post, auto gate) {
+        if constexpr (nv() <= 2) {
+            if (s.exact && a.h && a.pre) {
+                // two rows at a time once every SM has work for that and the next two fit
+                if (a.T >= 4 * int64_t{num_sms()} && shape_of(a.C, slots, 2).fifo.depth >= 2)
+                    return launch(&residual_norm_kernel<nv(), f32(), post(), gate(), 2, true>, 2);
+                return launch(&residual_norm_kernel<nv(), f32(), post(), gate(), 1, true>, 1);
+            }
+        }
+        return launch(&residual_norm_kernel<nv(), f32(), post(), gate(), 1, false>, 1);
     });
 }
 
 // Partial rows a backward launch writes at most: one a CTA, as many CTAs an SM
 // as its threads allow, no more than rows.
 int64_t residual_norm_parts(int64_t T, int64_t C) {
-    const int64_t per_sm = 2 * kMaxThreads / shape_of(C, 1).threads;
+    const int64_t per_sm = 2 * kMaxThreads / shape_of(C, 1, 1).threads;
     const int64_t most = num_sms() * (per_sm < 16 ? per_sm : 16);
     return T < most ? T : most;
 }
@@ -609,15 +688,22 @@ int64_t residual_norm_parts(int64_t T, int64_t C) {
 cudaError_t launch_residual_norm_backward(const ResidualNormGrad& a, cudaStream_t stream) {
     const int slot = a.r_f32 ? 2 : 1;
     const Shape s = shape_of(a.C, (a.dr ? slot : 0) + (a.dx ? 1 + slot : 0) + (a.h ? 1 : 0) +
-                                      (a.gate ? 1 : 0));
+                                      (a.gate ? 1 : 0), 1);
     int parts = 0;
     const cudaError_t e =
         with_instance(s.nv, a.r_f32, a.post, a.gate, [&](auto nv, auto f32, auto post, auto gate) {
-            auto* k = &residual_norm_backward_kernel<nv(), f32(), post(), gate()>;
-            parts = persistent_grid(reinterpret_cast<const void*>(k), s.threads, s.smem,
-                                    residual_norm_parts(a.T, a.C));
-            if (const cudaError_t e = upload_checks(stream)) return e;
-            return launch_pdl(k, parts, s.threads, s.smem, stream, true, a, s.fifo);
+            const auto launch = [&](auto* k) {
+                parts = persistent_grid(reinterpret_cast<const void*>(k), s.threads, s.smem,
+                                        residual_norm_parts(a.T, a.C));
+                if (const cudaError_t e = upload_checks(stream)) return e;
+                return launch_pdl(k, parts, s.threads, s.smem, stream, true, a, s.fifo);
+            };
+            if constexpr (nv() <= 2) {
+                if (s.exact && a.dr && a.dx && a.h)
+                    return launch(
+                        &residual_norm_backward_kernel<nv(), f32(), post(), gate(), true>);
+            }
+            return launch(&residual_norm_backward_kernel<nv(), f32(), post(), gate(), false>);
         });
     if (e != cudaSuccess || (!a.dw_pre && !a.dw_post)) return e;
     return launch_pdl(&sum_parts_kernel, static_cast<int>(a.C / (2 * kSumCols)),
