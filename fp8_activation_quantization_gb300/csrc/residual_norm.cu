@@ -87,23 +87,6 @@ struct CtaSum {
 // reads, only its own 16-byte pieces, so its wait for its own copies is all
 // the ordering there is.  Piece `slot` of vector `vec` of a stage:
 // (stage * slots + slot) * vecs + vec.
-__device__ __forceinline__ void cp_async16(uint4* dst, const void* src) {
-    if (!access_ok(src, 16, false)) return;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() {
-    asm volatile("cp.async.commit_group;" ::: "memory");
-}
-// All but the newest depth - 1 groups have arrived.
-__device__ __forceinline__ void cp_async_wait(int depth) {
-    switch (depth) {
-        case 1: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
-        case 2: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-        case 3: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-        default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-    }
-}
 constexpr int kMaxDepth = 4;
 
 struct Fifo {

@@ -29,6 +29,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr unsigned kAll = 0xffffffffu;
+constexpr int kDepth = 3;    // units in flight, the current one among them
 constexpr int kBf16Out = 2;  // in the place of an FP8 format: the gradients leave as bf16
 
 // Largest value of the eight lanes that share a group.
@@ -47,22 +48,8 @@ __device__ __forceinline__ float absmax16(const float* v) {
 // The flat stream of swiglu_flat.cu: a warp takes units of four groups of y
 // (lane l: 16 channels of group 4u + l / 8) and reads the 32-byte runs of
 // gate and up; the same registers give the two checkpoint groups and the group
-// of y.
-struct RawPair {
-    uint4 g[2], u[2];
-    float w;
-
-    __device__ __forceinline__ void load(const uint4* x, const float* wt, int64_t t, int j, int k,
-                                         int64_t H) {
-        const uint4* pg = x + t * (H / 4) + j * 16 + k * 2;
-        const uint4* pu = pg + H / 8;
-        g[0] = ld_stream(pg);
-        g[1] = ld_stream(pg + 1);
-        u[0] = ld_stream(pu);
-        u[1] = ld_stream(pu + 1);
-        w = wt ? ld_ro(wt + t) : 1.0f;
-    }
-};
+// of y.  The next two units are in flight as asynchronous copies into the
+// thread's own slots of shared memory, which costs no registers.
 
 // Codes of one lane's 16 values with the exact quotient, and its group's scale.
 template <int FMT>
@@ -73,56 +60,99 @@ __device__ __forceinline__ uint4 cast16(const float* v, float& sc) {
     return make_uint4(lo.x, lo.y, hi.x, hi.y);
 }
 
+// A bf16 run of a group is 16 vectors of 8 channels, of which lane k of the
+// group computes on vectors 2k and 2k + 1.  It is copied in the coalesced order
+// (lane k: vectors k and k + 8) and stored with the halves interleaved, vector
+// v at v ^ (v >> 3), so that neither the copies nor the reads of a quarter warp
+// meet in a bank.  The warp's lanes exchange vectors, hence the __syncwarp
+// between a wait and the reads; the same one lets the slots read an iteration
+// ago be overwritten.
+struct Run {
+    uint4 vec[kDepth][kThreads * 2];
+
+    __device__ __forceinline__ void copy(int stage, int tid, const uint4* run) {
+        const int k = tid & 7;
+        uint4* v = vec[stage] + (tid >> 3) * 16;
+        cp_async16(v + k, run + k);
+        cp_async16(v + ((k + 8) ^ 1), run + k + 8);
+    }
+    __device__ __forceinline__ void read(int stage, int tid, float* out) const {
+        const int k = tid & 7, at = 2 * k ^ (k >> 2);
+        const uint4* v = vec[stage] + (tid >> 3) * 16;
+        unpack8(v[at], out);
+        unpack8(v[at ^ 1], out + 8);
+    }
+};
+
+struct SaveSlots {
+    Run g, u;
+    float w[kDepth][kThreads];
+};
+
 template <int FMT, int CKPT>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, 4)
     swiglu_save_kernel(const uint4* __restrict__ x, const float* __restrict__ w,
                        uint4* __restrict__ out, void* __restrict__ sf, SfLayout lay,
                        uint4* __restrict__ ckpt, float* __restrict__ ckpt_sf, int64_t H,
                        int64_t n_groups, int64_t n_walk) {
+    extern __shared__ char shared[];
+    SaveSlots& slots = *reinterpret_cast<SaveSlots*>(shared);
     grid_dependency_launch();
-    const int lane = threadIdx.x & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
     const int sub = lane >> 3, k = lane & 7;
     const int GH = static_cast<int>(H / 128);
     const int64_t units = (n_walk + 3) / 4;
     const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
-    Walk cur(static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5), sub, step, GH);
+    Walk cur(static_cast<int64_t>(blockIdx.x) * kWarps + (tid >> 5), sub, step, GH);
+    Walk next = cur;
+    const auto fetch = [&](int stage) {
+        if (next.u < units && next.g < n_groups) {
+            const uint4* pg = x + next.t * (H / 4) + next.j * 16;
+            slots.g.copy(stage, tid, pg);
+            slots.u.copy(stage, tid, pg + H / 8);
+            if (w) cp_async4(&slots.w[stage][tid], w + next.t);
+        }
+        cp_async_commit();
+        next.next(step);
+    };
     grid_dependency_wait();
-    RawPair in = {};
-    if (cur.u < units && cur.g < n_groups) in.load(x, w, cur.t, cur.j, k, H);
+    for (int d = 0; d < kDepth - 1; ++d) fetch(d);
+    int stage = 0, ahead = kDepth - 1;
     while (cur.u < units) {
+        cp_async_wait(kDepth - 1);
+        __syncwarp();
+        fetch(ahead);
         const int64_t g = cur.g, t = cur.t;
         const int j = cur.j;
         const bool live = g < n_groups;
         float gv[16], uv[16];
-        unpack8(in.g[0], gv);
-        unpack8(in.g[1], gv + 8);
-        unpack8(in.u[0], uv);
-        unpack8(in.u[1], uv + 8);
-        const float wt = in.w;
-        // the next unit's loads go out before this unit's arithmetic
+        slots.g.read(stage, tid, gv);
+        slots.u.read(stage, tid, uv);
+        const float wt = w ? slots.w[stage][tid] : 1.0f;
+        stage = stage + 1 == kDepth ? 0 : stage + 1;
+        ahead = ahead + 1 == kDepth ? 0 : ahead + 1;
         cur.next(step);
-        if (cur.u < units && cur.g < n_groups) in.load(x, w, cur.t, cur.j, k, H);
 
+        uint4* pc = ckpt + t * (H / 8) + j * 8 + k;
         float sg, su;
         const uint4 cg = cast16<CKPT>(gv, sg);
+        if (live) st_stream(pc, cg);
         const uint4 cu = cast16<CKPT>(uv, su);
-        float v[16];
+        if (live) st_stream(pc + H / 16, cu);
 #pragma unroll
         for (int e = 0; e < 16; e += 2) {
-            float2 y = swiglu2(make_float2(gv[e], gv[e + 1]), make_float2(uv[e], uv[e + 1]));
-            if (w) y = mul2(y, make_float2(wt, wt));
-            v[e] = y.x;
-            v[e + 1] = y.y;
+            // the product by 1 of a row without a weight changes nothing
+            const float2 y = mul2(swiglu2(make_float2(gv[e], gv[e + 1]), make_float2(uv[e], uv[e + 1])),
+                                  make_float2(wt, wt));
+            gv[e] = y.x;
+            gv[e + 1] = y.y;
         }
         float sc, inv;
-        group_scale<FMT>(group_max(absmax16(v)), sc, inv);
+        group_scale<FMT>(group_max(absmax16(gv)), sc, inv);
         if (lay.flags & (kSfRoundPow2 | kSfPacked)) pow2_scale(sc, inv);
         if (live) {
-            const uint2 lo = quantize8_mul<FMT>(v, inv), hi = quantize8_mul<FMT>(v + 8, inv);
+            const uint2 lo = quantize8_mul<FMT>(gv, inv), hi = quantize8_mul<FMT>(gv + 8, inv);
             st_stream(out + g * 8 + k, make_uint4(lo.x, lo.y, hi.x, hi.y));
-            uint4* pc = ckpt + t * (H / 8) + j * 8 + k;
-            st_stream(pc, cg);
-            st_stream(pc + H / 16, cu);
         }
         if (k == 0) {
             store_scale(sf, lay, t, live, j, sc);
@@ -141,23 +171,6 @@ __global__ void __launch_bounds__(kThreads, 3)
 // its units of four groups in turn, so that dw[t] is one lane's running sum,
 // five shuffles and, for teams of several warps, one exchange through shared
 // memory, always in the same order.
-struct RestoreIn {
-    uint4 g, u, d[2];
-    float sg, su;
-
-    __device__ __forceinline__ void load(const uint4* ckpt, const float* ckpt_sf, const uint4* dy,
-                                         int64_t t, int j, int k, int64_t H, int GH) {
-        const uint4* pg = ckpt + t * (H / 8) + j * 8 + k;
-        g = ld_stream(pg);
-        u = ld_stream(pg + H / 16);
-        const uint4* pd = dy + t * (H / 8) + j * 16 + k * 2;
-        d[0] = ld_stream(pd);
-        d[1] = ld_stream(pd + 1);
-        sg = ld_ro(ckpt_sf + t * 2 * GH + j);
-        su = ld_ro(ckpt_sf + t * 2 * GH + GH + j);
-    }
-};
-
 template <int CKPT>
 __device__ __forceinline__ void decode16(const uint4& q, float s, float* v) {
     decode4<CKPT>(q.x, v);
@@ -196,84 +209,129 @@ __device__ __forceinline__ void store_grad(void* dx, void* dx_sf, const SfLayout
     }
 }
 
-template <int CKPT, int OUT>
+// One lane's place in its warp's walk: row t and first block u0 of the unit.
+struct RowWalk {
+    int64_t t;
+    int u0;
+    __device__ __forceinline__ void next(int member, int team, int GH, int64_t rows) {
+        u0 += team * 4;
+        if (u0 >= GH) {
+            u0 = member * 4;
+            t += rows;
+        }
+    }
+};
+
+struct RestoreSlots {
+    uint4 code[kDepth][2][kThreads];  // a lane's own codes and scales of g and u
+    float scale[kDepth][2][kThreads];
+    Run dy;
+};
+
+template <int CKPT, int OUT, bool Y>
 __global__ void __launch_bounds__(kThreads, 3)
     swiglu_restore_kernel(const uint4* __restrict__ ckpt, const float* __restrict__ ckpt_sf,
                           const uint4* __restrict__ dy, const float* __restrict__ w,
                           void* __restrict__ dx, void* __restrict__ dx_sf, SfLayout lay,
                           uint4* __restrict__ y, float* __restrict__ dw, int64_t T,
                           int64_t rows_walk, int64_t H, int team) {
+    extern __shared__ char shared[];
+    RestoreSlots& slots = *reinterpret_cast<RestoreSlots*>(shared);
     __shared__ float part[kWarps];
     grid_dependency_launch();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int sub = lane >> 3, k = lane & 7;
     const int GH = static_cast<int>(H / 128);
     const int member = warp & (team - 1);      // the warp's place in its team
     const int teams = kWarps / team;           // rows a CTA takes at a time
+    const int64_t step = static_cast<int64_t>(gridDim.x) * teams;
+    // units of the rows that hold data; a member of a team that is larger than
+    // the row's units has none
+    RowWalk ahead = {static_cast<int64_t>(blockIdx.x) * teams + warp / team, member * 4};
+    if (ahead.u0 >= GH) ahead.t = T;
+    const auto fetch = [&](int stage) {
+        const int j = ahead.u0 + sub;
+        if (ahead.t < T && j < GH) {
+            const uint4* pg = ckpt + ahead.t * (H / 8) + j * 8 + k;
+            cp_async16(&slots.code[stage][0][tid], pg);
+            cp_async16(&slots.code[stage][1][tid], pg + H / 16);
+            slots.dy.copy(stage, tid, dy + ahead.t * (H / 8) + j * 16);
+            const float* ps = ckpt_sf + ahead.t * 2 * GH + j;
+            cp_async4(&slots.scale[stage][0][tid], ps);
+            cp_async4(&slots.scale[stage][1][tid], ps + GH);
+        }
+        cp_async_commit();
+        ahead.next(member, team, GH, step);
+    };
     grid_dependency_wait();
-    for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * teams; t0 < rows_walk;
-         t0 += static_cast<int64_t>(gridDim.x) * teams) {
+    for (int d = 0; d < kDepth - 1; ++d) fetch(d);
+    int stage = 0, free_stage = kDepth - 1;
+    const auto weight = [&](int64_t t) { return w && t < T ? ld_ro(w + t) : 1.0f; };
+    float w_next = weight(static_cast<int64_t>(blockIdx.x) * teams + warp / team);
+    for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * teams; t0 < rows_walk; t0 += step) {
         const int64_t t = t0 + warp / team;
-        float dot = 0.0f;
-        if (t < rows_walk) {
-            const bool row = t < T;
-            const float wt = w && row ? ld_ro(w + t) : 1.0f;
-            for (int u0 = member * 4; u0 < GH; u0 += team * 4) {
-                const int j = u0 + sub;
-                const bool in_row = j < GH, live = row && in_row;
-                RestoreIn in = {};
-                if (live) in.load(ckpt, ckpt_sf, dy, t, j, k, H, GH);
-                float gv[16], uv[16], dv[16];
-                decode16<CKPT>(in.g, in.sg, gv);
-                decode16<CKPT>(in.u, in.su, uv);
-                unpack8(in.d[0], dv);
-                unpack8(in.d[1], dv + 8);
-                float yv[16];
+        const float wt = w_next;
+        w_next = weight(t + step);
+        const bool row = t < T;
+        float2 dot = make_float2(0.0f, 0.0f);
+        for (int u0 = member * 4; u0 < GH; u0 += team * 4) {
+            cp_async_wait(kDepth - 1);
+            __syncwarp();
+            fetch(free_stage);
+            const int j = u0 + sub;
+            const bool in_row = j < GH && t < rows_walk, live = row && j < GH;
+            float gv[16], uv[16], dv[16];
+            if (live) {
+                decode16<CKPT>(slots.code[stage][0][tid], slots.scale[stage][0][tid], gv);
+                decode16<CKPT>(slots.code[stage][1][tid], slots.scale[stage][1][tid], uv);
+                slots.dy.read(stage, tid, dv);
+            } else {
 #pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                    const float2 g = make_float2(gv[e], gv[e + 1]);
-                    const float2 u = make_float2(uv[e], uv[e + 1]);
-                    const float2 d = make_float2(dv[e], dv[e + 1]);
-                    float2 dg, du;
-                    swiglu_grad2(g, u, d, dg, du);
-                    // d silu(g) u is du u
-                    const float2 c = mul2(du, u);
-                    dot += c.x + c.y;
-                    if (y) {
-                        float2 v = swiglu2(g, u);
-                        if (w) v = mul2(v, make_float2(wt, wt));
-                        yv[e] = v.x;
-                        yv[e + 1] = v.y;
-                    }
-                    if (w) {
-                        dg = mul2(dg, make_float2(wt, wt));
-                        du = mul2(du, make_float2(wt, wt));
-                    }
-                    gv[e] = dg.x;
-                    gv[e + 1] = dg.y;
-                    uv[e] = du.x;
-                    uv[e + 1] = du.y;
+                for (int e = 0; e < 16; ++e) gv[e] = uv[e] = dv[e] = 0.0f;
+            }
+            stage = stage + 1 == kDepth ? 0 : stage + 1;
+            free_stage = free_stage + 1 == kDepth ? 0 : free_stage + 1;
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+                const float2 g = make_float2(gv[e], gv[e + 1]);
+                const float2 u = make_float2(uv[e], uv[e + 1]);
+                const float2 d = make_float2(dv[e], dv[e + 1]);
+                const float2 wd = mul2(d, make_float2(wt, wt));
+                float2 silu, dsilu;
+                silu_and_slope2(g, silu, dsilu);
+                const float2 s = mul2(silu, u);
+                dot = fma2(d, s, dot);
+                const float2 dg = mul2(mul2(wd, u), dsilu), du = mul2(wd, silu);
+                gv[e] = dg.x;
+                gv[e + 1] = dg.y;
+                uv[e] = du.x;
+                uv[e + 1] = du.y;
+                if constexpr (Y) {
+                    const float2 v = mul2(s, make_float2(wt, wt));
+                    dv[e] = v.x;
+                    dv[e + 1] = v.y;
                 }
-                store_grad<OUT>(dx, dx_sf, lay, t, j, k, live, in_row, gv);
-                store_grad<OUT>(dx, dx_sf, lay, t, GH + j, k, live, in_row, uv);
-                if (y && live) {
-                    uint4* py = y + t * (H / 8) + j * 16 + k * 2;
-                    st_stream(py, pack8_bf16(yv));
-                    st_stream(py + 1, pack8_bf16(yv + 8));
-                }
+            }
+            store_grad<OUT>(dx, dx_sf, lay, t, j, k, live, in_row, gv);
+            store_grad<OUT>(dx, dx_sf, lay, t, GH + j, k, live, in_row, uv);
+            if (Y && live) {
+                uint4* py = y + t * (H / 8) + j * 16 + k * 2;
+                st_stream(py, pack8_bf16(dv));
+                st_stream(py + 1, pack8_bf16(dv + 8));
             }
         }
         if (dw) {
+            float sum = dot.x + dot.y;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(kAll, dot, o);
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
             if (team > 1) {
                 __syncthreads();  // the sums of the rows before have been read
-                if (lane == 0) part[warp] = dot;
+                if (lane == 0) part[warp] = sum;
                 __syncthreads();
-                dot = 0.0f;
-                for (int i = 0; i < team; ++i) dot += part[warp - member + i];
+                sum = 0.0f;
+                for (int i = 0; i < team; ++i) sum += part[warp - member + i];
             }
-            if (lane == 0 && member == 0 && t < T) st_plain(dw + t, dot);
+            if (lane == 0 && member == 0 && row) st_plain(dw + t, sum);
         }
     }
 }
@@ -304,10 +362,11 @@ cudaError_t launch_swiglu_save(const void* x, const float* w, void* out, void* s
     return with_fmt(fmt, [&](auto f) {
         return with_fmt(ckpt_fmt, [&](auto c) {
             auto* k = &swiglu_save_kernel<decltype(f)::value, decltype(c)::value>;
-            const int grid = persistent_grid(reinterpret_cast<const void*>(k), kThreads, 0,
-                                             ((n_walk + 3) / 4 + kWarps - 1) / kWarps);
+            const int grid = persistent_grid(reinterpret_cast<const void*>(k), kThreads,
+                                             sizeof(SaveSlots), ((n_walk + 3) / 4 + kWarps - 1) / kWarps);
             if (const cudaError_t e = upload_checks(stream)) return e;
-            return launch_pdl(k, grid, kThreads, 0, stream, true, static_cast<const uint4*>(x), w,
+            return launch_pdl(k, grid, kThreads, sizeof(SaveSlots), stream, true,
+                              static_cast<const uint4*>(x), w,
                               static_cast<uint4*>(out), sf, lay, static_cast<uint4*>(ckpt),
                               ckpt_sf, H, n_groups, n_walk);
         });
@@ -320,19 +379,21 @@ cudaError_t launch_swiglu_restore(const void* ckpt, const float* ckpt_sf, const 
                                   unsigned sf_flags, cudaStream_t stream) {
     const SfLayout lay = layout_of(sf_flags, T, 2 * (H / 128));
     const int64_t rows = out_kind != kBf16Out && (sf_flags & kSfColMajor) ? lay.rows4 : T;
-    auto go = [&](auto c, auto o) {
-        auto* k = &swiglu_restore_kernel<decltype(c)::value, decltype(o)::value>;
-        // as many warps a row as it takes to give every SM some, up to its units
-        const int64_t units = (H / 128 + 3) / 4;
-        int team = 1;
-        while (team < kWarps && team < units && rows * team < int64_t{num_sms()} * 3 * kWarps)
-            team *= 2;
-        const int grid = persistent_grid(reinterpret_cast<const void*>(k), kThreads, 0,
+    // as many warps a row as it takes to give every SM some, up to its units
+    const int64_t units = (H / 128 + 3) / 4;
+    int team = 1;
+    while (team < kWarps && team < units && rows * team < int64_t{num_sms()} * 3 * kWarps) team *= 2;
+    const auto launch = [&](auto* k) {
+        const int grid = persistent_grid(reinterpret_cast<const void*>(k), kThreads, sizeof(RestoreSlots),
                                          (rows * team + kWarps - 1) / kWarps);
         if (const cudaError_t e = upload_checks(stream)) return e;
-        return launch_pdl(k, grid, kThreads, 0, stream, true, static_cast<const uint4*>(ckpt),
-                          ckpt_sf, static_cast<const uint4*>(dy), w, dx, dx_sf, lay,
-                          static_cast<uint4*>(y), dw, T, rows, H, team);
+        return launch_pdl(k, grid, kThreads, sizeof(RestoreSlots), stream, true,
+                          static_cast<const uint4*>(ckpt), ckpt_sf, static_cast<const uint4*>(dy),
+                          w, dx, dx_sf, lay, static_cast<uint4*>(y), dw, T, rows, H, team);
+    };
+    const auto go = [&](auto c, auto o) {
+        return y ? launch(&swiglu_restore_kernel<c(), o(), true>)
+                 : launch(&swiglu_restore_kernel<c(), o(), false>);
     };
     return with_fmt(ckpt_fmt, [&](auto c) {
         if (out_kind == kBf16Out) return go(c, std::integral_constant<int, kBf16Out>());

@@ -123,6 +123,36 @@ __device__ __forceinline__ uint4 ld_stream(const uint4* p) {
     return r;
 }
 
+// Asynchronous copies of 16 (not kept in L1) or 4 bytes from global to shared
+// memory, in groups; a thread that reads only what it copied itself needs no
+// barrier, its own wait orders them.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+    if (!access_ok(src, 16, false)) return;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+    if (!access_ok(src, 4, false)) return;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// All but the newest depth - 1 groups have arrived (1 <= depth <= 4).
+__device__ __forceinline__ void cp_async_wait(int depth) {
+    switch (depth) {
+        case 1: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+        case 2: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+        case 3: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+        default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    }
+}
+
 // Read-only loads through the non-coherent path (small per-row operands).
 __device__ __forceinline__ float ld_ro(const float* p) {
     return access_ok(p, 4, false) ? __ldg(p) : 0.0f;
@@ -584,17 +614,22 @@ __device__ __forceinline__ uint32_t clamped_total(uint32_t n) {
 // instead would leave sigma at its smallest normal value, so that dg grew like
 // 2^-126 * g for very negative g.)  Elsewhere the bound changes at most a
 // product that rounded above 1.
-__device__ __forceinline__ void swiglu_grad2(float2 g, float2 u, float2 d, float2& dg,
-                                             float2& du) {
+__device__ __forceinline__ void silu_and_slope2(float2 g, float2& silu, float2& dsilu) {
     const float2 t = mul2(g, make_float2(-1.4426950408889634f, -1.4426950408889634f));
     const float2 e = make_float2(ex2_approx(t.x), ex2_approx(t.y));
     const float2 den = add2(make_float2(1.0f, 1.0f), e);
     const float2 sig = make_float2(rcp_approx(den.x), rcp_approx(den.y));
     const float2 es = mul2(e, sig);
     const float2 one_minus_sig = make_float2(fminf(es.x, 1.0f), fminf(es.y, 1.0f));
-    const float2 dsilu = mul2(sig, fma2(g, one_minus_sig, make_float2(1.0f, 1.0f)));
+    dsilu = mul2(sig, fma2(g, one_minus_sig, make_float2(1.0f, 1.0f)));
+    silu = mul2(g, sig);
+}
+__device__ __forceinline__ void swiglu_grad2(float2 g, float2 u, float2 d, float2& dg,
+                                             float2& du) {
+    float2 silu, dsilu;
+    silu_and_slope2(g, silu, dsilu);
     dg = mul2(mul2(d, u), dsilu);
-    du = mul2(d, mul2(g, sig));
+    du = mul2(d, silu);
 }
 
 // Four bf16 packed in a uint2 -> four floats, element order preserved.
