@@ -191,19 +191,46 @@ __device__ __forceinline__ void put2(float* v, int e, float2 a) {
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
-// Codes of a vector's eight values; a group is half a warp's vectors.
-template <int FMT>
-__device__ __forceinline__ void cast8(const ResidualNorm& a, const SfLayout& lay, int64_t t,
-                                      int vecs, int vec, const float* v) {
-    float m = absmax8(v);
+// Codes and scales of a thread's vectors of ROWS rows; a group is half a warp's
+// vectors of one row.  The lanes of a half warp split the groups they share
+// among them on the way to the maxima, as CtaSum does, so the scales of all of
+// them are computed, and stored, at once; each lane then takes every group's.
+template <int FMT, int ROWS, int NV>
+__device__ __forceinline__ void cast_rows(const ResidualNorm& a, const SfLayout& lay, int64_t t,
+                                          int vecs, const float (&v)[ROWS][NV][8]) {
+    constexpr int kGroups = ROWS * NV, kLanes = 16 / kGroups;  // 1, 2 or 4 groups
+    const int lane = threadIdx.x & 31, half = lane & 15;
+    float m[kGroups];
 #pragma unroll
-    for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+    for (int g = 0; g < kGroups; ++g) m[g] = absmax8(v[g / NV][g % NV]);
+    float s = m[0];
+    if constexpr (kGroups == 2) {
+        const bool hi = lane & 8;
+        s = fmaxf(hi ? m[1] : m[0], __shfl_xor_sync(kAll, hi ? m[0] : m[1], 8));
+    } else if constexpr (kGroups == 4) {
+        const bool hi = lane & 8, up = lane & 4;
+        const float x = fmaxf(hi ? m[2] : m[0], __shfl_xor_sync(kAll, hi ? m[0] : m[2], 8));
+        const float y = fmaxf(hi ? m[3] : m[1], __shfl_xor_sync(kAll, hi ? m[1] : m[3], 8));
+        s = fmaxf(up ? y : x, __shfl_xor_sync(kAll, up ? x : y, 4));
+    }
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) s = fmaxf(s, __shfl_xor_sync(kAll, s, o));
     float sc, inv;
-    group_scale<FMT>(m, sc, inv);
+    group_scale<FMT>(s, sc, inv);
     if (lay.flags & (kSfRoundPow2 | kSfPacked)) pow2_scale(sc, inv);
-    if (vec < vecs) {
-        st_stream(static_cast<uint2*>(a.out) + t * vecs + vec, quantize8<FMT>(v, sc, inv));
-        if ((threadIdx.x & 15) == 0) store_scale(a.sf, lay, t, true, vec / 16, sc);
+    const int mine = half / kLanes;
+    const int64_t row = t + mine / NV;
+    const int at = threadIdx.x + mine % NV * blockDim.x;
+    if (half % kLanes == 0 && row < a.T && at < vecs)
+        store_scale(a.sf, lay, row, true, at / 16, sc);
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+        const int from = (lane & 16) + g * kLanes;
+        const float gs = __shfl_sync(kAll, sc, from), gi = __shfl_sync(kAll, inv, from);
+        const int vec = threadIdx.x + g % NV * blockDim.x;
+        if (vec < vecs && t + g / NV < a.T)
+            st_stream(static_cast<uint2*>(a.out) + (t + g / NV) * vecs + vec,
+                      quantize8<FMT>(v[g / NV][g % NV], gs, gi));
     }
 }
 
@@ -328,9 +355,9 @@ __global__ void __launch_bounds__(kMaxThreads)
         cta_sum(sum, turn);
 #pragma unroll
         for (int k = 0; k < ROWS; ++k) {
-            if (ROWS > 1 && t + k >= a.T) break;
+            const bool row = ROWS == 1 || t + k < a.T;
             const float q = rsqrtf(sum[k] * inv_c + a.eps);
-            if (tid == 0 && a.rstd_pre) st_plain(a.rstd_pre + t + k, q);
+            if (tid == 0 && a.rstd_pre && row) st_plain(a.rstd_pre + t + k, q);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int vec = tid + i * blockDim.x;
@@ -339,15 +366,15 @@ __global__ void __launch_bounds__(kMaxThreads)
                 if (inside(vec)) w_pre.get(i, vec, w);
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) put2(vi, e, mul2(mul2(at2(vi, e), two(q)), at2(w, e)));
-                if (a.x_out && inside(vec))
+                if (a.x_out && row && inside(vec))
                     st_stream(static_cast<uint4*>(a.x_out) + (t + k) * vecs + vec, pack8_bf16(vi));
-                if (!a.out) continue;
-                if (fmt == kFmtE4M3)
-                    cast8<kFmtE4M3>(a, lay, t + k, vecs, vec, vi);
-                else
-                    cast8<kFmtE5M2>(a, lay, t + k, vecs, vec, vi);
             }
         }
+        if (!a.out) continue;
+        if (fmt == kFmtE4M3)
+            cast_rows<kFmtE4M3>(a, lay, t, vecs, v);
+        else
+            cast_rows<kFmtE5M2>(a, lay, t, vecs, v);
     }
 }
 

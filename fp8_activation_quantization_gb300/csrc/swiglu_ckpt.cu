@@ -29,7 +29,12 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kDepth = 3;    // units in flight, the current one among them
+// Units in flight, the current one among them.  Backward, 65536 x 2048: bf16
+// gradients 201 us with two, 186 us with three; FP8 gradients and y 186 us with
+// two, 196 us with three; four are no better for either.
+constexpr int kSaveDepth = 3;
+template <int OUT>
+constexpr int kRestoreDepth = OUT == 2 ? 3 : 2;
 constexpr int kBf16Out = 2;  // in the place of an FP8 format: the gradients leave as bf16
 
 // Largest value of the eight lanes that share a group.
@@ -51,12 +56,36 @@ __device__ __forceinline__ float absmax16(const float* v) {
 // of y.  The next two units are in flight as asynchronous copies into the
 // thread's own slots of shared memory, which costs no registers.
 
-// Codes of one lane's 16 values with the exact quotient, and its group's scale.
+// Scales of two groups (a gate's and an up's) that eight lanes share: lanes
+// 0 - 3 end with the first one's maximum, 4 - 7 with the second's, so one scale
+// is computed for both; a lane then takes both from its two halves.
 template <int FMT>
-__device__ __forceinline__ uint4 cast16(const float* v, float& sc) {
-    float inv;
-    group_scale<FMT>(group_max(absmax16(v)), sc, inv);
+struct TwoScales {
+    float sc, inv;  // this lane's half's
+
+    __device__ __forceinline__ TwoScales(float m0, float m1, int k, bool pow2) {
+        const bool hi = k & 4;
+        float m = fmaxf(hi ? m1 : m0, __shfl_xor_sync(kAll, hi ? m0 : m1, 4));
+        m = fmaxf(m, __shfl_xor_sync(kAll, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(kAll, m, 2));
+        group_scale<FMT>(m, sc, inv);
+        if (pow2) pow2_scale(sc, inv);
+    }
+    static __device__ __forceinline__ float of(float mine, int lane, int which) {
+        return __shfl_sync(kAll, mine, (lane & ~7) + 4 * which);
+    }
+};
+
+// Codes of one lane's 16 values with the exact quotient.
+template <int FMT>
+__device__ __forceinline__ uint4 codes16(const float* v, float sc, float inv) {
     const uint2 lo = quantize8<FMT>(v, sc, inv), hi = quantize8<FMT>(v + 8, sc, inv);
+    return make_uint4(lo.x, lo.y, hi.x, hi.y);
+}
+// Codes of the products by the rounded reciprocal.
+template <int FMT>
+__device__ __forceinline__ uint4 codes16_mul(const float* v, float inv) {
+    const uint2 lo = quantize8_mul<FMT>(v, inv), hi = quantize8_mul<FMT>(v + 8, inv);
     return make_uint4(lo.x, lo.y, hi.x, hi.y);
 }
 
@@ -67,8 +96,9 @@ __device__ __forceinline__ uint4 cast16(const float* v, float& sc) {
 // meet in a bank.  The warp's lanes exchange vectors, hence the __syncwarp
 // between a wait and the reads; the same one lets the slots read an iteration
 // ago be overwritten.
+template <int DEPTH>
 struct Run {
-    uint4 vec[kDepth][kThreads * 2];
+    uint4 vec[DEPTH][kThreads * 2];
 
     __device__ __forceinline__ void copy(int stage, int tid, const uint4* run) {
         const int k = tid & 7;
@@ -85,11 +115,12 @@ struct Run {
 };
 
 struct SaveSlots {
-    Run g, u;
-    float w[kDepth][kThreads];
+    Run<kSaveDepth> g, u;
+    float w[kSaveDepth][kThreads];
 };
 
-template <int FMT, int CKPT>
+// SFX: a scale layout other than row-major fp32.
+template <int FMT, int CKPT, bool SFX>
 __global__ void __launch_bounds__(kThreads, 4)
     swiglu_save_kernel(const uint4* __restrict__ x, const float* __restrict__ w,
                        uint4* __restrict__ out, void* __restrict__ sf, SfLayout lay,
@@ -116,10 +147,10 @@ __global__ void __launch_bounds__(kThreads, 4)
         next.next(step);
     };
     grid_dependency_wait();
-    for (int d = 0; d < kDepth - 1; ++d) fetch(d);
-    int stage = 0, ahead = kDepth - 1;
+    for (int d = 0; d < kSaveDepth - 1; ++d) fetch(d);
+    int stage = 0, ahead = kSaveDepth - 1;
     while (cur.u < units) {
-        cp_async_wait(kDepth - 1);
+        cp_async_wait(kSaveDepth - 1);
         __syncwarp();
         fetch(ahead);
         const int64_t g = cur.g, t = cur.t;
@@ -129,16 +160,17 @@ __global__ void __launch_bounds__(kThreads, 4)
         slots.g.read(stage, tid, gv);
         slots.u.read(stage, tid, uv);
         const float wt = w ? slots.w[stage][tid] : 1.0f;
-        stage = stage + 1 == kDepth ? 0 : stage + 1;
-        ahead = ahead + 1 == kDepth ? 0 : ahead + 1;
+        stage = stage + 1 == kSaveDepth ? 0 : stage + 1;
+        ahead = ahead + 1 == kSaveDepth ? 0 : ahead + 1;
         cur.next(step);
 
         uint4* pc = ckpt + t * (H / 8) + j * 8 + k;
-        float sg, su;
-        const uint4 cg = cast16<CKPT>(gv, sg);
+        const TwoScales<CKPT> own(absmax16(gv), absmax16(uv), k, false);
+        const uint4 cg = codes16<CKPT>(gv, own.of(own.sc, lane, 0), own.of(own.inv, lane, 0));
         if (live) st_stream(pc, cg);
-        const uint4 cu = cast16<CKPT>(uv, su);
+        const uint4 cu = codes16<CKPT>(uv, own.of(own.sc, lane, 1), own.of(own.inv, lane, 1));
         if (live) st_stream(pc + H / 16, cu);
+        if (live && (k & 3) == 0) st_stream(ckpt_sf + t * 2 * GH + j + (k ? GH : 0), own.sc);
 #pragma unroll
         for (int e = 0; e < 16; e += 2) {
             // the product by 1 of a row without a weight changes nothing
@@ -149,17 +181,13 @@ __global__ void __launch_bounds__(kThreads, 4)
         }
         float sc, inv;
         group_scale<FMT>(group_max(absmax16(gv)), sc, inv);
-        if (lay.flags & (kSfRoundPow2 | kSfPacked)) pow2_scale(sc, inv);
-        if (live) {
-            const uint2 lo = quantize8_mul<FMT>(gv, inv), hi = quantize8_mul<FMT>(gv + 8, inv);
-            st_stream(out + g * 8 + k, make_uint4(lo.x, lo.y, hi.x, hi.y));
-        }
+        if (SFX && (lay.flags & (kSfRoundPow2 | kSfPacked))) pow2_scale(sc, inv);
+        if (live) st_stream(out + g * 8 + k, codes16_mul<FMT>(gv, inv));
         if (k == 0) {
-            store_scale(sf, lay, t, live, j, sc);
-            if (live) {
-                st_stream(ckpt_sf + t * 2 * GH + j, sg);
-                st_stream(ckpt_sf + t * 2 * GH + GH + j, su);
-            }
+            if constexpr (SFX)
+                store_scale(sf, lay, t, live, j, sc);
+            else if (live)
+                st_stream(static_cast<float*>(sf) + g, sc);
         }
     }
 }
@@ -185,28 +213,16 @@ __device__ __forceinline__ void decode16(const uint4& q, float s, float* v) {
     }
 }
 
-// One half of the gradients (16 values of a lane): bf16, or cast per token.
-// `live`: the group holds data; `owned`: its scale is this launch's to write
-// (data, or the padding rows of the column-major layouts).
-template <int OUT>
-__device__ __forceinline__ void store_grad(void* dx, void* dx_sf, const SfLayout& lay, int64_t t,
-                                           int j, int k, bool live, bool owned, const float* v) {
-    if constexpr (OUT == kBf16Out) {
-        if (!live) return;
-        uint4* p = static_cast<uint4*>(dx) + (t * lay.groups + j) * 16 + k * 2;
-        st_stream(p, pack8_bf16(v));
-        st_stream(p + 1, pack8_bf16(v + 8));
-    } else {
-        float sc, inv;
-        group_scale<OUT>(group_max(absmax16(v)), sc, inv);
-        if (lay.flags & (kSfRoundPow2 | kSfPacked)) pow2_scale(sc, inv);
-        if (live) {
-            const uint2 lo = quantize8_mul<OUT>(v, inv), hi = quantize8_mul<OUT>(v + 8, inv);
-            st_stream(static_cast<uint4*>(dx) + (t * lay.groups + j) * 8 + k,
-                      make_uint4(lo.x, lo.y, hi.x, hi.y));
-        }
-        if (k == 0 && owned) store_scale(dx_sf, lay, t, live, j, sc);
-    }
+// silu(g) and its slope s (1 + g (1 - s)) = s + silu(g) (1 - s) for two values.
+// 1 - s is taken as it stands: it is exact for g << 0, and for g > 0 its
+// rounding adds at most |g| u to a slope near 1.
+__device__ __forceinline__ void silu_and_slope2(float2 g, float2& silu, float2& slope) {
+    const float2 t = mul2(g, make_float2(-1.4426950408889634f, -1.4426950408889634f));
+    const float2 den = add2(make_float2(1.0f, 1.0f), make_float2(ex2_approx(t.x), ex2_approx(t.y)));
+    const float2 s = make_float2(rcp_approx(den.x), rcp_approx(den.y));
+    silu = mul2(g, s);
+    const float2 rest = fma2(s, make_float2(-1.0f, -1.0f), make_float2(1.0f, 1.0f));
+    slope = fma2(silu, rest, s);
 }
 
 // One lane's place in its warp's walk: row t and first block u0 of the unit.
@@ -222,13 +238,14 @@ struct RowWalk {
     }
 };
 
+template <int DEPTH>
 struct RestoreSlots {
-    uint4 code[kDepth][2][kThreads];  // a lane's own codes and scales of g and u
-    float scale[kDepth][2][kThreads];
-    Run dy;
+    uint4 code[DEPTH][2][kThreads];  // a lane's own codes and scales of g and u
+    float scale[DEPTH][2][kThreads];
+    Run<DEPTH> dy;
 };
 
-template <int CKPT, int OUT, bool Y>
+template <int CKPT, int OUT, bool Y, bool SFX>
 __global__ void __launch_bounds__(kThreads, 3)
     swiglu_restore_kernel(const uint4* __restrict__ ckpt, const float* __restrict__ ckpt_sf,
                           const uint4* __restrict__ dy, const float* __restrict__ w,
@@ -236,7 +253,8 @@ __global__ void __launch_bounds__(kThreads, 3)
                           uint4* __restrict__ y, float* __restrict__ dw, int64_t T,
                           int64_t rows_walk, int64_t H, int team) {
     extern __shared__ char shared[];
-    RestoreSlots& slots = *reinterpret_cast<RestoreSlots*>(shared);
+    constexpr int kDepth = kRestoreDepth<OUT>;
+    auto& slots = *reinterpret_cast<RestoreSlots<kDepth>*>(shared);
     __shared__ float part[kWarps];
     grid_dependency_launch();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -252,11 +270,13 @@ __global__ void __launch_bounds__(kThreads, 3)
     const auto fetch = [&](int stage) {
         const int j = ahead.u0 + sub;
         if (ahead.t < T && j < GH) {
-            const uint4* pg = ckpt + ahead.t * (H / 8) + j * 8 + k;
+            // a row of codes, and one of dy, is H / 8 pieces, one of scales H / 64
+            const int64_t row = ahead.t * (H / 8);
+            const uint4* pg = ckpt + row + (j * 8 + k);
             cp_async16(&slots.code[stage][0][tid], pg);
             cp_async16(&slots.code[stage][1][tid], pg + H / 16);
-            slots.dy.copy(stage, tid, dy + ahead.t * (H / 8) + j * 16);
-            const float* ps = ckpt_sf + ahead.t * 2 * GH + j;
+            slots.dy.copy(stage, tid, dy + row + j * 16);
+            const float* ps = ckpt_sf + (row >> 3) + j;
             cp_async4(&slots.scale[stage][0][tid], ps);
             cp_async4(&slots.scale[stage][1][tid], ps + GH);
         }
@@ -274,50 +294,74 @@ __global__ void __launch_bounds__(kThreads, 3)
         w_next = weight(t + step);
         const bool row = t < T;
         float2 dot = make_float2(0.0f, 0.0f);
+        // the row's first piece of codes (and of y), and of bf16 gradients
+        const int64_t row_at = t * (H / 8);
         for (int u0 = member * 4; u0 < GH; u0 += team * 4) {
             cp_async_wait(kDepth - 1);
             __syncwarp();
             fetch(free_stage);
             const int j = u0 + sub;
             const bool in_row = j < GH && t < rows_walk, live = row && j < GH;
+            // a group without data computes on what its slots hold; nothing of it is used
             float gv[16], uv[16], dv[16];
-            if (live) {
-                decode16<CKPT>(slots.code[stage][0][tid], slots.scale[stage][0][tid], gv);
-                decode16<CKPT>(slots.code[stage][1][tid], slots.scale[stage][1][tid], uv);
-                slots.dy.read(stage, tid, dv);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) gv[e] = uv[e] = dv[e] = 0.0f;
-            }
+            decode16<CKPT>(slots.code[stage][0][tid], slots.scale[stage][0][tid], gv);
+            decode16<CKPT>(slots.code[stage][1][tid], slots.scale[stage][1][tid], uv);
+            slots.dy.read(stage, tid, dv);
             stage = stage + 1 == kDepth ? 0 : stage + 1;
             free_stage = free_stage + 1 == kDepth ? 0 : free_stage + 1;
+            float2 unit_dot = make_float2(0.0f, 0.0f);
+            [[maybe_unused]] uint32_t yv[8];
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
                 const float2 g = make_float2(gv[e], gv[e + 1]);
                 const float2 u = make_float2(uv[e], uv[e + 1]);
                 const float2 d = make_float2(dv[e], dv[e + 1]);
                 const float2 wd = mul2(d, make_float2(wt, wt));
-                float2 silu, dsilu;
-                silu_and_slope2(g, silu, dsilu);
+                float2 silu, slope;
+                silu_and_slope2(g, silu, slope);
                 const float2 s = mul2(silu, u);
-                dot = fma2(d, s, dot);
-                const float2 dg = mul2(mul2(wd, u), dsilu), du = mul2(wd, silu);
+                unit_dot = fma2(d, s, unit_dot);
+                const float2 dg = mul2(mul2(wd, u), slope), du = mul2(wd, silu);
                 gv[e] = dg.x;
                 gv[e + 1] = dg.y;
                 uv[e] = du.x;
                 uv[e + 1] = du.y;
                 if constexpr (Y) {
                     const float2 v = mul2(s, make_float2(wt, wt));
-                    dv[e] = v.x;
-                    dv[e + 1] = v.y;
+                    yv[e / 2] = pack_bf16x2(v.x, v.y);
                 }
             }
-            store_grad<OUT>(dx, dx_sf, lay, t, j, k, live, in_row, gv);
-            store_grad<OUT>(dx, dx_sf, lay, t, GH + j, k, live, in_row, uv);
+            if (live) dot = add2(dot, unit_dot);
             if (Y && live) {
-                uint4* py = y + t * (H / 8) + j * 16 + k * 2;
-                st_stream(py, pack8_bf16(dv));
-                st_stream(py + 1, pack8_bf16(dv + 8));
+                uint4* py = y + row_at + (j * 16 + k * 2);
+                st_stream(py, make_uint4(yv[0], yv[1], yv[2], yv[3]));
+                st_stream(py + 1, make_uint4(yv[4], yv[5], yv[6], yv[7]));
+            }
+            if constexpr (OUT == kBf16Out) {
+                if (live) {
+                    uint4* p = static_cast<uint4*>(dx) + 2 * row_at + (j * 16 + k * 2);
+                    st_stream(p, pack8_bf16(gv));
+                    st_stream(p + 1, pack8_bf16(gv + 8));
+                    st_stream(p + H / 8, pack8_bf16(uv));
+                    st_stream(p + H / 8 + 1, pack8_bf16(uv + 8));
+                }
+            } else {
+                const TwoScales<OUT> two(absmax16(gv), absmax16(uv), k,
+                                         SFX && (lay.flags & (kSfRoundPow2 | kSfPacked)));
+                const uint4 cg = codes16_mul<OUT>(gv, two.of(two.inv, lane, 0));
+                const uint4 cu = codes16_mul<OUT>(uv, two.of(two.inv, lane, 1));
+                if (live) {
+                    uint4* p = static_cast<uint4*>(dx) + row_at + (j * 8 + k);
+                    st_stream(p, cg);
+                    st_stream(p + H / 16, cu);
+                }
+                if ((k & 3) == 0 && in_row) {
+                    const int group = j + (k ? GH : 0);
+                    if constexpr (SFX)
+                        store_scale(dx_sf, lay, t, live, group, two.sc);
+                    else if (live)
+                        st_stream(static_cast<float*>(dx_sf) + (row_at >> 3) + group, two.sc);
+                }
             }
         }
         if (dw) {
@@ -359,16 +403,18 @@ cudaError_t launch_swiglu_save(const void* x, const float* w, void* out, void* s
     const SfLayout lay = layout_of(sf_flags, T, H / 128);
     const int64_t n_groups = T * lay.groups;
     const int64_t n_walk = (sf_flags & kSfColMajor) ? lay.rows4 * lay.groups : n_groups;
+    const auto launch = [&](auto* k) {
+        const int grid = persistent_grid(reinterpret_cast<const void*>(k), kThreads,
+                                         sizeof(SaveSlots), ((n_walk + 3) / 4 + kWarps - 1) / kWarps);
+        if (const cudaError_t e = upload_checks(stream)) return e;
+        return launch_pdl(k, grid, kThreads, sizeof(SaveSlots), stream, true,
+                          static_cast<const uint4*>(x), w, static_cast<uint4*>(out), sf, lay,
+                          static_cast<uint4*>(ckpt), ckpt_sf, H, n_groups, n_walk);
+    };
     return with_fmt(fmt, [&](auto f) {
         return with_fmt(ckpt_fmt, [&](auto c) {
-            auto* k = &swiglu_save_kernel<decltype(f)::value, decltype(c)::value>;
-            const int grid = persistent_grid(reinterpret_cast<const void*>(k), kThreads,
-                                             sizeof(SaveSlots), ((n_walk + 3) / 4 + kWarps - 1) / kWarps);
-            if (const cudaError_t e = upload_checks(stream)) return e;
-            return launch_pdl(k, grid, kThreads, sizeof(SaveSlots), stream, true,
-                              static_cast<const uint4*>(x), w,
-                              static_cast<uint4*>(out), sf, lay, static_cast<uint4*>(ckpt),
-                              ckpt_sf, H, n_groups, n_walk);
+            return sf_flags & ~kQReciprocal ? launch(&swiglu_save_kernel<f(), c(), true>)
+                                            : launch(&swiglu_save_kernel<f(), c(), false>);
         });
     });
 }
@@ -383,17 +429,22 @@ cudaError_t launch_swiglu_restore(const void* ckpt, const float* ckpt_sf, const 
     const int64_t units = (H / 128 + 3) / 4;
     int team = 1;
     while (team < kWarps && team < units && rows * team < int64_t{num_sms()} * 3 * kWarps) team *= 2;
-    const auto launch = [&](auto* k) {
-        const int grid = persistent_grid(reinterpret_cast<const void*>(k), kThreads, sizeof(RestoreSlots),
+    const auto launch = [&](auto* k, size_t smem) {
+        const int grid = persistent_grid(reinterpret_cast<const void*>(k), kThreads, smem,
                                          (rows * team + kWarps - 1) / kWarps);
         if (const cudaError_t e = upload_checks(stream)) return e;
-        return launch_pdl(k, grid, kThreads, sizeof(RestoreSlots), stream, true,
+        return launch_pdl(k, grid, kThreads, smem, stream, true,
                           static_cast<const uint4*>(ckpt), ckpt_sf, static_cast<const uint4*>(dy),
                           w, dx, dx_sf, lay, static_cast<uint4*>(y), dw, T, rows, H, team);
     };
     const auto go = [&](auto c, auto o) {
-        return y ? launch(&swiglu_restore_kernel<c(), o(), true>)
-                 : launch(&swiglu_restore_kernel<c(), o(), false>);
+        constexpr size_t smem = sizeof(RestoreSlots<kRestoreDepth<o()>>);
+        if constexpr (o() != kBf16Out)
+            if (sf_flags & ~kQReciprocal)
+                return y ? launch(&swiglu_restore_kernel<c(), o(), true, true>, smem)
+                         : launch(&swiglu_restore_kernel<c(), o(), false, true>, smem);
+        return y ? launch(&swiglu_restore_kernel<c(), o(), true, false>, smem)
+                 : launch(&swiglu_restore_kernel<c(), o(), false, false>, smem);
     };
     return with_fmt(ckpt_fmt, [&](auto c) {
         if (out_kind == kBf16Out) return go(c, std::integral_constant<int, kBf16Out>());

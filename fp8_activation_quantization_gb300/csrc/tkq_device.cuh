@@ -614,22 +614,17 @@ __device__ __forceinline__ uint32_t clamped_total(uint32_t n) {
 // instead would leave sigma at its smallest normal value, so that dg grew like
 // 2^-126 * g for very negative g.)  Elsewhere the bound changes at most a
 // product that rounded above 1.
-__device__ __forceinline__ void silu_and_slope2(float2 g, float2& silu, float2& dsilu) {
+__device__ __forceinline__ void swiglu_grad2(float2 g, float2 u, float2 d, float2& dg,
+                                             float2& du) {
     const float2 t = mul2(g, make_float2(-1.4426950408889634f, -1.4426950408889634f));
     const float2 e = make_float2(ex2_approx(t.x), ex2_approx(t.y));
     const float2 den = add2(make_float2(1.0f, 1.0f), e);
     const float2 sig = make_float2(rcp_approx(den.x), rcp_approx(den.y));
     const float2 es = mul2(e, sig);
     const float2 one_minus_sig = make_float2(fminf(es.x, 1.0f), fminf(es.y, 1.0f));
-    dsilu = mul2(sig, fma2(g, one_minus_sig, make_float2(1.0f, 1.0f)));
-    silu = mul2(g, sig);
-}
-__device__ __forceinline__ void swiglu_grad2(float2 g, float2 u, float2 d, float2& dg,
-                                             float2& du) {
-    float2 silu, dsilu;
-    silu_and_slope2(g, silu, dsilu);
+    const float2 dsilu = mul2(sig, fma2(g, one_minus_sig, make_float2(1.0f, 1.0f)));
     dg = mul2(mul2(d, u), dsilu);
-    du = mul2(d, silu);
+    du = mul2(d, mul2(g, sig));
 }
 
 // Four bf16 packed in a uint2 -> four floats, element order preserved.
