@@ -32,16 +32,15 @@ namespace tkq {
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kMaxThreads = 512;
 
-constexpr int kMaxWarps = kMaxThreads / 32;
 
 // Sums of N values over the CTA, in the same order each time.  The lanes first
 // split the values among them (half of a pair to each half of the warp), so
 // that N values take log2(N) steps more than one, not N times as many.  Two
 // buffers in turn: a thread past the barrier of one sum has read the sum before.
-template <int N>
+template <int N, int THREADS>
 struct CtaSum {
+    static constexpr int kMaxWarps = THREADS / 32;
     static constexpr int kPad = N == 1 ? 1 : N == 2 ? 2 : 4;  // values, lanes of one: 32 / kPad
     static constexpr int kLanes = 32 / kPad;
     float buf[2][kPad][kMaxWarps];
@@ -140,11 +139,11 @@ __device__ __forceinline__ void weights8(const float* w, int vec, float scale, f
     v[4] = b.x * scale; v[5] = b.y * scale; v[6] = b.z * scale; v[7] = b.w * scale;
 }
 
-// A thread's weights: kept in registers for all its rows where they fit (up to
-// two vectors a thread), else read again for each row.
-template <int NV>
+// A thread's weights: kept in registers for all its rows where they fit (KEPT),
+// else read again for each row.
+template <int NV, bool KEPT>
 struct Weights {
-    static constexpr bool kKept = NV <= 2;
+    static constexpr bool kKept = KEPT;
     float kept[kKept ? NV : 1][8];
     const float* w;
     float scale;
@@ -234,16 +233,28 @@ __device__ __forceinline__ void cast_rows(const ResidualNorm& a, const SfLayout&
     }
 }
 
+// Three ways to hold a row, by its width (measured at T C = 59 - 67 million,
+// bf16 stream, post-norm, gate and cast):
+//   up to 4096 channels   one vector a thread, 64 registers, 1024 threads an SM:
+//                         4096: 101 us, 159 us with the 128 registers below (one
+//                         CTA an SM); 1024: 51 us, 58 us
+//   up to 8192            two vectors, 128 registers: 7168: 88 us, 95 us with one
+//                         vector and 896 threads; 5120: 73 us, 76 us
+//   up to 16384           two vectors, 64 registers, the weights read again for
+//                         each row: 16384: 137 us, 148 us with four and 512 threads
+template <int NV, bool KEPT>
+constexpr int kForwardThreads = NV == 2 && KEPT ? 512 : 1024;
+
 // ROWS consecutive rows are taken at a time, so that their reductions share the
 // barriers and the shuffles, and one row's arithmetic covers the other's
 // latencies.  WHOLE: there is a block and a pre-norm, and the row is exactly
 // the CTA's vectors, so nothing of that is asked again for each vector.
-template <int NV, bool F32, bool POST, bool GATE, int ROWS, bool WHOLE>
-__global__ void __launch_bounds__(kMaxThreads)
+template <int NV, bool KEPT, bool F32, bool POST, bool GATE, int ROWS, bool WHOLE>
+__global__ void __launch_bounds__(kForwardThreads<NV, KEPT>)
     residual_norm_kernel(const ResidualNorm a, const SfLayout lay, int64_t rows_walk, int fmt,
                          Fifo q8) {
     extern __shared__ uint4 fifo[];
-    __shared__ CtaSum<ROWS> cta_sum;
+    __shared__ CtaSum<ROWS, kForwardThreads<NV, KEPT>> cta_sum;
     grid_dependency_launch();
     constexpr int kR = F32 ? 2 : 1;   // slots of r; then h, gate
     int turn = 0;
@@ -273,7 +284,7 @@ __global__ void __launch_bounds__(kMaxThreads)
     const int64_t start = static_cast<int64_t>(blockIdx.x) * ROWS;
     grid_dependency_wait();
     for (int d = 0; d < q8.depth - 1; ++d) fetch_rows(start + d * step, d);
-    Weights<NV> w_post, w_pre;
+    Weights<NV, KEPT> w_post, w_pre;
     w_post.init(a.w_post, a.res_scale, vecs);
     w_pre.init(a.w_pre, 1.0f, vecs);
     int stage = 0, ahead = q8.depth - 1;
@@ -391,14 +402,17 @@ __global__ void __launch_bounds__(kMaxThreads)
 // gradients are summed over a CTA's rows in registers and written as one
 // partial row a CTA; sum_parts_kernel adds them up in order.
 // WHOLE: dr', dx and h are given and the row is exactly the CTA's vectors.
+// 128 registers a thread: capped at 96 (640 threads) the kernel took 228 us instead
+// of 172 us at 16384 x 4096.
+constexpr int kBackwardThreads = 512;
 template <int NV, bool F32, bool POST, bool GATE, bool WHOLE>
-__global__ void __launch_bounds__(kMaxThreads)
+__global__ void __launch_bounds__(kBackwardThreads)
     residual_norm_backward_kernel(const ResidualNormGrad a, Fifo q8) {
     extern __shared__ uint4 fifo[];
-    __shared__ CtaSum<POST ? 3 : 1> cta_sum;
+    __shared__ CtaSum<POST ? 3 : 1, kBackwardThreads> cta_sum;
     grid_dependency_launch();
     constexpr int kS = F32 ? 2 : 1;   // slots of a stream: h, gate, dr, dx, r
-    constexpr bool kKept = Weights<NV>::kKept;
+    constexpr bool kKept = NV <= 2;
     const bool has_dr = WHOLE || a.dr, has_dx = WHOLE || a.dx, has_h = WHOLE || a.h;
     int turn = 0;
     const int tid = threadIdx.x, vecs = static_cast<int>(a.C / 8);
@@ -441,7 +455,7 @@ __global__ void __launch_bounds__(kMaxThreads)
     grid_dependency_wait();
     for (int d = 0; d < q8.depth - 1; ++d)
         fetch_row(blockIdx.x + static_cast<int64_t>(d) * gridDim.x, d);
-    Weights<NV> w_post, w_pre;
+    Weights<NV, kKept> w_post, w_pre;
     w_post.init(a.w_post, a.res_scale, vecs);
     w_pre.init(a.w_pre, 1.0f, vecs);
     float p_next = 1.0f, q_next = 0.0f;
@@ -610,50 +624,51 @@ __global__ void __launch_bounds__(kSumCols* kSumSlices)
 }
 
 // Vectors a thread holds, threads a CTA and stages in flight for rows of C
-// channels of `slots` 16-byte pieces a vector, `rows` at a time: CTAs of at most
-// 512 threads (128 registers), about 768 threads an SM, which share 224 KB of
-// shared memory for up to four stages each.
+// channels of `slots` 16-byte pieces a vector, `rows` at a time.  The CTAs that an
+// SM's registers hold (`threads_per_sm`) share 224 KB of shared memory for up to
+// four stages each; rather than less than two stages there are fewer CTAs.
 struct Shape {
-    int nv, threads;
+    int threads;
     bool exact;  // the row is exactly the CTA's vectors
     size_t smem;
     Fifo fifo;
 };
 constexpr size_t kSmemPerSm = 224 * 1024;
-constexpr int kThreadsPerSm = 768;
-Shape shape_of(int64_t C, int slots, int rows) {
+Shape shape_of(int64_t C, int nv, int threads_per_sm, int slots, int rows) {
     Shape s;
     const int vecs = static_cast<int>(C / 8);
-    s.nv = vecs <= kMaxThreads ? 1 : vecs <= 2 * kMaxThreads ? 2 : 4;
-    s.threads = ((vecs + s.nv - 1) / s.nv + 31) / 32 * 32;
-    s.exact = vecs == s.nv * s.threads;
-    const size_t row = static_cast<size_t>(slots) * vecs * 16 * rows;
-    const size_t ctas = kThreadsPerSm / s.threads < 16 ? kThreadsPerSm / s.threads : 16;
-    size_t depth = ctas ? kSmemPerSm / (row * ctas) : 0;
-    if (depth < 2) depth = kSmemPerSm / row >= 2 ? 2 : 1;
-    if (depth > kMaxDepth) depth = kMaxDepth;
+    s.threads = ((vecs + nv - 1) / nv + 31) / 32 * 32;
+    s.exact = vecs == nv * s.threads;
+    const size_t stage = static_cast<size_t>(slots) * vecs * 16 * rows;
+    int ctas = threads_per_sm / s.threads;
+    ctas = ctas < 1 ? 1 : ctas > 16 ? 16 : ctas;
+    while (ctas > 1 && kSmemPerSm / (stage * ctas) < 2) --ctas;
+    size_t depth = kSmemPerSm / (stage * ctas);
+    depth = depth < 1 ? 1 : depth > kMaxDepth ? kMaxDepth : depth;
     s.fifo = {static_cast<int>(depth), slots};
-    s.smem = depth * row;
+    s.smem = depth * stage;
     return s;
 }
 
-// The instance for the vectors a thread, the stream's type, and whether there
-// are a post-norm and a gate.
 template <typename F>
-cudaError_t with_instance(int nv, bool f32, bool post, bool gate, F&& f) {
-    const auto flag = [](bool b, auto&& g) {
-        return b ? g(std::true_type()) : g(std::false_type());
-    };
-    return flag(f32, [&](auto f32_) {
-        return flag(post, [&](auto post_) {
-            return flag(gate, [&](auto gate_) {
-                if (nv == 1) return f(std::integral_constant<int, 1>(), f32_, post_, gate_);
-                if (nv == 2) return f(std::integral_constant<int, 2>(), f32_, post_, gate_);
-                return f(std::integral_constant<int, 4>(), f32_, post_, gate_);
-            });
+cudaError_t with_flag(bool b, F&& f) {
+    return b ? f(std::true_type()) : f(std::false_type());
+}
+// The instance for the stream's type and whether there are a post-norm and a gate.
+template <typename F>
+cudaError_t with_options(bool f32, bool post, bool gate, F&& f) {
+    return with_flag(f32, [&](auto f32_) {
+        return with_flag(post, [&](auto post_) {
+            return with_flag(gate, [&](auto gate_) { return f(f32_, post_, gate_); });
         });
     });
 }
+
+int backward_nv(int64_t C) {
+    const int64_t vecs = C / 8;
+    return vecs <= kBackwardThreads ? 1 : vecs <= 2 * kBackwardThreads ? 2 : 4;
+}
+constexpr int kBackwardThreadsPerSm = 768;  // below 4096 channels, of about 80 registers
 
 }  // namespace
 
@@ -666,55 +681,65 @@ cudaError_t launch_residual_norm(const ResidualNorm& a, int fmt, unsigned sf_fla
     lay.rows4 = (a.T + 3) / 4 * 4;
     const int64_t rows = a.out && (sf_flags & kSfColMajor) ? lay.rows4 : a.T;
     const int slots = (a.r_f32 ? 2 : 1) + (a.h ? 1 : 0) + (a.gate ? 1 : 0);
-    const auto launch = [&](auto* k, int rows_at_once) {
-        const Shape s = shape_of(a.C, slots, rows_at_once);
+    const int nv = a.C <= 4096 ? 1 : 2;
+    const bool kept = a.C <= 8192;
+    const int per_sm = nv == 1 ? kForwardThreads<1, true>
+                       : kept  ? kForwardThreads<2, true>
+                               : kForwardThreads<2, false>;
+    const Shape one = shape_of(a.C, nv, per_sm, slots, 1);
+    const Shape pair = shape_of(a.C, nv, per_sm, slots, 2);
+    const auto launch = [&](auto* k, const Shape& s, int rows_at_once) {
         const int grid = persistent_grid(reinterpret_cast<const void*>(k), s.threads, s.smem,
                                          (rows + rows_at_once - 1) / rows_at_once);
         if (const cudaError_t e = upload_checks(stream)) return e;
         return launch_pdl(k, grid, s.threads, s.smem, stream, true, a, lay, rows, fmt, s.fifo);
     };
-    const Shape s = shape_of(a.C, slots, 1);
-    return with_instance(s.nv, a.r_f32, a.post, a.gate, [&](auto nv, auto f32, auto post, auto gate) {
-        if constexpr (nv() <= 2) {
-            if (s.exact && a.h && a.pre) {
+    return with_options(a.r_f32, a.post, a.gate, [&](auto f32, auto post, auto gate) {
+        if (!kept)
+            return launch(&residual_norm_kernel<2, false, f32(), post(), gate(), 1, false>, one, 1);
+        return with_flag(nv == 2, [&](auto wide) {
+            return with_flag(one.exact && a.h && a.pre, [&](auto whole) {
+                constexpr int n = wide() ? 2 : 1;
                 // two rows at a time once every SM has work for that and the next two fit
-                if (a.T >= 4 * int64_t{num_sms()} && shape_of(a.C, slots, 2).fifo.depth >= 2)
-                    return launch(&residual_norm_kernel<nv(), f32(), post(), gate(), 2, true>, 2);
-                return launch(&residual_norm_kernel<nv(), f32(), post(), gate(), 1, true>, 1);
-            }
-        }
-        return launch(&residual_norm_kernel<nv(), f32(), post(), gate(), 1, false>, 1);
+                if (a.T >= 4 * int64_t{num_sms()} && pair.fifo.depth >= 2)
+                    return launch(
+                        &residual_norm_kernel<n, true, f32(), post(), gate(), 2, whole()>, pair, 2);
+                return launch(&residual_norm_kernel<n, true, f32(), post(), gate(), 1, whole()>, one,
+                              1);
+            });
+        });
     });
 }
 
 // Partial rows a backward launch writes at most: one a CTA, as many CTAs an SM
 // as its threads allow, no more than rows.
 int64_t residual_norm_parts(int64_t T, int64_t C) {
-    const int64_t per_sm = 2 * kMaxThreads / shape_of(C, 1, 1).threads;
+    const int nv = backward_nv(C);
+    const int64_t per_sm = 2 * kBackwardThreads / shape_of(C, nv, kBackwardThreadsPerSm, 1, 1).threads;
     const int64_t most = num_sms() * (per_sm < 16 ? per_sm : 16);
     return T < most ? T : most;
 }
 
 cudaError_t launch_residual_norm_backward(const ResidualNormGrad& a, cudaStream_t stream) {
     const int slot = a.r_f32 ? 2 : 1;
-    const Shape s = shape_of(a.C, (a.dr ? slot : 0) + (a.dx ? 1 + slot : 0) + (a.h ? 1 : 0) +
-                                      (a.gate ? 1 : 0), 1);
+    const int slots = (a.dr ? slot : 0) + (a.dx ? 1 + slot : 0) + (a.h ? 1 : 0) + (a.gate ? 1 : 0);
+    const int nv = backward_nv(a.C);
+    const Shape s = shape_of(a.C, nv, kBackwardThreadsPerSm, slots, 1);
     int parts = 0;
-    const cudaError_t e =
-        with_instance(s.nv, a.r_f32, a.post, a.gate, [&](auto nv, auto f32, auto post, auto gate) {
-            const auto launch = [&](auto* k) {
-                parts = persistent_grid(reinterpret_cast<const void*>(k), s.threads, s.smem,
-                                        residual_norm_parts(a.T, a.C));
-                if (const cudaError_t e = upload_checks(stream)) return e;
-                return launch_pdl(k, parts, s.threads, s.smem, stream, true, a, s.fifo);
-            };
-            if constexpr (nv() <= 2) {
-                if (s.exact && a.dr && a.dx && a.h)
-                    return launch(
-                        &residual_norm_backward_kernel<nv(), f32(), post(), gate(), true>);
-            }
-            return launch(&residual_norm_backward_kernel<nv(), f32(), post(), gate(), false>);
+    const auto launch = [&](auto* k) {
+        parts = persistent_grid(reinterpret_cast<const void*>(k), s.threads, s.smem,
+                                residual_norm_parts(a.T, a.C));
+        if (const cudaError_t e = upload_checks(stream)) return e;
+        return launch_pdl(k, parts, s.threads, s.smem, stream, true, a, s.fifo);
+    };
+    const cudaError_t e = with_options(a.r_f32, a.post, a.gate, [&](auto f32, auto post, auto gate) {
+        if (nv == 4) return launch(&residual_norm_backward_kernel<4, f32(), post(), gate(), false>);
+        return with_flag(s.exact && a.dr && a.dx && a.h, [&](auto whole) {
+            if (nv == 2)
+                return launch(&residual_norm_backward_kernel<2, f32(), post(), gate(), whole()>);
+            return launch(&residual_norm_backward_kernel<1, f32(), post(), gate(), whole()>);
         });
+    });
     if (e != cudaSuccess || (!a.dw_pre && !a.dw_post)) return e;
     return launch_pdl(&sum_parts_kernel, static_cast<int>(a.C / (2 * kSumCols)),
                       kSumCols * kSumSlices, 0, stream, true,
