@@ -18,10 +18,13 @@
 // without any expert is all -1.  A logit of +inf counts as the largest finite
 // number, which keeps exp(x - m) defined.
 //
-// One warp per token, the logits in registers (lane l holds experts l, l + 32,
-// ...).  All maxima are taken on order-preserving integer images of the floats
-// by the warp's integer reduction, so the choice is exact and does not depend
-// on any order of evaluation.
+// One warp per token, the logits in registers: lane l holds the SLOTS experts
+// from l * SLOTS on, so a lower lane holds lower indices and a group of experts
+// is a run of lanes.  Both directions are bound by instructions, not memory
+// (16384 x 256 fp32 is 2.7 us of reads): the choice is therefore made in two
+// steps.  The k-th largest of the 32 lanes' maxima, found by k reductions, bounds
+// the k-th largest key from below; the few keys that reach it are gathered, one
+// a lane, and ranked by counting.
 #include <type_traits>
 
 #include <cuda_runtime.h>
@@ -38,32 +41,79 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr float kLargest = 3.402823466e+38f;
 constexpr float kMinusInf = -__builtin_huge_valf();
 
-// Order-preserving image of a key, 0 for a key that cannot be chosen (-inf, NaN).
-__device__ __forceinline__ uint32_t image(float key) {
-    const uint32_t b = __float_as_uint(key);
-    const uint32_t u = b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
-    return key > kMinusInf ? u : 0u;
-}
-__device__ __forceinline__ float from_image(uint32_t u) {
-    return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xffffffffu));
-}
-
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
     return v;
 }
+// The largest of the warp's values (no NaN among them).
+__device__ __forceinline__ float warp_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
 
-// One logit; -inf stands for an absent expert, +inf becomes the largest number.
-template <bool BF16>
-__device__ __forceinline__ float load_logit(const void* row, int e) {
-    float x;
-    if constexpr (BF16)
-        x = __uint_as_float(static_cast<uint32_t>(ld_ro(static_cast<const uint16_t*>(row) + e))
-                            << 16);
-    else
-        x = ld_ro(static_cast<const float*>(row) + e);
-    return x > kMinusInf ? fminf(x, kLargest) : kMinusInf;
+// A lane's logits as loaded.  `wide`: rows and E allow loads of a lane's logits
+// as vectors (wide_rows below), else they are read one by one.
+template <int SLOTS, bool BF16>
+struct Raw {
+    static constexpr int kItem = BF16 ? 2 : 4;
+    static constexpr int kBytes = SLOTS * kItem < 16 ? SLOTS * kItem : 16;  // of one load
+    static constexpr int kVec = kBytes / kItem;                            // its logits
+    uint32_t w[(SLOTS * kItem + 3) / 4];
+
+    // -inf everywhere: what no load overwrites, beyond the last expert, is absent.
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof w / 4); ++i) w[i] = BF16 ? 0xff80ff80u : 0xff800000u;
+    }
+    __device__ __forceinline__ void load(const void* row, int lane, int E, bool wide) {
+        const char* p = static_cast<const char*>(row) + lane * SLOTS * kItem;
+        if (kBytes >= 8 && wide) {
+#pragma unroll
+            for (int s = 0; s < SLOTS; s += kVec) {
+                if (lane * SLOTS + s >= E) continue;
+                uint32_t* to = w + s * kItem / 4;
+                if constexpr (kBytes == 16) {
+                    const uint4 v = ld_ro(reinterpret_cast<const uint4*>(p + s * kItem));
+                    to[0] = v.x; to[1] = v.y; to[2] = v.z; to[3] = v.w;
+                } else if constexpr (kBytes == 8) {
+                    const uint2 v = ld_ro(reinterpret_cast<const uint2*>(p + s * kItem));
+                    to[0] = v.x; to[1] = v.y;
+                }
+            }
+            return;
+        }
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s) {
+            if (lane * SLOTS + s >= E) continue;
+            if constexpr (BF16) {
+                const uint32_t v = ld_ro(reinterpret_cast<const uint16_t*>(p) + s);
+                w[s / 2] = s % 2 ? (w[s / 2] & 0xffffu) | v << 16 : (w[s / 2] & 0xffff0000u) | v;
+            } else {
+                w[s] = __float_as_uint(ld_ro(reinterpret_cast<const float*>(p) + s));
+            }
+        }
+    }
+    // -inf stands for an absent expert, +inf becomes the largest number.
+    __device__ __forceinline__ void values(float (&x)[SLOTS]) const {
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s) {
+            float v;
+            if constexpr (BF16)
+                v = s % 2 ? bf16_hi(w[s / 2]) : bf16_lo(w[s / 2]);
+            else
+                v = __uint_as_float(w[s]);
+            x[s] = v > kMinusInf ? fminf(v, kLargest) : kMinusInf;
+        }
+    }
+};
+
+template <int SLOTS, bool BF16>
+bool wide_rows(const void* base, int64_t ld, int E) {
+    using R = Raw<SLOTS, BF16>;
+    return reinterpret_cast<uintptr_t>(base) % R::kBytes == 0 && ld * R::kItem % R::kBytes == 0 &&
+           E % R::kVec == 0;
 }
 
 template <bool BF16>
@@ -71,133 +121,210 @@ __device__ __forceinline__ const void* row_of(const void* logits, int64_t t, int
     return static_cast<const char*>(logits) + t * ld * (BF16 ? 2 : 4);
 }
 
-// Scores of the lane's logits in place (x becomes the score, 0 where absent).
+__device__ __forceinline__ float logistic(float x) { return rcp_approx(1.0f + expf(-x)); }
+
+// Scores of the lane's logits (0 where absent).
 template <int SLOTS>
-__device__ __forceinline__ void to_scores(float (&x)[SLOTS], bool sigmoid) {
+__device__ __forceinline__ void scores_of(const float (&x)[SLOTS], bool sigmoid,
+                                          float (&p)[SLOTS]) {
     if (sigmoid) {
 #pragma unroll
-        for (int s = 0; s < SLOTS; ++s)
-            x[s] = x[s] > kMinusInf ? __fdiv_rn(1.0f, 1.0f + expf(-x[s])) : 0.0f;
+        for (int s = 0; s < SLOTS; ++s) p[s] = logistic(x[s]);  // exp(inf) = inf gives 0
         return;
     }
-    uint32_t m = 0;
+    float m = x[0];
 #pragma unroll
-    for (int s = 0; s < SLOTS; ++s) m = max(m, image(x[s]));
-    m = __reduce_max_sync(kAll, m);
-    const float top = m ? from_image(m) : 0.0f;
+    for (int s = 1; s < SLOTS; ++s) m = fmaxf(m, x[s]);
+    m = warp_max(m);
+    const float top = m > kMinusInf ? m : 0.0f;
     float sum = 0.0f;
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
-        x[s] = x[s] > kMinusInf ? expf(x[s] - top) : 0.0f;
-        sum += x[s];
+        p[s] = expf(x[s] - top);
+        sum += p[s];
     }
-    sum = fmaxf(warp_sum(sum), 1.0f);  // at least exp(0) unless no expert is there
+    // at least exp(0) unless no expert is there
+    const float r = __fdiv_rn(1.0f, fmaxf(warp_sum(sum), 1.0f));
 #pragma unroll
-    for (int s = 0; s < SLOTS; ++s) x[s] = __fdiv_rn(x[s], sum);
+    for (int s = 0; s < SLOTS; ++s) p[s] *= r;
+}
+
+// What a warp keeps in shared memory: the gathered keys with their experts and
+// scores, and the choice in order.
+struct Bench {
+    float2 key[32];  // key, and its expert as bits
+    float score[32], chosen_score[32];
+    int chosen[32];
+};
+
+// Takes the keys of the experts outside the best topk_groups groups out.  The
+// group's score comes from its lanes where groups are runs of 1, 2, 4 .. lanes
+// (lanes > 0), else lane g reads group g's keys from shared memory.
+template <int SLOTS>
+__device__ __forceinline__ void keep_groups(float (&key)[SLOTS], const RouteShape& sh, int lane,
+                                            int lanes, float* shared_keys) {
+    const int per = sh.E / sh.groups;
+    float best = kMinusInf, second = kMinusInf;
+    const auto take = [&](float v) {
+        second = fmaxf(second, fminf(best, v));
+        best = fmaxf(best, v);
+    };
+    if (lanes > 0) {
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s) take(key[s]);
+        for (int o = 1; o < lanes; o <<= 1) {
+            const float b = __shfl_xor_sync(kAll, best, o), c = __shfl_xor_sync(kAll, second, o);
+            second = fmaxf(fmaxf(second, c), fminf(best, b));
+            best = fmaxf(best, b);
+        }
+    } else {
+        __syncwarp();
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s)
+            if (lane * SLOTS + s < sh.E) shared_keys[lane * SLOTS + s] = key[s];
+        __syncwarp();
+        if (lane < sh.groups)
+            for (int i = 0; i < per; ++i) take(shared_keys[lane * per + i]);
+    }
+    const float score = sh.group_top == 2 && second > kMinusInf ? best + second : best;
+    // rank of a group: how many are better, or equal and before it
+    const int step = lanes > 0 ? lanes : 1;
+    const int mine = lane / step;
+    int rank = 0;
+    for (int g = 0; g < sh.groups; ++g) {
+        const float v = __shfl_sync(kAll, score, g * step);
+        rank += v > score || (v == score && g < mine);
+    }
+    const unsigned kept = __ballot_sync(kAll, mine < sh.groups && rank < sh.topk_groups);
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) {
+        const int g = lanes > 0 ? lane : min((lane * SLOTS + s) / per, 31);
+        if (!(kept >> g & 1u)) key[s] = kMinusInf;
+    }
+}
+
+// The k largest keys in falling order, ties to the lowest index, into
+// bench.chosen / chosen_score (untouched beyond what there is).
+template <int SLOTS>
+__device__ __forceinline__ void choose(float (&key)[SLOTS], const float (&score)[SLOTS], int k,
+                                       int lane, Bench& bench) {
+    float top = key[0];
+#pragma unroll
+    for (int s = 1; s < SLOTS; ++s) top = fmaxf(top, key[s]);
+    // the k-th largest of the lanes' maxima
+    float bound = kMinusInf, left = top;
+    for (int i = 0; i < k; ++i) {
+        bound = warp_max(left);
+        if (!(bound > kMinusInf)) break;
+        const unsigned who = __ballot_sync(kAll, left == bound);
+        if (lane == __ffs(who) - 1) left = kMinusInf;
+    }
+    int count = 0;
+    const unsigned below = (1u << lane) - 1;
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) {
+        const bool in = key[s] >= bound && key[s] > kMinusInf;
+        const unsigned who = __ballot_sync(kAll, in);
+        const int at = count + __popc(who & below);
+        if (in && at < 32) {
+            bench.key[at] = make_float2(key[s], __int_as_float(lane * SLOTS + s));
+            bench.score[at] = score[s];
+        }
+        count += __popc(who);
+    }
+    __syncwarp();
+    if (count <= 32) {
+        const float2 mine = bench.key[lane];
+        const int id = __float_as_int(mine.y);
+        int rank = 0;
+        for (int i = 0; i < count; ++i) {
+            const float2 v = bench.key[i];
+            rank += v.x > mine.x || (v.x == mine.x && __float_as_int(v.y) < id);
+        }
+        if (lane < count && rank < k) {
+            bench.chosen[rank] = id;
+            bench.chosen_score[rank] = bench.score[lane];
+        }
+    } else {
+        // many ties, or k near the number of lanes: one key a round
+        for (int i = 0; i < k; ++i) {
+            float m = key[0];
+#pragma unroll
+            for (int s = 1; s < SLOTS; ++s) m = fmaxf(m, key[s]);
+            const float best = warp_max(m);
+            if (!(best > kMinusInf)) break;
+            const unsigned who = __ballot_sync(kAll, m == best);
+            if (lane != __ffs(who) - 1) continue;
+            bool done = false;
+#pragma unroll
+            for (int s = 0; s < SLOTS; ++s)
+                if (!done && key[s] == best) {
+                    bench.chosen[i] = lane * SLOTS + s;
+                    bench.chosen_score[i] = score[s];
+                    key[s] = kMinusInf;
+                    done = true;
+                }
+        }
+    }
+    __syncwarp();
 }
 
 template <int SLOTS, bool BF16>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, SLOTS <= 8 ? 4 : 1)
     route_topk_kernel(const void* __restrict__ logits, const float* __restrict__ bias,
                       int32_t* __restrict__ ids, float* __restrict__ weights,
-                      int32_t* __restrict__ counts, int64_t T, int64_t ld, RouteShape sh) {
-    extern __shared__ uint32_t shared[];
+                      int32_t* __restrict__ counts, int64_t T, int64_t ld, RouteShape sh,
+                      bool wide, int lanes) {
+    extern __shared__ float shared[];
+    __shared__ Bench benches[kWarps];
     grid_dependency_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int32_t* tally = reinterpret_cast<int32_t*>(shared);  // [E], when counts are wanted
-    uint32_t* keys = shared + (counts ? sh.E : 0) + warp * sh.E;  // [E] a warp, with groups
+    Bench& bench = benches[warp];
+    int32_t* tally = reinterpret_cast<int32_t*>(shared);           // [E], when counts are wanted
+    float* keys = shared + (counts ? sh.E : 0) + warp * sh.E;      // [E] a warp, when lanes == 0
     if (counts) {
         for (int e = threadIdx.x; e < sh.E; e += kThreads) tally[e] = 0;
         __syncthreads();
     }
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
+    int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
     grid_dependency_wait();
     float b[SLOTS];
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
-        const int e = lane + 32 * s;
+        const int e = lane * SLOTS + s;
         b[s] = bias && e < sh.E ? ld_ro(bias + e) : 0.0f;
     }
-    const int per = sh.E / sh.groups;
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < T;
-         t += static_cast<int64_t>(gridDim.x) * kWarps) {
-        const void* row = row_of<BF16>(logits, t, ld);
-        float x[SLOTS];
-        uint32_t u[SLOTS];
+    Raw<SLOTS, BF16> raw;
+    raw.clear();
+    if (t < T) raw.load(row_of<BF16>(logits, t, ld), lane, sh.E, wide);
+    for (; t < T; t += step) {
+        float x[SLOTS], p[SLOTS];
+        raw.values(x);
+        if (t + step < T) raw.load(row_of<BF16>(logits, t + step, ld), lane, sh.E, wide);
+        scores_of<SLOTS>(x, sh.sigmoid, p);
 #pragma unroll
         for (int s = 0; s < SLOTS; ++s) {
-            const int e = lane + 32 * s;
-            x[s] = e < sh.E ? load_logit<BF16>(row, e) : kMinusInf;
-            u[s] = x[s] > kMinusInf;
+            const float key = p[s] + b[s];
+            x[s] = x[s] > kMinusInf && key > kMinusInf ? key : kMinusInf;  // NaN: a bias of NaN
         }
-        to_scores<SLOTS>(x, sh.sigmoid);
-#pragma unroll
-        for (int s = 0; s < SLOTS; ++s) u[s] = u[s] ? image(x[s] + b[s]) : 0u;
+        if (sh.groups > 1) keep_groups<SLOTS>(x, sh, lane, lanes, keys);
+        bench.chosen[lane] = -1;
+        bench.chosen_score[lane] = 0.0f;
+        choose<SLOTS>(x, p, sh.k, lane, bench);
 
-        if (sh.groups > 1) {
-            // lane g scores group g from the warp's copy of the keys
-            __syncwarp();
-#pragma unroll
-            for (int s = 0; s < SLOTS; ++s)
-                if (lane + 32 * s < sh.E) keys[lane + 32 * s] = u[s];
-            __syncwarp();
-            uint32_t best = 0, second = 0;
-            if (lane < sh.groups)
-                for (int i = 0; i < per; ++i) {
-                    const uint32_t v = keys[lane * per + i];
-                    second = max(second, min(best, v));
-                    best = max(best, v);
-                }
-            uint32_t score = best;
-            if (sh.group_top == 2 && second) score = image(from_image(best) + from_image(second));
-            unsigned kept = 0;
-            for (int i = 0; i < sh.topk_groups; ++i) {
-                const uint32_t m = __reduce_max_sync(kAll, score);
-                const int g = __ffs(__ballot_sync(kAll, score == m)) - 1;
-                kept |= 1u << g;
-                if (lane == g) score = 0;
-                if (m == 0) break;
-            }
-#pragma unroll
-            for (int s = 0; s < SLOTS; ++s)
-                if (!(kept >> ((lane + 32 * s) / per) & 1u)) u[s] = 0;
-        }
-
-        // k rounds of: the largest key, its lowest index, taken out
-        int my_id = -1;
-        float my_w = 0.0f;
-        for (int i = 0; i < sh.k; ++i) {
-            uint32_t lmax = 0;
-#pragma unroll
-            for (int s = 0; s < SLOTS; ++s) lmax = max(lmax, u[s]);
-            const uint32_t m = __reduce_max_sync(kAll, lmax);
-            if (m == 0) break;
-            unsigned e = ~0u;
-            float sc = 0.0f;
-#pragma unroll
-            for (int s = SLOTS - 1; s >= 0; --s)
-                if (u[s] == m) {
-                    e = lane + 32 * s;
-                    sc = x[s];
-                }
-            const unsigned first = __reduce_min_sync(kAll, e);
-            const float w = __shfl_sync(kAll, sc, first & 31);
-#pragma unroll
-            for (int s = 0; s < SLOTS; ++s)
-                if (first == lane + 32u * s) u[s] = 0;
-            if (lane == i) {
-                my_id = static_cast<int>(first);
-                my_w = w;
-            }
-        }
+        const int id = bench.chosen[lane];
+        float w = lane < sh.k ? bench.chosen_score[lane] : 0.0f;
         if (sh.renorm) {
-            const float total = warp_sum(my_w);
-            my_w = total > 0.0f ? __fdiv_rn(my_w, total) : 0.0f;
+            const float total = warp_sum(w);
+            w = total > 0.0f ? __fdiv_rn(w, total) : 0.0f;
         }
         if (lane < sh.k) {
-            st_plain(ids + t * sh.k + lane, my_id);
-            st_plain(weights + t * sh.k + lane, my_w * sh.scale);
-            if (counts && my_id >= 0) atomicAdd(tally + my_id, 1);
+            st_plain(ids + t * sh.k + lane, id);
+            st_plain(weights + t * sh.k + lane, w * sh.scale);
+            if (counts && id >= 0) atomicAdd(tally + id, 1);
         }
+        __syncwarp();
     }
     if (counts) {
         __syncthreads();
@@ -206,80 +333,153 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
-template <int SLOTS, bool BF16>
+// One output row from the warp's copy in shared memory, as 16-byte vectors where
+// the rows allow it.
+template <bool BF16>
+__device__ __forceinline__ void store_row(void* out, const float* row, int E, int lane, bool wide) {
+    constexpr int kVec = BF16 ? 8 : 4;
+    if (wide) {
+        for (int e = lane * kVec; e < E; e += 32 * kVec) {
+            uint4* to = static_cast<uint4*>(out) + e / kVec;
+            const float4 a = *reinterpret_cast<const float4*>(row + e);
+            if constexpr (BF16) {
+                const float4 b = *reinterpret_cast<const float4*>(row + e + 4);
+                const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                st_stream(to, pack8_bf16(v));
+            } else {
+                st_stream(to, make_uint4(__float_as_uint(a.x), __float_as_uint(a.y),
+                                         __float_as_uint(a.z), __float_as_uint(a.w)));
+            }
+        }
+        return;
+    }
+    for (int e = lane; e < E; e += 32) {
+        if constexpr (BF16)
+            st_plain(static_cast<uint16_t*>(out) + e,
+                     static_cast<uint16_t>(pack_bf16x2(row[e], 0.0f)));
+        else
+            st_plain(static_cast<float*>(out) + e, row[e]);
+    }
+}
+
+// ds of the lane's slot from a = scale * dweight and the chosen scores; by the
+// weights p / S, which are exactly 1 for a single expert: its gradient is 0.
+__device__ __forceinline__ float score_grad(float a, float score, bool renorm) {
+    if (!renorm) return a;
+    const float total = warp_sum(score);
+    const float r = total > 0.0f ? __fdiv_rn(score, total) : 0.0f;
+    const float dot = warp_sum(a * r);
+    return total > 0.0f ? __fdiv_rn(a - dot, total) : 0.0f;
+}
+
+// Adds v to row[id] for every lane with id >= 0; an id given more than once adds
+// up in the order of its slots.
+__device__ __forceinline__ void scatter(float* row, int id, float v, int lane) {
+    const unsigned same = __match_any_sync(kAll, id);
+    float sum = 0.0f;
+    unsigned rest = same;
+    while (__any_sync(kAll, rest)) {
+        const int from = rest ? __ffs(rest) - 1 : lane;
+        const float x = __shfl_sync(kAll, v, from);
+        if (rest) sum += x;
+        rest &= rest - 1;
+        if (__all_sync(kAll, id < 0 || !rest)) break;
+    }
+    if (id >= 0 && lane == __ffs(same) - 1) row[id] += sum;
+}
+
+// Floats of a warp's row in shared memory: all lanes' slots, or E rounded up to
+// whole 16-byte vectors of bf16 where no slots are written (slots 0).
+__host__ __device__ constexpr int row_length(int E, int slots) {
+    return slots ? (slots < 4 ? (32 * slots + 7) / 8 * 8 : 32 * slots) : (E + 7) / 8 * 8;
+}
+
+// The lane's slots into the warp's row, as vectors where there are four or more.
+template <int SLOTS>
+__device__ __forceinline__ void put_row(float* row, int lane, const float (&v)[SLOTS]) {
+    float* to = row + lane * SLOTS;
+    if constexpr (SLOTS >= 4) {
+#pragma unroll
+        for (int s = 0; s < SLOTS; s += 4)
+            *reinterpret_cast<float4*>(to + s) = make_float4(v[s], v[s + 1], v[s + 2], v[s + 3]);
+    } else {
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s) to[s] = v[s];
+    }
+}
+
+template <int SLOTS, bool BF16, bool SIGMOID>
 __global__ void __launch_bounds__(kThreads)
     route_backward_kernel(const void* __restrict__ logits, const int32_t* __restrict__ ids,
                           const float* __restrict__ dweights, void* __restrict__ dlogits,
-                          int64_t T, int64_t ld, RouteShape sh) {
-    extern __shared__ uint32_t shared[];
+                          int64_t T, int64_t ld, RouteShape sh, bool wide, bool wide_out) {
+    extern __shared__ __align__(16) float shared[];
     grid_dependency_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float* ds = reinterpret_cast<float*>(shared) + warp * sh.E;  // [E] a warp
+    const int length = row_length(sh.E, SIGMOID ? 0 : SLOTS);
+    float* row = shared + warp * length;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
+    int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+    // the slot's id (one outside [0, E) is an empty slot) and gradient
+    int next_id = -1;
+    float next_a = 0.0f;
+    Raw<SLOTS, BF16> raw;
+    raw.clear();
+    const auto load = [&](int64_t at) {
+        if (at >= T) return;
+        if constexpr (!SIGMOID) raw.load(row_of<BF16>(logits, at, ld), lane, sh.E, wide);
+        if (lane < sh.k) {
+            next_id = ld_ro(ids + at * sh.k + lane);
+            next_a = ld_ro(dweights + at * sh.k + lane);
+        }
+    };
     grid_dependency_wait();
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < T;
-         t += static_cast<int64_t>(gridDim.x) * kWarps) {
-        const void* row = row_of<BF16>(logits, t, ld);
-        float x[SLOTS], p[SLOTS];
-#pragma unroll
-        for (int s = 0; s < SLOTS; ++s) {
-            const int e = lane + 32 * s;
-            x[s] = e < sh.E ? load_logit<BF16>(row, e) : kMinusInf;
-            p[s] = x[s];
-        }
-        to_scores<SLOTS>(p, sh.sigmoid);
-        // ids outside [0, E) are empty slots
-        int id = lane < sh.k ? ld_ro(ids + t * sh.k + lane) : -1;
-        if (id < 0 || id >= sh.E) id = -1;
-        float a = id >= 0 ? sh.scale * ld_ro(dweights + t * sh.k + lane) : 0.0f;
-        __syncwarp();
-        if (sh.renorm) {
-#pragma unroll
-            for (int s = 0; s < SLOTS; ++s)
-                if (lane + 32 * s < sh.E) ds[lane + 32 * s] = p[s];
-            __syncwarp();
-            const float score = id >= 0 ? ds[id] : 0.0f;
-            const float total = warp_sum(score);
-            // by the weights p / S, which are exactly 1 for a single expert: its gradient is 0
-            const float dot = warp_sum(total > 0.0f ? a * __fdiv_rn(score, total) : 0.0f);
-            a = total > 0.0f && id >= 0 ? __fdiv_rn(a - dot, total) : 0.0f;
-            __syncwarp();
-        }
-#pragma unroll
-        for (int s = 0; s < SLOTS; ++s)
-            if (lane + 32 * s < sh.E) ds[lane + 32 * s] = 0.0f;
-        __syncwarp();
-        for (int i = 0; i < sh.k; ++i) {  // in order: an id given twice adds up the same each time
-            if (lane == i && id >= 0) ds[id] += a;
-            __syncwarp();
-        }
-        float dot = 0.0f;
-        float g[SLOTS];
-#pragma unroll
-        for (int s = 0; s < SLOTS; ++s) {
-            g[s] = lane + 32 * s < sh.E ? ds[lane + 32 * s] : 0.0f;
-            dot += g[s] * p[s];
-        }
-        if (!sh.sigmoid) dot = warp_sum(dot);
-        char* out = static_cast<char*>(dlogits) + t * sh.E * (BF16 ? 2 : 4);
-#pragma unroll
-        for (int s = 0; s < SLOTS; ++s) {
-            const int e = lane + 32 * s;
-            if (e >= sh.E) continue;
-            float d;
-            if (sh.sigmoid) {
-                // s (1 - s) = exp(-|x|) / (1 + exp(-|x|))^2, without cancellation
-                const float q = expf(-fabsf(x[s]));
-                d = __fdiv_rn(g[s] * q, (1.0f + q) * (1.0f + q));
-            } else {
-                d = p[s] * (g[s] - dot);
+    load(t);
+    for (; t < T; t += step) {
+        const int id = next_id >= 0 && next_id < sh.E ? next_id : -1;
+        float a = id >= 0 ? sh.scale * next_a : 0.0f;
+        float d = 0.0f;  // what the chosen expert's logit gets beside the row's share
+        if constexpr (SIGMOID) {
+            // only the chosen logits count
+            float x = kMinusInf;
+            if (id >= 0) {
+                const void* from = row_of<BF16>(logits, t, ld);
+                if constexpr (BF16)
+                    x = __uint_as_float(
+                        static_cast<uint32_t>(ld_ro(static_cast<const uint16_t*>(from) + id)) << 16);
+                else
+                    x = ld_ro(static_cast<const float*>(from) + id);
+                x = x > kMinusInf ? fminf(x, kLargest) : kMinusInf;
             }
-            if (!(x[s] > kMinusInf)) d = 0.0f;
-            if constexpr (BF16)
-                st_plain(reinterpret_cast<uint16_t*>(out) + e,
-                         static_cast<uint16_t>(pack_bf16x2(d, 0.0f)));
-            else
-                st_plain(reinterpret_cast<float*>(out) + e, d);
+            load(t + step);
+            for (int e = lane * 4; e < length; e += 128)
+                *reinterpret_cast<float4*>(row + e) = make_float4(0.f, 0.f, 0.f, 0.f);
+            a = score_grad(a, logistic(x), sh.renorm);
+            // s (1 - s) = exp(-|x|) / (1 + exp(-|x|))^2, without cancellation
+            const float q = expf(-fabsf(x)), r = rcp_approx(1.0f + q);
+            d = a * q * r * r;
+        } else {
+            // dx_e = s_e (ds_e - dot): -s_e dot for all, s_e ds_e for the chosen
+            float x[SLOTS], p[SLOTS];
+            raw.values(x);
+            load(t + step);
+            scores_of<SLOTS>(x, false, p);
+            put_row<SLOTS>(row, lane, p);
+            __syncwarp();
+            const float score = id >= 0 ? row[id] : 0.0f;
+            a = score_grad(a, score, sh.renorm);
+            d = id >= 0 ? a * score : 0.0f;
+            const float dot = warp_sum(d);
+#pragma unroll
+            for (int s = 0; s < SLOTS; ++s) p[s] *= -dot;
+            __syncwarp();
+            put_row<SLOTS>(row, lane, p);
         }
+        __syncwarp();
+        scatter(row, id, d, lane);
+        __syncwarp();
+        store_row<BF16>(static_cast<char*>(dlogits) + t * sh.E * (BF16 ? 2 : 4), row, sh.E, lane,
+                        wide_out);
         __syncwarp();
     }
 }
@@ -303,27 +503,45 @@ cudaError_t launch_route_topk(const void* logits, const float* bias, int32_t* id
     return with_slots(sh.E, [&](auto slots) {
         constexpr int S = decltype(slots)::value;
         auto* k = sh.bf16 ? &route_topk_kernel<S, true> : &route_topk_kernel<S, false>;
-        const size_t smem = 4u * sh.E * ((counts ? 1 : 0) + (sh.groups > 1 ? kWarps : 0));
+        const bool wide = sh.bf16 ? wide_rows<S, true>(logits, ld, sh.E)
+                                  : wide_rows<S, false>(logits, ld, sh.E);
+        // lanes of a group, when groups are runs of a power of two of them
+        const int per = sh.E / sh.groups;
+        int lanes = per % S == 0 ? per / S : 0;
+        if (lanes & (lanes - 1)) lanes = 0;
+        const size_t smem = 4u * sh.E * ((counts ? 1 : 0) + (sh.groups > 1 && !lanes ? kWarps : 0));
         const int grid = persistent_grid(reinterpret_cast<const void*>(k), kThreads, smem,
                                          (T + kWarps - 1) / kWarps);
         if (const cudaError_t e = upload_checks(stream)) return e;
         return launch_pdl(k, grid, kThreads, smem, stream, true, logits, bias, ids, weights,
-                          counts, T, ld, sh);
+                          counts, T, ld, sh, wide, lanes);
     });
 }
 
 cudaError_t launch_route_topk_backward(const void* logits, const int32_t* ids,
                                        const float* dweights, void* dlogits, int64_t T, int64_t ld,
                                        const RouteShape& sh, cudaStream_t stream) {
-    return with_slots(sh.E, [&](auto slots) {
-        constexpr int S = decltype(slots)::value;
-        auto* k = sh.bf16 ? &route_backward_kernel<S, true> : &route_backward_kernel<S, false>;
-        const size_t smem = 4u * sh.E * kWarps;
+    const auto launch = [&](auto* k, int slots, bool wide) {
+        const int64_t item = sh.bf16 ? 2 : 4;
+        const bool wide_out =
+            reinterpret_cast<uintptr_t>(dlogits) % 16 == 0 && sh.E * item % 16 == 0;
+        const size_t smem = 4u * row_length(sh.E, slots) * kWarps;
         const int grid = persistent_grid(reinterpret_cast<const void*>(k), kThreads, smem,
                                          (T + kWarps - 1) / kWarps);
         if (const cudaError_t e = upload_checks(stream)) return e;
         return launch_pdl(k, grid, kThreads, smem, stream, true, logits, ids, dweights, dlogits, T,
-                          ld, sh);
+                          ld, sh, wide, wide_out);
+    };
+    // the sigmoid's gradient reads the chosen logits alone
+    if (sh.sigmoid)
+        return sh.bf16 ? launch(&route_backward_kernel<1, true, true>, 0, false)
+                       : launch(&route_backward_kernel<1, false, true>, 0, false);
+    return with_slots(sh.E, [&](auto slots) {
+        constexpr int S = decltype(slots)::value;
+        return sh.bf16 ? launch(&route_backward_kernel<S, true, false>, S,
+                                wide_rows<S, true>(logits, ld, sh.E))
+                       : launch(&route_backward_kernel<S, false, false>, S,
+                                wide_rows<S, false>(logits, ld, sh.E));
     });
 }
 

@@ -168,6 +168,13 @@ __device__ __forceinline__ uint16_t ld_ro(const uint16_t* p) {
     return access_ok(p, 2, false) ? __ldg(p) : uint16_t{0};
 }
 
+__device__ __forceinline__ uint4 ld_ro(const uint4* p) {
+    return access_ok(p, 16, false) ? __ldg(p) : make_uint4(0, 0, 0, 0);
+}
+__device__ __forceinline__ uint2 ld_ro(const uint2* p) {
+    return access_ok(p, 8, false) ? __ldg(p) : make_uint2(0, 0);
+}
+
 // Streaming stores (.cs: the output is not read again by this kernel).
 __device__ __forceinline__ void st_stream(uint2* p, uint2 v) {
     if (!access_ok(p, 8, true)) return;
