@@ -722,12 +722,14 @@ def cast_back(x, sf, fmt=None, group_size=(1, GROUP), out_dtype=None, out=None):
 def _check_like(t, name, shape, dtypes, device):
     """A tensor operand: contiguous, of one of `dtypes` and of `shape`, on `device`."""
     import torch
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape
+            and t.device == device and t.is_contiguous()):
+        return
     if not isinstance(t, torch.Tensor) or t.device != device or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous CUDA tensor on the inputs' device")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {', '.join(map(str, dtypes))}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {list(shape)}")
+    raise ValueError(f"{name} must have shape {list(shape)}")
 
 
 def _check_logits(logits, scores):
@@ -779,10 +781,11 @@ def route_topk(logits, k: int, scores: str = "softmax", bias=None, num_groups: i
         weights = torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev)
     else:
         _check_out(weights, "weights", logits, 4 * T * k, dtype=torch.float32)
+    lib = _lib or load_library()
     with _device_ctx(dev):
-        st = tkq_route_topk(_ptr(logits), _ptr(bias), _ptr(ids), _ptr(weights), _ptr(counts), T, E,
-                            ld, dtype, k, num_groups, topk_groups, num_topk_sum, flags, scale,
-                            _stream_handle(dev))
+        st = lib.tkq_route_topk(_ptr(logits), _ptr(bias), _ptr(ids), _ptr(weights), _ptr(counts), T, E,
+                                ld, dtype, k, num_groups, topk_groups, num_topk_sum, flags, scale,
+                                _stream_handle(dev))
     if st:
         raise TkqError(st, "tkq_route_topk")
     return ids, weights
@@ -807,9 +810,10 @@ def route_topk_backward(logits, ids, dweights, scores: str = "softmax", renormal
         out = torch.empty((T, E), dtype=logits.dtype, device=dev)
     else:
         _check_out(out, "out", logits, T * E * logits.element_size(), dtype=logits.dtype)
+    lib = _lib or load_library()
     with _device_ctx(dev):
-        st = tkq_route_topk_backward(_ptr(logits), _ptr(ids), _ptr(dweights), _ptr(out), T, E, ld,
-                                     dtype, k, flags, scale, _stream_handle(dev))
+        st = lib.tkq_route_topk_backward(_ptr(logits), _ptr(ids), _ptr(dweights), _ptr(out), T, E, ld,
+                                         dtype, k, flags, scale, _stream_handle(dev))
     if st:
         raise TkqError(st, "tkq_route_topk_backward")
     return out
@@ -838,10 +842,11 @@ def swiglu_forward_cast_and_checkpoint(x, fmt="e4m3", num_per_channels: int = GR
     out_sf = sf_tensor(T, H // g, flags, dev)
     ckpt = torch.empty((T, H2), dtype=_fp8_dtype(cf), device=dev)
     ckpt_sf = torch.empty((T, 2 * (H // g)), dtype=torch.float32, device=dev)
+    lib = _lib or load_library()
     with _device_ctx(dev):
-        st = tkq_swiglu_cast_checkpoint(_ptr(x), _ptr(topk_weights), _ptr(out), _ptr(out_sf),
-                                        _ptr(ckpt), _ptr(ckpt_sf), T, H, num_per_channels, f, cf,
-                                        flags, _stream_handle(dev))
+        st = lib.tkq_swiglu_cast_checkpoint(_ptr(x), _ptr(topk_weights), _ptr(out), _ptr(out_sf),
+                                            _ptr(ckpt), _ptr(ckpt_sf), T, H, num_per_channels, f, cf,
+                                            flags, _stream_handle(dev))
     if st:
         raise TkqError(st, "tkq_swiglu_cast_checkpoint")
     return out, out_sf, ckpt, ckpt_sf
@@ -885,17 +890,18 @@ def swiglu_backward_from_checkpoint(ckpt, ckpt_sf, dy, fmt=None, num_per_channel
         f = _fmt_code(fmt)
         dx = torch.empty((T, 2 * H), dtype=_fp8_dtype(f), device=dev)
         dx_sf = sf_tensor(T, 2 * (H // g), flags, dev)
+    lib = _lib or load_library()
     with _device_ctx(dev):
         stream = _stream_handle(dev)
         if fmt is None:
-            st = tkq_swiglu_checkpoint_backward(_ptr(ckpt), _ptr(ckpt_sf), _ptr(dy),
-                                                _ptr(topk_weights), _ptr(dx), _ptr(y), _ptr(dw), T,
-                                                H, num_per_channels, cf, stream)
+            st = lib.tkq_swiglu_checkpoint_backward(_ptr(ckpt), _ptr(ckpt_sf), _ptr(dy),
+                                                    _ptr(topk_weights), _ptr(dx), _ptr(y), _ptr(dw), T,
+                                                    H, num_per_channels, cf, stream)
         else:
-            st = tkq_swiglu_checkpoint_backward_cast(_ptr(ckpt), _ptr(ckpt_sf), _ptr(dy),
-                                                     _ptr(topk_weights), _ptr(dx), _ptr(dx_sf),
-                                                     _ptr(y), _ptr(dw), T, H, num_per_channels, cf,
-                                                     f, flags, stream)
+            st = lib.tkq_swiglu_checkpoint_backward_cast(_ptr(ckpt), _ptr(ckpt_sf), _ptr(dy),
+                                                         _ptr(topk_weights), _ptr(dx), _ptr(dx_sf),
+                                                         _ptr(y), _ptr(dw), T, H, num_per_channels, cf,
+                                                         f, flags, stream)
     if st:
         raise TkqError(st, "tkq_swiglu_checkpoint_backward")
     return dx, dx_sf, dw, y
@@ -960,12 +966,13 @@ def residual_norm_and_cast(r, h=None, w_post=None, gate=None, w_pre=None, post_n
             x = torch.empty((T, C), dtype=torch.bfloat16, device=dev)
     elif w_pre is not None:
         raise ValueError("w_pre needs fmt or with_bf16")
+    lib = _lib or load_library()
     with _device_ctx(dev):
-        st = tkq_residual_norm_cast(_ptr(r), _ptr(h), _ptr(w_post), _ptr(gate), _ptr(w_pre),
-                                    None if h is None else _ptr(r_out), _ptr(out), _ptr(sf),
-                                    _ptr(x), _ptr(rstd_post), _ptr(rstd_pre), T, C,
-                                    num_per_channels, f, sf_flags, flags, res_scale, eps,
-                                    _stream_handle(dev))
+        st = lib.tkq_residual_norm_cast(_ptr(r), _ptr(h), _ptr(w_post), _ptr(gate), _ptr(w_pre),
+                                        None if h is None else _ptr(r_out), _ptr(out), _ptr(sf),
+                                        _ptr(x), _ptr(rstd_post), _ptr(rstd_pre), T, C,
+                                        num_per_channels, f, sf_flags, flags, res_scale, eps,
+                                        _stream_handle(dev))
     if st:
         raise TkqError(st, "tkq_residual_norm_cast")
     return r_out, out, sf, x, rstd_post, rstd_pre
@@ -1013,6 +1020,7 @@ def residual_norm_backward(dr, r, h=None, dx=None, w_post=None, gate=None, w_pre
     elif w_post is not None or gate is not None or rstd_post is not None:
         raise ValueError("w_post, gate and rstd_post need h")
     dr_out = torch.empty_like(lead)
+    lib = _lib or load_library()
     with _device_ctx(dev):
         if T == 0:  # sums over no rows
             for dw in (dw_post, dw_pre):
@@ -1021,11 +1029,11 @@ def residual_norm_backward(dr, r, h=None, dx=None, w_post=None, gate=None, w_pre
         elif dw_post is not None or dw_pre is not None:
             work = torch.empty((max(tkq_residual_norm_workspace(T, C), 0),), dtype=torch.uint8,
                                device=dev)
-        st = tkq_residual_norm_backward(_ptr(dr), _ptr(dx), _ptr(r) if dx is not None else None,
-                                        _ptr(h), _ptr(w_post), _ptr(gate), _ptr(w_pre),
-                                        _ptr(rstd_post), _ptr(rstd_pre), _ptr(dr_out), _ptr(dh),
-                                        _ptr(dgate), _ptr(dw_post), _ptr(dw_pre), _ptr(work), T, C,
-                                        flags, res_scale, _stream_handle(dev))
+        st = lib.tkq_residual_norm_backward(_ptr(dr), _ptr(dx), _ptr(r) if dx is not None else None,
+                                            _ptr(h), _ptr(w_post), _ptr(gate), _ptr(w_pre),
+                                            _ptr(rstd_post), _ptr(rstd_pre), _ptr(dr_out), _ptr(dh),
+                                            _ptr(dgate), _ptr(dw_post), _ptr(dw_pre), _ptr(work), T, C,
+                                            flags, res_scale, _stream_handle(dev))
     if st:
         raise TkqError(st, "tkq_residual_norm_backward")
     return dr_out, dh, dgate, dw_post, dw_pre
