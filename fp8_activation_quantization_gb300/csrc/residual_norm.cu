@@ -402,14 +402,24 @@ __global__ void __launch_bounds__(kForwardThreads<NV, KEPT>)
 // gradients are summed over a CTA's rows in registers and written as one
 // partial row a CTA; sum_parts_kernel adds them up in order.
 // WHOLE: dr', dx and h are given and the row is exactly the CTA's vectors.
-// 128 registers a thread: capped at 96 (640 threads) the kernel took 228 us instead
-// of 172 us at 16384 x 4096.
-constexpr int kBackwardThreads = 512;
-template <int NV, bool F32, bool POST, bool GATE, bool WHOLE>
-__global__ void __launch_bounds__(kBackwardThreads)
+// How a row is held, by its width (16 bytes a channel; measured at T C = 59 - 67
+// million, bf16 stream, gate):
+//   up to 4096 channels   one vector a thread, 512 threads of 128 registers:
+//                         4096: 171 us, 278 us with the 72 registers below;
+//                         2048: 165 us, 227 us
+//   up to 7168            one vector, 896 threads of 72 registers: 7168: 162 us,
+//                         174 us with two vectors and 448 threads of 128 registers
+//   up to 8192            two vectors, 512 threads of 128 registers
+//   up to 16384           four, the stream and the weights not kept
+struct BackwardKind {
+    int nv, threads;
+};
+constexpr BackwardKind kNarrow = {1, 512}, kMiddle = {1, 896}, kWide = {2, 512}, kWidest = {4, 512};
+template <int NV, int THREADS, bool F32, bool POST, bool GATE, bool WHOLE>
+__global__ void __launch_bounds__(THREADS)
     residual_norm_backward_kernel(const ResidualNormGrad a, Fifo q8) {
     extern __shared__ uint4 fifo[];
-    __shared__ CtaSum<POST ? 3 : 1, kBackwardThreads> cta_sum;
+    __shared__ CtaSum<POST ? 3 : 1, THREADS> cta_sum;
     grid_dependency_launch();
     constexpr int kS = F32 ? 2 : 1;   // slots of a stream: h, gate, dr, dx, r
     constexpr bool kKept = NV <= 2;
@@ -664,11 +674,14 @@ cudaError_t with_options(bool f32, bool post, bool gate, F&& f) {
     });
 }
 
-int backward_nv(int64_t C) {
+BackwardKind backward_kind(int64_t C) {
     const int64_t vecs = C / 8;
-    return vecs <= kBackwardThreads ? 1 : vecs <= 2 * kBackwardThreads ? 2 : 4;
+    return vecs <= kNarrow.threads     ? kNarrow
+           : vecs <= kMiddle.threads   ? kMiddle
+           : vecs <= 2 * kWide.threads ? kWide
+                                       : kWidest;
 }
-constexpr int kBackwardThreadsPerSm = 768;  // below 4096 channels, of about 80 registers
+constexpr int kBackwardThreadsPerSm = 768;  // narrow rows, of about 80 registers
 
 }  // namespace
 
@@ -714,8 +727,8 @@ cudaError_t launch_residual_norm(const ResidualNorm& a, int fmt, unsigned sf_fla
 // Partial rows a backward launch writes at most: one a CTA, as many CTAs an SM
 // as its threads allow, no more than rows.
 int64_t residual_norm_parts(int64_t T, int64_t C) {
-    const int nv = backward_nv(C);
-    const int64_t per_sm = 2 * kBackwardThreads / shape_of(C, nv, kBackwardThreadsPerSm, 1, 1).threads;
+    const int nv = backward_kind(C).nv;
+    const int64_t per_sm = 1024 / shape_of(C, nv, kBackwardThreadsPerSm, 1, 1).threads;
     const int64_t most = num_sms() * (per_sm < 16 ? per_sm : 16);
     return T < most ? T : most;
 }
@@ -723,8 +736,8 @@ int64_t residual_norm_parts(int64_t T, int64_t C) {
 cudaError_t launch_residual_norm_backward(const ResidualNormGrad& a, cudaStream_t stream) {
     const int slot = a.r_f32 ? 2 : 1;
     const int slots = (a.dr ? slot : 0) + (a.dx ? 1 + slot : 0) + (a.h ? 1 : 0) + (a.gate ? 1 : 0);
-    const int nv = backward_nv(a.C);
-    const Shape s = shape_of(a.C, nv, kBackwardThreadsPerSm, slots, 1);
+    const BackwardKind kind = backward_kind(a.C);
+    const Shape s = shape_of(a.C, kind.nv, kBackwardThreadsPerSm, slots, 1);
     int parts = 0;
     const auto launch = [&](auto* k) {
         parts = persistent_grid(reinterpret_cast<const void*>(k), s.threads, s.smem,
@@ -733,11 +746,18 @@ cudaError_t launch_residual_norm_backward(const ResidualNormGrad& a, cudaStream_
         return launch_pdl(k, parts, s.threads, s.smem, stream, true, a, s.fifo);
     };
     const cudaError_t e = with_options(a.r_f32, a.post, a.gate, [&](auto f32, auto post, auto gate) {
-        if (nv == 4) return launch(&residual_norm_backward_kernel<4, f32(), post(), gate(), false>);
+        const auto of = [&](auto nv, auto threads, auto whole) {
+            return launch(&residual_norm_backward_kernel<nv(), threads(), f32(), post(), gate(),
+                                                         whole()>);
+        };
+        using std::integral_constant;
+        constexpr integral_constant<int, 512> few;
+        constexpr integral_constant<int, 896> many;
+        if (kind.nv == 4) return of(integral_constant<int, 4>(), few, std::false_type());
         return with_flag(s.exact && a.dr && a.dx && a.h, [&](auto whole) {
-            if (nv == 2)
-                return launch(&residual_norm_backward_kernel<2, f32(), post(), gate(), whole()>);
-            return launch(&residual_norm_backward_kernel<1, f32(), post(), gate(), whole()>);
+            if (kind.nv == 2) return of(integral_constant<int, 2>(), few, whole);
+            return kind.threads == few() ? of(integral_constant<int, 1>(), few, whole)
+                                         : of(integral_constant<int, 1>(), many, whole);
         });
     });
     if (e != cudaSuccess || (!a.dw_pre && !a.dw_post)) return e;
