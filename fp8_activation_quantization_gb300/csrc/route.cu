@@ -149,12 +149,11 @@ __device__ __forceinline__ void scores_of(const float (&x)[SLOTS], bool sigmoid,
     for (int s = 0; s < SLOTS; ++s) p[s] *= r;
 }
 
-// What a warp keeps in shared memory: the gathered keys with their experts and
-// scores, and the choice in order.
-struct Bench {
-    float2 key[32];  // key, and its expert as bits
-    float score[32], chosen_score[32];
-    int chosen[32];
+// What a warp keeps in shared memory: the gathered keys (-inf where there is
+// none) with their experts and scores, and the choice in order.
+struct alignas(16) Bench {
+    float key[32], score[32], chosen_score[32];
+    int id[32], chosen[32];
 };
 
 // Takes the keys of the experts outside the best topk_groups groups out.  The
@@ -219,30 +218,42 @@ __device__ __forceinline__ void choose(float (&key)[SLOTS], const float (&score)
         const unsigned who = __ballot_sync(kAll, left == bound);
         if (lane == __ffs(who) - 1) left = kMinusInf;
     }
-    int count = 0;
-    const unsigned below = (1u << lane) - 1;
+    // gathered in the order of the lanes and their slots, which is that of the experts
+    unsigned in = 0;
 #pragma unroll
-    for (int s = 0; s < SLOTS; ++s) {
-        const bool in = key[s] >= bound && key[s] > kMinusInf;
-        const unsigned who = __ballot_sync(kAll, in);
-        const int at = count + __popc(who & below);
-        if (in && at < 32) {
-            bench.key[at] = make_float2(key[s], __int_as_float(lane * SLOTS + s));
-            bench.score[at] = score[s];
-        }
-        count += __popc(who);
+    for (int s = 0; s < SLOTS; ++s)
+        in |= (key[s] >= bound && key[s] > kMinusInf ? 1u : 0u) << s;
+    const int own = __popc(in);
+    int upto = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(kAll, upto, o);
+        if (lane >= o) upto += v;
     }
-    __syncwarp();
+    const int count = __shfl_sync(kAll, upto, 31);
     if (count <= 32) {
-        const float2 mine = bench.key[lane];
-        const int id = __float_as_int(mine.y);
+        int at = upto - own;
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s)
+            if (in >> s & 1u) {
+                bench.key[at] = key[s];
+                bench.score[at] = score[s];
+                bench.id[at] = lane * SLOTS + s;
+                ++at;
+            }
+        __syncwarp();
+        // rank: how many are larger, or equal and before it
+        const float mine = bench.key[lane];
         int rank = 0;
-        for (int i = 0; i < count; ++i) {
-            const float2 v = bench.key[i];
-            rank += v.x > mine.x || (v.x == mine.x && __float_as_int(v.y) < id);
+        for (int i = 0; i < count; i += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(bench.key + i);
+            rank += v.x > mine || (v.x == mine && i < lane);
+            rank += v.y > mine || (v.y == mine && i + 1 < lane);
+            rank += v.z > mine || (v.z == mine && i + 2 < lane);
+            rank += v.w > mine || (v.w == mine && i + 3 < lane);
         }
         if (lane < count && rank < k) {
-            bench.chosen[rank] = id;
+            bench.chosen[rank] = bench.id[lane];
             bench.chosen_score[rank] = bench.score[lane];
         }
     } else {
@@ -309,8 +320,10 @@ __global__ void __launch_bounds__(kThreads, SLOTS <= 8 ? 4 : 1)
             x[s] = x[s] > kMinusInf && key > kMinusInf ? key : kMinusInf;  // NaN: a bias of NaN
         }
         if (sh.groups > 1) keep_groups<SLOTS>(x, sh, lane, lanes, keys);
+        bench.key[lane] = kMinusInf;
         bench.chosen[lane] = -1;
         bench.chosen_score[lane] = 0.0f;
+        __syncwarp();
         choose<SLOTS>(x, p, sh.k, lane, bench);
 
         const int id = bench.chosen[lane];
