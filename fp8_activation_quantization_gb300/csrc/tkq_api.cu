@@ -905,7 +905,7 @@ const char* tkq_status_string(int status) {
     }
 }
 
-int tkq_version(void) { return 200; }
+int tkq_version(void) { return 300; }
 
 int tkq_checked_build(void) {
 #ifdef TKQ_CHECKED
