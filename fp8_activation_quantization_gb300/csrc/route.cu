@@ -18,18 +18,19 @@
 // without any expert is all -1.  A logit of +inf counts as the largest finite
 // number, which keeps exp(x - m) defined.
 //
-// One warp per token, the logits in registers: lane l holds the SLOTS experts
-// from l * SLOTS on, so a lower lane holds lower indices and a group of experts
-// is a run of lanes.  The forward is bound by instructions, not memory (16384 x
-// 256 fp32 is 2.7 us of reads): the choice is therefore made in two steps.  The
-// k-th largest of the 32 lanes' maxima, found by k reductions, bounds the k-th
-// largest key from below; the few keys that reach it are gathered, one a lane,
-// and ranked by counting.  k rounds over all of a lane's keys took 35.0 us for 8
-// of 256 experts in 8 groups at 16384 tokens, this takes 21.0 us (1000
-// instructions a token).  The backward writes each row through shared memory, so
-// that it leaves as 16-byte vectors: 9.5 us (3.6 TB/s) for the softmax, 6.9 us
-// for the sigmoid, which reads the chosen logits alone; 18.9 us with scalar
-// accesses.
+// Logits in registers: lane l of a token's lanes holds the SLOTS experts from
+// l * SLOTS on, so a lower lane holds lower indices and a group of experts is a
+// run of lanes.  The forward is bound by instructions, not memory (16384 x 256
+// fp32 is 2.7 us of reads).  So a token has 8 or 16 lanes where its experts fit
+// (LANES, `with_lanes`), and 4 or 2 tokens share a warp's instructions; and the
+// choice is made in two steps: the k-th largest of the lanes' maxima bounds the
+// k-th largest key from below; the few keys that reach it are gathered and ranked
+// by counting.  8 of 256 experts at 16384 tokens: 12.0 us; in 8 groups of which 4
+// are searched, with a bias, 18.3 us (35.0 us with k rounds over all keys).
+// The backward has one warp per token and writes each row through shared memory,
+// so that it leaves as 16-byte vectors: 9.5 us (3.6 TB/s) for the softmax at
+// 16384 x 256, 6.9 us for the sigmoid, which reads the chosen logits alone;
+// 18.9 us with scalar accesses.
 #include <type_traits>
 
 #include <cuda_runtime.h>
@@ -46,16 +47,24 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr float kLargest = 3.402823466e+38f;
 constexpr float kMinusInf = -__builtin_huge_valf();
 
-__device__ __forceinline__ float warp_sum(float v) {
+// Sum and maximum (no NaN) over LANES consecutive lanes.
+template <int LANES>
+__device__ __forceinline__ float team_sum(float v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
     return v;
 }
-// The largest of the warp's values (no NaN among them).
-__device__ __forceinline__ float warp_max(float v) {
-    float r;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-    return r;
+__device__ __forceinline__ float warp_sum(float v) { return team_sum<32>(v); }
+template <int LANES>
+__device__ __forceinline__ float team_max(float v) {
+    if constexpr (LANES == 32) {
+        float r;
+        asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+        return r;
+    }
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+    return v;
 }
 
 // A lane's logits as loaded.  `wide`: rows and E allow loads of a lane's logits
@@ -129,7 +138,7 @@ __device__ __forceinline__ const void* row_of(const void* logits, int64_t t, int
 __device__ __forceinline__ float logistic(float x) { return rcp_approx(1.0f + expf(-x)); }
 
 // Scores of the lane's logits (0 where absent).
-template <int SLOTS>
+template <int SLOTS, int LANES>
 __device__ __forceinline__ void scores_of(const float (&x)[SLOTS], bool sigmoid,
                                           float (&p)[SLOTS]) {
     if (sigmoid) {
@@ -140,7 +149,7 @@ __device__ __forceinline__ void scores_of(const float (&x)[SLOTS], bool sigmoid,
     float m = x[0];
 #pragma unroll
     for (int s = 1; s < SLOTS; ++s) m = fmaxf(m, x[s]);
-    m = warp_max(m);
+    m = team_max<LANES>(m);
     const float top = m > kMinusInf ? m : 0.0f;
     float sum = 0.0f;
 #pragma unroll
@@ -149,199 +158,256 @@ __device__ __forceinline__ void scores_of(const float (&x)[SLOTS], bool sigmoid,
         sum += p[s];
     }
     // at least exp(0) unless no expert is there
-    const float r = __fdiv_rn(1.0f, fmaxf(warp_sum(sum), 1.0f));
+    const float r = __fdiv_rn(1.0f, fmaxf(team_sum<LANES>(sum), 1.0f));
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) p[s] *= r;
 }
 
-// What a warp keeps in shared memory: the gathered keys (-inf where there is
+// What a token keeps in shared memory: the gathered keys (-inf where there is
 // none) with their experts and scores, and the choice in order.
+constexpr int kBench = 64;  // keys gathered at most
 struct alignas(16) Bench {
-    float key[32], score[32], chosen_score[32];
-    int id[32], chosen[32];
+    float key[kBench], score[kBench], chosen_score[32];
+    int id[kBench], chosen[32];
+
+    template <int LANES>
+    __device__ __forceinline__ void clear(int l) {
+        for (int i = 4 * l; i < kBench; i += 4 * LANES)
+            *reinterpret_cast<float4*>(key + i) =
+                make_float4(kMinusInf, kMinusInf, kMinusInf, kMinusInf);
+        for (int i = l; i < 32; i += LANES) {
+            chosen[i] = -1;
+            chosen_score[i] = 0.0f;
+        }
+    }
 };
 
-// Takes the keys of the experts outside the best topk_groups groups out.  The
+// Takes the keys of the experts outside the best topk_groups groups out.  A
 // group's score comes from its lanes where groups are runs of 1, 2, 4 .. lanes
-// (lanes > 0), else lane g reads group g's keys from shared memory.
-template <int SLOTS>
-__device__ __forceinline__ void keep_groups(float (&key)[SLOTS], const RouteShape& sh, int lane,
-                                            int lanes, float* shared_keys) {
+// (group_lanes > 0), else one lane reads a group's keys from shared memory.
+template <int SLOTS, int LANES>
+__device__ __forceinline__ void keep_groups(float (&key)[SLOTS], const RouteShape& sh, int l,
+                                            int group_lanes, float* shared_keys) {
     const int per = sh.E / sh.groups;
     float best = kMinusInf, second = kMinusInf;
     const auto take = [&](float v) {
         second = fmaxf(second, fminf(best, v));
         best = fmaxf(best, v);
     };
-    if (lanes > 0) {
+    const auto score_of = [&] {
+        return sh.group_top == 2 && second > kMinusInf ? best + second : best;
+    };
+    // rank of a group: how many are better, or equal and before it
+    if (group_lanes > 0) {
 #pragma unroll
         for (int s = 0; s < SLOTS; ++s) take(key[s]);
-        for (int o = 1; o < lanes; o <<= 1) {
+        for (int o = 1; o < group_lanes; o <<= 1) {
             const float b = __shfl_xor_sync(kAll, best, o), c = __shfl_xor_sync(kAll, second, o);
             second = fmaxf(fmaxf(second, c), fminf(best, b));
             best = fmaxf(best, b);
         }
-    } else {
-        __syncwarp();
+        const float score = score_of();
+        const int mine = l / group_lanes;
+        int rank = 0;
+#pragma unroll 4
+        for (int g = 0; g < sh.groups; ++g) {
+            const float v = __shfl_sync(kAll, score, g * group_lanes, LANES);
+            rank += v > score || (v == score && g < mine);
+        }
+        if (rank >= sh.topk_groups) {
 #pragma unroll
-        for (int s = 0; s < SLOTS; ++s)
-            if (lane * SLOTS + s < sh.E) shared_keys[lane * SLOTS + s] = key[s];
-        __syncwarp();
-        if (lane < sh.groups)
-            for (int i = 0; i < per; ++i) take(shared_keys[lane * per + i]);
+            for (int s = 0; s < SLOTS; ++s) key[s] = kMinusInf;
+        }
+        return;
     }
-    const float score = sh.group_top == 2 && second > kMinusInf ? best + second : best;
-    // rank of a group: how many are better, or equal and before it
-    const int step = lanes > 0 ? lanes : 1;
-    const int mine = lane / step;
-    int rank = 0;
-    for (int g = 0; g < sh.groups; ++g) {
-        const float v = __shfl_sync(kAll, score, g * step);
-        rank += v > score || (v == score && g < mine);
+    // [E] keys, then [32] scores; as many lanes a group as there are, a part of
+    // its keys each
+    float* scores = shared_keys + sh.E;
+    __syncwarp();
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s)
+        if (l * SLOTS + s < sh.E) shared_keys[l * SLOTS + s] = key[s];
+    __syncwarp();
+    int parts = 1;
+    while (parts * 2 * sh.groups <= LANES) parts *= 2;
+    for (int g0 = 0; g0 < sh.groups; g0 += LANES / parts) {
+        const int g = g0 + l / parts;
+        best = second = kMinusInf;
+        if (g < sh.groups)
+            for (int i = l % parts; i < per; i += parts) take(shared_keys[g * per + i]);
+        for (int o = 1; o < parts; o <<= 1) {
+            const float b = __shfl_xor_sync(kAll, best, o), c = __shfl_xor_sync(kAll, second, o);
+            second = fmaxf(fmaxf(second, c), fminf(best, b));
+            best = fmaxf(best, b);
+        }
+        if (g < sh.groups && l % parts == 0) scores[g] = score_of();
     }
-    const unsigned kept = __ballot_sync(kAll, mine < sh.groups && rank < sh.topk_groups);
+    __syncwarp();
+    unsigned kept = 0;
+    for (int g = l; g < sh.groups; g += LANES) {
+        const float mine = scores[g];
+        int rank = 0;
+        for (int i = 0; i < sh.groups; ++i) {
+            const float v = scores[i];
+            rank += v > mine || (v == mine && i < g);
+        }
+        kept |= (rank < sh.topk_groups ? 1u : 0u) << g;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) kept |= __shfl_xor_sync(kAll, kept, o);
+    int g = l * SLOTS / per, left = per - (l * SLOTS - g * per);  // of the group's experts
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
-        const int g = lanes > 0 ? lane : min((lane * SLOTS + s) / per, 31);
-        if (!(kept >> g & 1u)) key[s] = kMinusInf;
+        if (g > 31 || !(kept >> g & 1u)) key[s] = kMinusInf;
+        if (--left == 0) {
+            ++g;
+            left = per;
+        }
     }
 }
 
 // The k largest keys in falling order, ties to the lowest index, into
-// bench.chosen / chosen_score (untouched beyond what there is).
-template <int SLOTS>
+// bench.chosen / chosen_score (untouched beyond what there is).  All tokens of the
+// warp go through the same steps.
+template <int SLOTS, int LANES>
 __device__ __forceinline__ void choose(float (&key)[SLOTS], const float (&score)[SLOTS], int k,
-                                       int lane, Bench& bench) {
+                                       int l, Bench& bench) {
     float top = key[0];
 #pragma unroll
     for (int s = 1; s < SLOTS; ++s) top = fmaxf(top, key[s]);
-    // the k-th largest of the lanes' maxima
-    float bound = kMinusInf, left = top;
-    for (int i = 0; i < k; ++i) {
-        bound = warp_max(left);
-        if (!(bound > kMinusInf)) break;
-        const unsigned who = __ballot_sync(kAll, left == bound);
-        if (lane == __ffs(who) - 1) left = kMinusInf;
-    }
+    // the k-th largest of the lanes' maxima: the least of those that fewer than k
+    // others exceed; any key there is, if there are fewer lanes than k with one
+    int larger = 0;
+#pragma unroll
+    for (int o = 1; o < LANES; ++o) larger += __shfl_xor_sync(kAll, top, o) > top;
+    const float least = -team_max<LANES>(larger < k ? -top : kMinusInf);
+    const float bound = k <= LANES ? fmaxf(least, -kLargest) : -kLargest;
     // gathered in the order of the lanes and their slots, which is that of the experts
     unsigned in = 0;
 #pragma unroll
-    for (int s = 0; s < SLOTS; ++s)
-        in |= (key[s] >= bound && key[s] > kMinusInf ? 1u : 0u) << s;
+    for (int s = 0; s < SLOTS; ++s) in |= (key[s] >= bound ? 1u : 0u) << s;
     const int own = __popc(in);
     int upto = own;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(kAll, upto, o);
-        if (lane >= o) upto += v;
+    for (int o = 1; o < LANES; o <<= 1) {
+        const int v = __shfl_up_sync(kAll, upto, o, LANES);
+        if (l >= o) upto += v;
     }
-    const int count = __shfl_sync(kAll, upto, 31);
-    if (count <= 32) {
+    const int count = __shfl_sync(kAll, upto, LANES - 1, LANES);
+    const int most = __reduce_max_sync(kAll, count);
+    if (most <= kBench) {
         int at = upto - own;
 #pragma unroll
         for (int s = 0; s < SLOTS; ++s)
             if (in >> s & 1u) {
                 bench.key[at] = key[s];
                 bench.score[at] = score[s];
-                bench.id[at] = lane * SLOTS + s;
+                bench.id[at] = l * SLOTS + s;
                 ++at;
             }
         __syncwarp();
-        // rank: how many are larger, or equal and before it
-        const float mine = bench.key[lane];
-        int rank = 0;
-        for (int i = 0; i < count; i += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(bench.key + i);
-            rank += v.x > mine || (v.x == mine && i < lane);
-            rank += v.y > mine || (v.y == mine && i + 1 < lane);
-            rank += v.z > mine || (v.z == mine && i + 2 < lane);
-            rank += v.w > mine || (v.w == mine && i + 3 < lane);
-        }
-        if (lane < count && rank < k) {
-            bench.chosen[rank] = bench.id[lane];
-            bench.chosen_score[rank] = bench.score[lane];
+        for (int c = l; c - l < most; c += LANES) {
+            // rank: how many are larger, or equal and before it
+            const float mine = c < kBench ? bench.key[c] : kMinusInf;
+            int rank = 0;
+            for (int i = 0; i < most; i += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(bench.key + i);
+                rank += v.x > mine || (v.x == mine && i < c);
+                rank += v.y > mine || (v.y == mine && i + 1 < c);
+                rank += v.z > mine || (v.z == mine && i + 2 < c);
+                rank += v.w > mine || (v.w == mine && i + 3 < c);
+            }
+            if (c < count && rank < k) {
+                bench.chosen[rank] = bench.id[c];
+                bench.chosen_score[rank] = bench.score[c];
+            }
         }
     } else {
         // many ties, or k near the number of lanes: one key a round
+        const int base = threadIdx.x & 31 & ~(LANES - 1);
         for (int i = 0; i < k; ++i) {
             float m = key[0];
 #pragma unroll
             for (int s = 1; s < SLOTS; ++s) m = fmaxf(m, key[s]);
-            const float best = warp_max(m);
-            if (!(best > kMinusInf)) break;
-            const unsigned who = __ballot_sync(kAll, m == best);
-            if (lane != __ffs(who) - 1) continue;
-            bool done = false;
+            const float best = team_max<LANES>(m);
+            const unsigned who = __ballot_sync(kAll, m == best) >> base;
+            bool mine = best > kMinusInf && l == __ffs(who) - 1;
 #pragma unroll
             for (int s = 0; s < SLOTS; ++s)
-                if (!done && key[s] == best) {
-                    bench.chosen[i] = lane * SLOTS + s;
+                if (mine && key[s] == best) {
+                    bench.chosen[i] = l * SLOTS + s;
                     bench.chosen_score[i] = score[s];
                     key[s] = kMinusInf;
-                    done = true;
+                    mine = false;
                 }
         }
     }
     __syncwarp();
 }
 
-template <int SLOTS, bool BF16>
-__global__ void __launch_bounds__(kThreads, SLOTS <= 8 ? 4 : 1)
+template <int SLOTS, int LANES, bool BF16>
+__global__ void __launch_bounds__(kThreads)
     route_topk_kernel(const void* __restrict__ logits, const float* __restrict__ bias,
                       int32_t* __restrict__ ids, float* __restrict__ weights,
                       int32_t* __restrict__ counts, int64_t T, int64_t ld, RouteShape sh,
-                      bool wide, int lanes) {
-    extern __shared__ float shared[];
-    __shared__ Bench benches[kWarps];
+                      bool wide, int group_lanes) {
+    constexpr int kTokens = 32 / LANES;  // of a warp
+    constexpr int kPitch = SLOTS + 4;    // of a lane's biases: vectors in different banks
+    extern __shared__ __align__(16) float shared[];
+    __shared__ Bench benches[kWarps * kTokens];
+    __shared__ __align__(16) float biases[LANES * kPitch];
     grid_dependency_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    Bench& bench = benches[warp];
-    int32_t* tally = reinterpret_cast<int32_t*>(shared);           // [E], when counts are wanted
-    float* keys = shared + (counts ? sh.E : 0) + warp * sh.E;      // [E] a warp, when lanes == 0
-    if (counts) {
+    const int l = lane % LANES, team = warp * kTokens + lane / LANES;
+    Bench& bench = benches[team];
+    int32_t* tally = reinterpret_cast<int32_t*>(shared);               // [E], when counts are wanted
+    float* keys = shared + (counts ? sh.E : 0) + team * (sh.E + 32);   // when group_lanes == 0
+    if (counts)
         for (int e = threadIdx.x; e < sh.E; e += kThreads) tally[e] = 0;
-        __syncthreads();
-    }
-    const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
-    int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps * kTokens;
+    int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps * kTokens + team;
     grid_dependency_wait();
-    float b[SLOTS];
-#pragma unroll
-    for (int s = 0; s < SLOTS; ++s) {
-        const int e = lane * SLOTS + s;
-        b[s] = bias && e < sh.E ? ld_ro(bias + e) : 0.0f;
+    // a bias of NaN takes its expert out as -inf does
+    for (int e = threadIdx.x; e < LANES * SLOTS; e += kThreads) {
+        const float b = bias && e < sh.E ? ld_ro(bias + e) : 0.0f;
+        biases[e / SLOTS * kPitch + e % SLOTS] = b > kMinusInf ? b : kMinusInf;
     }
+    __syncthreads();
     Raw<SLOTS, BF16> raw;
     raw.clear();
-    if (t < T) raw.load(row_of<BF16>(logits, t, ld), lane, sh.E, wide);
-    for (; t < T; t += step) {
+    if (t < T) raw.load(row_of<BF16>(logits, t, ld), l, sh.E, wide);
+    // a warp's tokens go together: the first lane's token says whether there is one
+    for (int64_t t0 = t - lane / LANES; t0 < T; t0 += step, t += step) {
         float x[SLOTS], p[SLOTS];
         raw.values(x);
-        if (t + step < T) raw.load(row_of<BF16>(logits, t + step, ld), lane, sh.E, wide);
-        scores_of<SLOTS>(x, sh.sigmoid, p);
+        if (t + step < T) raw.load(row_of<BF16>(logits, t + step, ld), l, sh.E, wide);
+        scores_of<SLOTS, LANES>(x, sh.sigmoid, p);
 #pragma unroll
-        for (int s = 0; s < SLOTS; ++s) {
-            const float key = p[s] + b[s];
-            x[s] = x[s] > kMinusInf && key > kMinusInf ? key : kMinusInf;  // NaN: a bias of NaN
+        for (int s = 0; s < SLOTS; s += 4) {
+            const float4 b = *reinterpret_cast<const float4*>(biases + l * kPitch + s);
+            x[s] = x[s] > kMinusInf ? p[s] + b.x : kMinusInf;
+            x[s + 1] = x[s + 1] > kMinusInf ? p[s + 1] + b.y : kMinusInf;
+            x[s + 2] = x[s + 2] > kMinusInf ? p[s + 2] + b.z : kMinusInf;
+            x[s + 3] = x[s + 3] > kMinusInf ? p[s + 3] + b.w : kMinusInf;
         }
-        if (sh.groups > 1) keep_groups<SLOTS>(x, sh, lane, lanes, keys);
-        bench.key[lane] = kMinusInf;
-        bench.chosen[lane] = -1;
-        bench.chosen_score[lane] = 0.0f;
+        if (sh.groups > 1) keep_groups<SLOTS, LANES>(x, sh, l, group_lanes, keys);
+        bench.clear<LANES>(l);
         __syncwarp();
-        choose<SLOTS>(x, p, sh.k, lane, bench);
+        choose<SLOTS, LANES>(x, p, sh.k, l, bench);
 
-        const int id = bench.chosen[lane];
-        float w = lane < sh.k ? bench.chosen_score[lane] : 0.0f;
-        if (sh.renorm) {
-            const float total = warp_sum(w);
-            w = total > 0.0f ? __fdiv_rn(w, total) : 0.0f;
-        }
-        if (lane < sh.k) {
-            st_plain(ids + t * sh.k + lane, id);
-            st_plain(weights + t * sh.k + lane, w * sh.scale);
-            if (counts && id >= 0) atomicAdd(tally + id, 1);
-        }
+        float total = 0.0f;
+        for (int i = l; i < sh.k; i += LANES) total += bench.chosen_score[i];
+        total = team_sum<LANES>(total);
+        if (t < T)
+            for (int i = l; i < sh.k; i += LANES) {
+                const int id = bench.chosen[i];
+                float w = bench.chosen_score[i];
+                if (sh.renorm) w = total > 0.0f ? __fdiv_rn(w, total) : 0.0f;
+                st_plain(ids + t * sh.k + i, id);
+                st_plain(weights + t * sh.k + i, w * sh.scale);
+                if (counts && id >= 0) atomicAdd(tally + id, 1);
+            }
         __syncwarp();
     }
     if (counts) {
@@ -481,7 +547,7 @@ __global__ void __launch_bounds__(kThreads)
             float x[SLOTS], p[SLOTS];
             raw.values(x);
             load(t + step);
-            scores_of<SLOTS>(x, false, p);
+            scores_of<SLOTS, 32>(x, false, p);
             put_row<SLOTS>(row, lane, p);
             __syncwarp();
             const float score = id >= 0 ? row[id] : 0.0f;
@@ -502,15 +568,41 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
-// Registers for E logits a lane: the next power of two of E / 32.
+// The backward's registers for E logits a lane: the next power of two of E / 32.
 template <typename F>
 cudaError_t with_slots(int E, F&& f) {
-    if (E <= 32) return f(std::integral_constant<int, 1>());
-    if (E <= 64) return f(std::integral_constant<int, 2>());
-    if (E <= 128) return f(std::integral_constant<int, 4>());
-    if (E <= 256) return f(std::integral_constant<int, 8>());
-    if (E <= 512) return f(std::integral_constant<int, 16>());
-    return f(std::integral_constant<int, 32>());
+    using std::integral_constant;
+    if (E <= 32) return f(integral_constant<int, 1>());
+    if (E <= 64) return f(integral_constant<int, 2>());
+    if (E <= 128) return f(integral_constant<int, 4>());
+    if (E <= 256) return f(integral_constant<int, 8>());
+    if (E <= 512) return f(integral_constant<int, 16>());
+    return f(integral_constant<int, 32>());
+}
+// The forward's slots and lanes a token.  Fewer lanes share a warp's instructions
+// among more tokens, but the bound that `choose` starts from, the k-th largest of
+// the lanes' maxima, is near only while the searched experts fill 2 k lanes: the
+// fewest lanes, of up to 16 logits each, of which that holds.  Up to 32 experts
+// all of them may be gathered.  65536 tokens, 8 of 256: 38 us with 16 lanes, 53 us
+// with 32; 16 of 256: 97 us and 54 us; 8 of 64: 28 us with 8, 21 us with 16.
+template <typename F>
+cudaError_t with_lanes(const RouteShape& sh, F&& f) {
+    using std::integral_constant;
+    constexpr integral_constant<int, 4> c4;
+    constexpr integral_constant<int, 8> c8;
+    constexpr integral_constant<int, 16> c16;
+    constexpr integral_constant<int, 32> c32;
+    const int E = sh.E;
+    // whether the searched experts fill 2 k lanes, `slots` each
+    const auto fill = [&](int slots) {
+        return E * sh.topk_groups >= 2 * sh.k * slots * sh.groups;
+    };
+    if (E <= 32) return f(c4, c8);
+    if (E <= 64) return fill(8) ? f(c8, c8) : f(c4, c16);
+    if (E <= 128) return fill(16) ? f(c16, c8) : fill(8) ? f(c8, c16) : f(c4, c32);
+    if (E <= 256) return fill(16) ? f(c16, c16) : f(c8, c32);
+    if (E <= 512) return f(c16, c32);
+    return f(c32, c32);
 }
 
 }  // namespace
@@ -518,21 +610,23 @@ cudaError_t with_slots(int E, F&& f) {
 cudaError_t launch_route_topk(const void* logits, const float* bias, int32_t* ids, float* weights,
                               int32_t* counts, int64_t T, int64_t ld, const RouteShape& sh,
                               cudaStream_t stream) {
-    return with_slots(sh.E, [&](auto slots) {
-        constexpr int S = decltype(slots)::value;
-        auto* k = sh.bf16 ? &route_topk_kernel<S, true> : &route_topk_kernel<S, false>;
+    return with_lanes(sh, [&](auto slots, auto lanes) {
+        constexpr int S = decltype(slots)::value, L = decltype(lanes)::value;
+        constexpr int kTokens = kWarps * 32 / L;  // of a CTA
+        auto* k = sh.bf16 ? &route_topk_kernel<S, L, true> : &route_topk_kernel<S, L, false>;
         const bool wide = sh.bf16 ? wide_rows<S, true>(logits, ld, sh.E)
                                   : wide_rows<S, false>(logits, ld, sh.E);
         // lanes of a group, when groups are runs of a power of two of them
         const int per = sh.E / sh.groups;
-        int lanes = per % S == 0 ? per / S : 0;
-        if (lanes & (lanes - 1)) lanes = 0;
-        const size_t smem = 4u * sh.E * ((counts ? 1 : 0) + (sh.groups > 1 && !lanes ? kWarps : 0));
+        int group_lanes = per % S == 0 ? per / S : 0;
+        if (group_lanes & (group_lanes - 1)) group_lanes = 0;
+        const size_t smem =
+            4u * ((counts ? sh.E : 0) + (sh.groups > 1 && !group_lanes ? kTokens * (sh.E + 32) : 0));
         const int grid = persistent_grid(reinterpret_cast<const void*>(k), kThreads, smem,
-                                         (T + kWarps - 1) / kWarps);
+                                         (T + kTokens - 1) / kTokens);
         if (const cudaError_t e = upload_checks(stream)) return e;
         return launch_pdl(k, grid, kThreads, smem, stream, true, logits, bias, ids, weights,
-                          counts, T, ld, sh, wide, lanes);
+                          counts, T, ld, sh, wide, group_lanes);
     });
 }
 

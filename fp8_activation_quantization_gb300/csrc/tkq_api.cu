@@ -235,8 +235,8 @@ int persistent_grid(const void* kernel, int threads, size_t smem, int64_t blocks
         if (it != g_occ.end()) per_sm = it->second;
     }
     if (per_sm == 0) {
-        // 48 KB, a kernel's static shared memory among them, need no permission
-        if (smem > 40 * 1024) {
+        // 48 KB need no permission, a kernel's static shared memory (33 KB at most) among them
+        if (smem > 14 * 1024) {
             // the limit only goes up: a kernel may be launched with several sizes
             std::lock_guard<std::mutex> lock(g_occ_mutex);
             size_t& limit = g_smem_limit[OccKey{kernel, dev, 0, 0}];

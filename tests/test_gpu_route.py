@@ -152,6 +152,19 @@ def test_ties_go_to_the_lowest_index(cuda_device):
         _check_forward(x, cuda_device, kind, 12, groups=12, topk_groups=3)
 
 
+@pytest.mark.parametrize("E,k,groups", [(256, 8, 1), (256, 8, 8), (128, 4, 1), (64, 4, 1), (64, 8, 4),
+                                        (32, 32, 1), (200, 3, 5)])
+def test_rows_of_all_kinds_side_by_side(cuda_device, E, k, groups):
+    """Neighbouring tokens, which may share a warp, with nothing in common: all logits equal (more
+    ties than are gathered), ordinary, a few experts only, none."""
+    x = _logits(E, 41, dict(E=E, kind="sigmoid", groups=groups), torch.float32)
+    x[::4] = 0.25
+    x[1::4, 3:] = -INF
+    x[3::8] = -INF
+    for kind in ("softmax", "sigmoid"):
+        _check_forward(x, cuda_device, kind, k, groups=groups, topk_groups=max(1, groups // 2))
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_strided_and_odd_addresses(cuda_device, dtype):
     """Logits as columns of a wider matrix, from an odd element on."""
