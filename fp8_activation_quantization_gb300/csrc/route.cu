@@ -61,10 +61,11 @@ __device__ __forceinline__ float team_max(float v) {
         float r;
         asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
         return r;
-    }
+    } else {
 #pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
-    return v;
+        for (int o = LANES / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+        return v;
+    }
 }
 
 // A lane's logits as loaded.  `wide`: rows and E allow loads of a lane's logits

@@ -201,7 +201,8 @@ __global__ void __launch_bounds__(kThreads, 4)
 // A row belongs to `team` consecutive warps of a CTA (1, 2, 4 or 8), which take
 // its units of four groups in turn, so that dw[t] is one lane's running sum,
 // five shuffles and, for teams of several warps, one exchange through shared
-// memory, always in the same order.
+// memory, always in the same order.  Rows of one or two groups go four or two
+// (`pack`) to a warp, so that its lanes are filled.
 template <int CKPT>
 __device__ __forceinline__ void decode16(const uint4& q, float s, float* v) {
     decode4<CKPT>(q.x, v);
@@ -264,14 +265,18 @@ __global__ void __launch_bounds__(kThreads, 3)
     const int sub = lane >> 3, k = lane & 7;
     const int GH = static_cast<int>(H / 128);
     const int member = warp & (team - 1);      // the warp's place in its team
-    const int teams = kWarps / team;           // rows a CTA takes at a time
+    const int teams = kWarps / team;           // (packs of) rows a CTA takes at a time
+    const int pack = GH == 1 ? 4 : GH == 2 ? 2 : 1;
+    const int j0 = pack > 1 ? sub % GH : sub;     // the lane's group in a unit,
+    const int in_pack = pack > 1 ? sub / GH : 0;  // its row in a pack
     const int64_t step = static_cast<int64_t>(gridDim.x) * teams;
     // units of the rows that hold data; a member of a team that is larger than
     // the row's units has none
-    RowWalk ahead = {static_cast<int64_t>(blockIdx.x) * teams + warp / team, member * 4};
+    const int64_t first = (static_cast<int64_t>(blockIdx.x) * teams + warp / team) * pack + in_pack;
+    RowWalk ahead = {first, member * 4};
     if (ahead.u0 >= GH) ahead.t = T;
     const auto fetch = [&](int stage) {
-        const int j = ahead.u0 + sub;
+        const int j = ahead.u0 + j0;
         if (ahead.t < T && j < GH) {
             // a row of codes, and one of dy, is H / 8 pieces, one of scales H / 64
             const int64_t row = ahead.t * (H / 8);
@@ -284,17 +289,18 @@ __global__ void __launch_bounds__(kThreads, 3)
             cp_async4(&slots.scale[stage][1][tid], ps + GH);
         }
         cp_async_commit();
-        ahead.next(member, team, GH, step);
+        ahead.next(member, team, GH, step * pack);
     };
     grid_dependency_wait();
     for (int d = 0; d < kDepth - 1; ++d) fetch(d);
     int stage = 0, free_stage = kDepth - 1;
     const auto weight = [&](int64_t t) { return w && t < T ? ld_ro(w + t) : 1.0f; };
-    float w_next = weight(static_cast<int64_t>(blockIdx.x) * teams + warp / team);
-    for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * teams; t0 < rows_walk; t0 += step) {
-        const int64_t t = t0 + warp / team;
+    float w_next = weight(first);
+    int64_t t = first;
+    for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * teams * pack; t0 < rows_walk;
+         t0 += step * pack, t += step * pack) {
         const float wt = w_next;
-        w_next = weight(t + step);
+        w_next = weight(t + step * pack);
         const bool row = t < T;
         float2 dot = make_float2(0.0f, 0.0f);
         // the row's first piece of codes (and of y), and of bf16 gradients
@@ -303,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 3)
             cp_async_wait(kDepth - 1);
             __syncwarp();
             fetch(free_stage);
-            const int j = u0 + sub;
+            const int j = u0 + j0;
             const bool in_row = j < GH && t < rows_walk, live = row && j < GH;
             // a group without data computes on what its slots hold; nothing of it is used
             float gv[16], uv[16], dv[16];
@@ -335,10 +341,12 @@ __global__ void __launch_bounds__(kThreads, 3)
                 }
             }
             if (live) dot = add2(dot, unit_dot);
-            if (Y && live) {
-                uint4* py = y + row_at + (j * 16 + k * 2);
-                st_stream(py, make_uint4(yv[0], yv[1], yv[2], yv[3]));
-                st_stream(py + 1, make_uint4(yv[4], yv[5], yv[6], yv[7]));
+            if constexpr (Y) {
+                if (live) {
+                    uint4* py = y + row_at + (j * 16 + k * 2);
+                    st_stream(py, make_uint4(yv[0], yv[1], yv[2], yv[3]));
+                    st_stream(py + 1, make_uint4(yv[4], yv[5], yv[6], yv[7]));
+                }
             }
             if constexpr (OUT == kBf16Out) {
                 if (live) {
@@ -369,8 +377,7 @@ __global__ void __launch_bounds__(kThreads, 3)
         }
         if (dw) {
             float sum = dot.x + dot.y;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+            for (int o = 16 / pack; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
             if (team > 1) {
                 __syncthreads();  // the sums of the rows before have been read
                 if (lane == 0) part[warp] = sum;
@@ -378,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 3)
                 sum = 0.0f;
                 for (int i = 0; i < team; ++i) sum += part[warp - member + i];
             }
-            if (lane == 0 && member == 0 && row) st_plain(dw + t, sum);
+            if (lane % (32 / pack) == 0 && member == 0 && row) st_plain(dw + t, sum);
         }
     }
 }
@@ -430,11 +437,12 @@ cudaError_t launch_swiglu_restore(const void* ckpt, const float* ckpt_sf, const 
     const int64_t rows = out_kind != kBf16Out && (sf_flags & kSfColMajor) ? lay.rows4 : T;
     // as many warps a row as it takes to give every SM some, up to its units
     const int64_t units = (H / 128 + 3) / 4;
+    const int64_t packs = H == 128 ? (rows + 3) / 4 : H == 256 ? (rows + 1) / 2 : rows;
     int team = 1;
     while (team < kWarps && team < units && rows * team < int64_t{num_sms()} * 3 * kWarps) team *= 2;
     const auto launch = [&](auto* k, size_t smem) {
         const int grid = persistent_grid(reinterpret_cast<const void*>(k), kThreads, smem,
-                                         (rows * team + kWarps - 1) / kWarps);
+                                         (packs * team + kWarps - 1) / kWarps);
         if (const cudaError_t e = upload_checks(stream)) return e;
         return launch_pdl(k, grid, kThreads, smem, stream, true,
                           static_cast<const uint4*>(ckpt), ckpt_sf, static_cast<const uint4*>(dy),
