@@ -265,11 +265,12 @@ constexpr int kBackwardThreadsPerSm = 768;  // narrow rows, of about 80 register
 }  // namespace
 
 // Partial rows a backward launch writes at most: one a CTA, as many CTAs an SM
-// as its threads allow, no more than rows.
+// as its threads allow, no more than rows.  The caller's workspace is sized by
+// this, so it must not change between that and the launch.
 int64_t residual_norm_parts(int64_t T, int64_t C) {
     const int nv = backward_kind(C, true).nv;  // the kind with the fewer threads
     const int64_t per_sm = 1024 / shape_of(C, nv, kBackwardThreadsPerSm, 1, 1).threads;
-    const int64_t most = num_sms() * (per_sm < 16 ? per_sm : 16);
+    const int64_t most = device_sms() * (per_sm < 16 ? per_sm : 16);
     return T < most ? T : most;
 }
 

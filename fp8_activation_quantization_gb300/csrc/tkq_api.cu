@@ -59,13 +59,9 @@ Range span(const void* p, int64_t bytes) {
 bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
 }  // namespace
 
-int num_sms() {
+int device_sms() {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 1;
-    if (const char* env = std::getenv("TKQ_NUM_SMS")) {
-        const int v = std::atoi(env);
-        if (v > 0) return v;
-    }
     if (dev < kMaxDevices) {
         int v = g_sms[dev].load(std::memory_order_relaxed);
         if (v > 0) return v;
@@ -75,6 +71,14 @@ int num_sms() {
         v = 1;
     if (dev < kMaxDevices) g_sms[dev].store(v, std::memory_order_relaxed);
     return v;
+}
+
+int num_sms() {
+    if (const char* env = std::getenv("TKQ_NUM_SMS")) {
+        const int v = std::atoi(env);
+        if (v > 0) return v;
+    }
+    return device_sms();
 }
 
 bool swiglu_flat_chosen(int64_t T, int64_t H, bool weighted) {

@@ -19,6 +19,8 @@ bool encode_bf16_2d(CUtensorMap* map, const void* base, int64_t cols, int64_t ro
 // Number of SMs of the current device (cached per device; the environment
 // variable TKQ_NUM_SMS overrides it for grid sizing experiments).
 int num_sms();
+// The same without the override: what a caller's buffer is sized by.
+int device_sms();
 
 // Address of the library's device status word on the current device (bit
 // kDeviceTimeout: a bounded wait inside a kernel gave up).  Resolved once per

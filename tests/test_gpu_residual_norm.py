@@ -258,6 +258,25 @@ def test_repeats_bit_for_bit(cuda_device):
             assert all(torch.equal(_bytes(x), _bytes(y)) for x, y in zip(first, got))
 
 
+def test_workspace_does_not_depend_on_the_grid_override(cuda_device, monkeypatch):
+    """The environment variable that sizes grids for another number of SMs changes neither the
+    workspace a caller has to bring nor, but for the order of the weight sums, the results."""
+    T, C = 700, 1024
+    _, dev = _inputs(2, T, C, False, True, True, True, cuda_device)
+    dx = torch.randn(T, C, device=cuda_device).bfloat16()
+    r1, _, _, _, p, q = tkq.residual_norm_and_cast(**dev)
+    args = (dx, r1, dev["h"], dx, dev["w_post"], dev["gate"], dev["w_pre"], p, q)
+    ref, size = tkq.residual_norm_backward(*args), tkq.tkq_residual_norm_workspace(T, C)
+    for sms in ("3", "1000"):
+        monkeypatch.setenv("TKQ_NUM_SMS", sms)
+        assert tkq.tkq_residual_norm_workspace(T, C) == size
+        got = tkq.residual_norm_backward(*args)
+        for a, b in zip(ref[:3], got[:3]):
+            assert torch.equal(_bytes(a), _bytes(b))
+        for a, b in zip(ref[3:], got[3:]):      # the same terms in another order
+            assert (a - b).abs().le(2 * (T + 100) * U * a.abs().max()).all()
+
+
 def test_offsets_beyond_32_bits(cuda_device):
     T, C, n = 140001, 16384, 21
     _, dev = _inputs(1, n, C, False, True, True, True, cuda_device)
