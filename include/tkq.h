@@ -457,7 +457,9 @@ tkq_status tkq_residual_norm_cast(const void* r, const void* h, const float* w_p
  *   dr_out  : [T, C] of the stream's type;  dh, dgate : bf16 [T, C], given
  *             exactly with h and gate;  dw_post, dw_pre : fp32 [C] or NULL
  *   workspace : tkq_residual_norm_workspace(T, C) bytes, 16-byte aligned
- *             (NULL when no weight gradient is asked for)
+ *             (NULL when no weight gradient is asked for); the size is that for
+ *             the device current at the call, and TKQ_NUM_SMS does not change
+ *             it.  Its length is not passed, so a shorter one is not noticed
  * Sums over rows are taken in a fixed order: results repeat bit for bit on one
  * kind of GPU.  T == 0 launches nothing (the weight gradients are not written).
  */

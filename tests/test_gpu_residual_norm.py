@@ -277,6 +277,39 @@ def test_workspace_does_not_depend_on_the_grid_override(cuda_device, monkeypatch
             assert (a - b).abs().le(2 * (T + 100) * U * a.abs().max()).all()
 
 
+@pytest.mark.parametrize("asked,launched", [("3", None), (None, "1000"), ("3", "1000")])
+def test_workspace_sized_under_another_override(asked, launched, cuda_device, monkeypatch):
+    """A workspace of the size that was asked for is enough when the override changes before the
+    launch: more rows than the device has partial rows, and the bytes behind it stay as they were."""
+    def override(value):
+        if value is None:
+            monkeypatch.delenv("TKQ_NUM_SMS", raising=False)
+        else:
+            monkeypatch.setenv("TKQ_NUM_SMS", value)
+    T, C, guard = 5000, 1024, 1 << 16
+    dx = torch.randn(T, C, device=cuda_device).bfloat16()
+    r = torch.randn(T, C, device=cuda_device).bfloat16()
+    q = torch.rand(T, device=cuda_device) + 0.5
+    override(None)
+    _, _, _, _, ref = tkq.residual_norm_backward(None, r, dx=dx, w_pre=torch.ones(C, device=cuda_device),
+                                                 rstd_pre=q)
+    override(asked)
+    size = tkq.tkq_residual_norm_workspace(T, C)
+    assert size < T * 2 * C * 4
+    work = torch.full((size + guard,), 0xA5, dtype=torch.uint8, device=cuda_device)
+    w, dr, dw = torch.ones(C, device=cuda_device), torch.empty_like(r), torch.empty(C, device=cuda_device)
+    override(launched)
+    st = tkq.tkq_residual_norm_backward(
+        None, dx.data_ptr(), r.data_ptr(), None, None, None, w.data_ptr(), None, q.data_ptr(),
+        dr.data_ptr(), None, None, None, dw.data_ptr(), work.data_ptr(), T, C, tkq.NORM_PRE, 1.0,
+        torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert st == 0 and (work[size:] == 0xA5).all()
+    # the same terms in another order: one u for each row, of the sum of magnitudes
+    terms = (dx.double() * r.double() * q.double()[:, None]).abs().sum(0)
+    assert ((dw - ref).abs().double() <= 2 * (T + 160) * U * terms).all()
+
+
 def test_offsets_beyond_32_bits(cuda_device):
     T, C, n = 140001, 16384, 21
     _, dev = _inputs(1, n, C, False, True, True, True, cuda_device)
