@@ -536,6 +536,7 @@ __global__ void __launch_bounds__(kThreads)
                     x = ld_ro(static_cast<const float*>(from) + id);
                 x = x > kMinusInf ? fminf(x, kLargest) : kMinusInf;
             }
+            if (x == kMinusInf) a = 0.0f;  // an absent expert: an empty slot
             load(t + step);
             for (int e = lane * 4; e < length; e += 128)
                 *reinterpret_cast<float4*>(row + e) = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -552,6 +553,7 @@ __global__ void __launch_bounds__(kThreads)
             put_row<SLOTS>(row, lane, p);
             __syncwarp();
             const float score = id >= 0 ? row[id] : 0.0f;
+            if (!(score > 0.0f)) a = 0.0f;  // an absent expert: an empty slot
             a = score_grad(a, score, sh.renorm);
             d = id >= 0 ? a * score : 0.0f;
             const float dot = warp_sum(d);

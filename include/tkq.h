@@ -365,7 +365,8 @@ tkq_status tkq_route_topk(const void* logits, const float* bias, int32_t* ids, f
  * a_i = scale * dweights[t, i], p_i the chosen scores and S their sum,
  *   ds_i = a_i, or with TKQ_ROUTE_RENORM (a_i - sum_j a_j p_j / S) / S  (0 if S = 0)
  *   dlogits = ds s (1 - s)  (sigmoid)   or   s (ds - sum_j ds_j s_j)  (softmax)
- * and 0 for absent experts.  An id outside [0, E) is an empty slot.
+ * and 0 for absent experts.  An id outside [0, E), or of an absent expert, is an
+ * empty slot: its dweights, of whatever value, count for nothing.
  *   logits : [T, E] as above;  ids : int32 [T, k];  dweights : fp32 [T, k];
  *   dlogits : [T, E], contiguous, of the logits' type
  */
