@@ -8,9 +8,12 @@
 // and no weight.
 //   score_e = 1 / (1 + exp(-x_e))           or  exp(x_e - m) / sum_j exp(x_j - m)
 //   w_i     = scale * score_(e_i) [/ sum_j score_(e_j)]
-// Backward, with a_i = scale * dw_i, p_i the chosen scores and S their sum:
-//   ds_i = a_i,  or renormalised  (a_i - sum_j a_j (p_j / S)) / S
-//   dx_e = ds_e s_e (1 - s_e)               or  s_e (ds_e - sum_j ds_j s_j)
+// Backward, with a_i = scale * dw_i, p_i the chosen scores, S their sum, r_i = p_i / S:
+//   dx_e = a_e s_e (1 - s_e)                or  s_e (a_e - sum_j a_j p_j), renormalised
+//   dx_e = (a_e - sum_j a_j r_j) r_e [(1 - s_e)]  of the chosen, 0 elsewhere: the
+// sum over the experts that the softmax's gradient takes off is then 0.  The r_i
+// come from the chosen logits alone, by the distance from the largest of them, so
+// that they hold where the scores themselves underflow.
 //
 // An expert is absent from a token's row when its logit is -inf or NaN: it has
 // no share in the softmax, is never chosen and gets no gradient.  When fewer
@@ -447,14 +450,44 @@ __device__ __forceinline__ void store_row(void* out, const float* row, int E, in
     }
 }
 
-// ds of the lane's slot from a = scale * dweight and the chosen scores; by the
-// weights p / S, which are exactly 1 for a single expert: its gradient is 0.
-__device__ __forceinline__ float score_grad(float a, float score, bool renorm) {
-    if (!renorm) return a;
-    const float total = warp_sum(score);
-    const float r = total > 0.0f ? __fdiv_rn(score, total) : 0.0f;
-    const float dot = warp_sum(a * r);
-    return total > 0.0f ? __fdiv_rn(a - dot, total) : 0.0f;
+// The chosen expert's logit, as values() gives it; -inf for an empty slot.
+template <bool BF16>
+__device__ __forceinline__ float logit_of(const void* row, int id) {
+    if (id < 0) return kMinusInf;
+    float x;
+    if constexpr (BF16)
+        x = __uint_as_float(static_cast<uint32_t>(ld_ro(static_cast<const uint16_t*>(row) + id)) << 16);
+    else
+        x = ld_ro(static_cast<const float*>(row) + id);
+    return x > kMinusInf ? fminf(x, kLargest) : kMinusInf;
+}
+
+// A score up to a factor that all chosen experts share, `lead` their largest
+// score_lead: exp(x - lead), times 1 / (1 + exp(-|x|)) for the sigmoid.  Of order
+// one for the largest, however small the scores are.
+__device__ __forceinline__ float score_lead(float x, bool sigmoid) {
+    return sigmoid ? fminf(x, 0.0f) : x;
+}
+__device__ __forceinline__ float score_ratio(float x, bool sigmoid, float lead) {
+    if (!(x > kMinusInf)) return 0.0f;
+    const float e = expf(score_lead(x, sigmoid) - lead);
+    return sigmoid ? e * rcp_approx(1.0f + expf(-fabsf(x))) : e;
+}
+
+// Gradient of the lane's chosen logit from a = scale * dweight.  A single
+// renormalised expert has r = 1 exactly, and the gradient 0.
+__device__ __forceinline__ float chosen_grad(float a, float x, const RouteShape& sh) {
+    if (!sh.renorm) {  // the sigmoid: s (1 - s), without cancellation
+        const float q = expf(-fabsf(x)), r = rcp_approx(1.0f + q);
+        return a * q * r * r;
+    }
+    const float part = score_ratio(x, sh.sigmoid, team_max<32>(score_lead(x, sh.sigmoid)));
+    const float total = warp_sum(part);
+    const float share = total > 0.0f ? __fdiv_rn(part, total) : 0.0f;
+    const float d = (a - warp_sum(a * share)) * share;
+    if (!sh.sigmoid) return d;
+    const float q = expf(-fabsf(x)), r = rcp_approx(1.0f + q);
+    return d * (x > 0.0f ? q * r : r);  // 1 - s
 }
 
 // Adds v to row[id] for every lane with id >= 0; an id given more than once adds
@@ -493,7 +526,8 @@ __device__ __forceinline__ void put_row(float* row, int lane, const float (&v)[S
     }
 }
 
-template <int SLOTS, bool BF16, bool SIGMOID>
+// CHOSEN: only the chosen logits count (the sigmoid, renormalised weights).
+template <int SLOTS, bool BF16, bool CHOSEN>
 __global__ void __launch_bounds__(kThreads)
     route_backward_kernel(const void* __restrict__ logits, const int32_t* __restrict__ ids,
                           const float* __restrict__ dweights, void* __restrict__ dlogits,
@@ -501,7 +535,7 @@ __global__ void __launch_bounds__(kThreads)
     extern __shared__ __align__(16) float shared[];
     grid_dependency_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int length = row_length(sh.E, SIGMOID ? 0 : SLOTS);
+    const int length = row_length(sh.E, CHOSEN ? 0 : SLOTS);
     float* row = shared + warp * length;
     const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
     int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
@@ -512,7 +546,7 @@ __global__ void __launch_bounds__(kThreads)
     raw.clear();
     const auto load = [&](int64_t at) {
         if (at >= T) return;
-        if constexpr (!SIGMOID) raw.load(row_of<BF16>(logits, at, ld), lane, sh.E, wide);
+        if constexpr (!CHOSEN) raw.load(row_of<BF16>(logits, at, ld), lane, sh.E, wide);
         if (lane < sh.k) {
             next_id = ld_ro(ids + at * sh.k + lane);
             next_a = ld_ro(dweights + at * sh.k + lane);
@@ -524,28 +558,15 @@ __global__ void __launch_bounds__(kThreads)
         const int id = next_id >= 0 && next_id < sh.E ? next_id : -1;
         float a = id >= 0 ? sh.scale * next_a : 0.0f;
         float d = 0.0f;  // what the chosen expert's logit gets beside the row's share
-        if constexpr (SIGMOID) {
-            // only the chosen logits count
-            float x = kMinusInf;
-            if (id >= 0) {
-                const void* from = row_of<BF16>(logits, t, ld);
-                if constexpr (BF16)
-                    x = __uint_as_float(
-                        static_cast<uint32_t>(ld_ro(static_cast<const uint16_t*>(from) + id)) << 16);
-                else
-                    x = ld_ro(static_cast<const float*>(from) + id);
-                x = x > kMinusInf ? fminf(x, kLargest) : kMinusInf;
-            }
+        if constexpr (CHOSEN) {
+            const float x = logit_of<BF16>(row_of<BF16>(logits, t, ld), id);
             if (x == kMinusInf) a = 0.0f;  // an absent expert: an empty slot
             load(t + step);
             for (int e = lane * 4; e < length; e += 128)
                 *reinterpret_cast<float4*>(row + e) = make_float4(0.f, 0.f, 0.f, 0.f);
-            a = score_grad(a, logistic(x), sh.renorm);
-            // s (1 - s) = exp(-|x|) / (1 + exp(-|x|))^2, without cancellation
-            const float q = expf(-fabsf(x)), r = rcp_approx(1.0f + q);
-            d = a * q * r * r;
+            d = chosen_grad(a, x, sh);
         } else {
-            // dx_e = s_e (ds_e - dot): -s_e dot for all, s_e ds_e for the chosen
+            // dx_e = s_e (a_e - dot): -s_e dot for all, s_e a_e for the chosen
             float x[SLOTS], p[SLOTS];
             raw.values(x);
             load(t + step);
@@ -553,9 +574,7 @@ __global__ void __launch_bounds__(kThreads)
             put_row<SLOTS>(row, lane, p);
             __syncwarp();
             const float score = id >= 0 ? row[id] : 0.0f;
-            if (!(score > 0.0f)) a = 0.0f;  // an absent expert: an empty slot
-            a = score_grad(a, score, sh.renorm);
-            d = id >= 0 ? a * score : 0.0f;
+            d = score > 0.0f ? a * score : 0.0f;  // an absent expert: an empty slot
             const float dot = warp_sum(d);
 #pragma unroll
             for (int s = 0; s < SLOTS; ++s) p[s] *= -dot;
@@ -647,8 +666,8 @@ cudaError_t launch_route_topk_backward(const void* logits, const int32_t* ids,
         return launch_pdl(k, grid, kThreads, smem, stream, true, logits, ids, dweights, dlogits, T,
                           ld, sh, wide, wide_out);
     };
-    // the sigmoid's gradient reads the chosen logits alone
-    if (sh.sigmoid)
+    // these gradients read the chosen logits alone
+    if (sh.sigmoid || sh.renorm)
         return sh.bf16 ? launch(&route_backward_kernel<1, true, true>, 0, false)
                        : launch(&route_backward_kernel<1, false, true>, 0, false);
     return with_slots(sh.E, [&](auto slots) {

@@ -363,8 +363,10 @@ tkq_status tkq_route_topk(const void* logits, const float* bias, int32_t* ids, f
  * Gradient of the routing weights with respect to the logits, for the ids a
  * tkq_route_topk call gave (the choice itself has no gradient).  With
  * a_i = scale * dweights[t, i], p_i the chosen scores and S their sum,
- *   ds_i = a_i, or with TKQ_ROUTE_RENORM (a_i - sum_j a_j p_j / S) / S  (0 if S = 0)
+ *   ds_i = a_i, or with TKQ_ROUTE_RENORM (a_i - sum_j a_j p_j / S) / S
  *   dlogits = ds s (1 - s)  (sigmoid)   or   s (ds - sum_j ds_j s_j)  (softmax)
+ * (the shares p_i / S are taken of the chosen logits' distances from the largest of
+ * them, so they are defined where the scores themselves underflow)
  * and 0 for absent experts.  An id outside [0, E), or of an absent expert, is an
  * empty slot: its dweights, of whatever value, count for nothing.
  *   logits : [T, E] as above;  ids : int32 [T, k];  dweights : fp32 [T, k];

@@ -1,13 +1,24 @@
-"""Routing's edges: gradients that meet absent experts."""
+"""Routing where the chosen experts' scores are tiny, against the 64-bit formulas.
+
+A bias, or ids given by the caller, can choose experts whose scores lie far below the smallest binary32
+number, while the renormalised weights, ratios of them, are of order one.
+
+Error bounds, u = 2^-24: a ratio is made of exponentials of differences of logits, each rounded once
+(|difference| u) and 2 ulp off, and then of the same sums, products and divisions as anywhere else, so
+the bounds of test_gpu_route hold with `spread` the largest difference of two logits of a row, here
+without a cap: (2 spread + 64) u of a weight, (2 spread + 96) u of the magnitudes of a gradient's terms."""
 from __future__ import annotations
 
 import pytest
 import torch
 
 import fp8_activation_quantization_gb300 as tkq
+from tests import blocks64 as B
+from tests.test_gpu_route import _grad_bound
 
 pytestmark = pytest.mark.gpu
 
+U = 2.0 ** -24
 INF = float("inf")
 NAN = float("nan")
 
@@ -18,6 +29,62 @@ def _library(cuda_device):
     __graft_entry__.build()
     tkq.load_library()
     yield
+
+
+def _spread(x):
+    x = torch.where(x > -INF, x.double(), NAN)
+    return (x.nan_to_num(-INF).amax(1) - x.nan_to_num(INF).amin(1)).clamp(min=0)[:, None]
+
+
+# how far the chosen logits lie below 0 and below the row's largest logit: scores that are ordinary,
+# subnormal, and no binary32 number at all
+DEPTHS = [20.0, 87.0, 95.0, 101.0, 140.0, 300.0, 600.0]
+
+
+def _low(T, E, seed, dtype):
+    """Rows whose first quarter of experts is near 0 and the rest near -depth (kind softmax), or all
+    near -depth from column E // 4 on; the depth changes from row to row."""
+    gen = torch.Generator().manual_seed(seed)
+    x = torch.randn(T, E, generator=gen)
+    depth = torch.tensor([DEPTHS[t % len(DEPTHS)] for t in range(T)])[:, None]
+    x[:, E // 4:] -= depth
+    return x.to(dtype), gen
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k", [(24, 5), (256, 8), (1000, 32)])
+def test_gradient_of_tiny_scores(cuda_device, dtype, kind, E, k):
+    T = 29
+    x, gen = _low(T, E, E + k, dtype)
+    ids = torch.stack([torch.randperm(E - E // 4, generator=gen)[:k] + E // 4 for _ in range(T)]).int()
+    ids[::5, 1] = -1
+    dw = torch.randn(T, k, generator=gen) * 5
+    for renorm in (True, False):
+        ref = B.route_backward(x.double(), ids, dw.double(), kind, renorm, 1.5)
+        got = tkq.route_topk_backward(x.to(cuda_device), ids.to(cuda_device), dw.to(cuda_device),
+                                      scores=kind, renormalize=renorm, scale=1.5).cpu().double()
+        bound = (2 * _spread(x) + 96) * U * _grad_bound(x.double(), ids, dw.double(), kind, renorm, 1.5)
+        if dtype == torch.bfloat16:
+            bound = bound + 2.0 ** -8 * ref.abs()
+        assert torch.isfinite(got).all()
+        # a non-renormalised gradient may underflow: the smallest normal number times what it is multiplied by
+        assert (got - ref).abs().le(bound + 2.0 ** -120).all()
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+def test_gradient_given_by_hand(cuda_device, kind):
+    x = torch.tensor([[100.0, 5.0, 4.0, 3.0], [0.0, -90.0, -91.0, -92.0]])
+    ids = torch.tensor([[1, 2], [1, 2]], dtype=torch.int32)
+    dw = torch.tensor([[1.0, -1.0], [100.0, -100.0]])
+    got = tkq.route_topk_backward(x.to(cuda_device), ids.to(cuda_device), dw.to(cuda_device), scores=kind)
+    # weights 1 / (1 + e^-1) and its complement: slope w (1 - w) of their difference, twice; the first
+    # row's sigmoids are ordinary
+    slope = 2 * 0.7310585786300049 * 0.2689414213699951
+    want = torch.tensor([[0, slope, -slope, 0], [0, 100 * slope, -100 * slope, 0]], dtype=torch.float64)
+    if kind == "sigmoid":
+        want[0] = B.route_backward(x.double(), ids, dw.double(), kind, True, 1.0)[0]
+    assert (got.cpu().double() - want).abs().max() < 100 * (2 * 100 + 96) * U
 
 
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
