@@ -49,6 +49,9 @@ constexpr int kWarps = kThreads / 32;
 constexpr unsigned kAll = 0xffffffffu;
 constexpr float kLargest = 3.402823466e+38f;
 constexpr float kMinusInf = -__builtin_huge_valf();
+// Below this sum of the chosen scores the smallest of them may have lost bits that
+// count, or the sigmoid's (below 2^-126, about exp(-87)) be 0.
+constexpr float kTinyTotal = 0x1p-64f;
 
 // Sum and maximum (no NaN) over LANES consecutive lanes.
 template <int LANES>
@@ -350,6 +353,30 @@ __device__ __forceinline__ void choose(float (&key)[SLOTS], const float (&score)
     __syncwarp();
 }
 
+// The chosen expert's logit, as values() gives it; -inf for an empty slot.
+template <bool BF16>
+__device__ __forceinline__ float logit_of(const void* row, int id) {
+    if (id < 0) return kMinusInf;
+    float x;
+    if constexpr (BF16)
+        x = __uint_as_float(static_cast<uint32_t>(ld_ro(static_cast<const uint16_t*>(row) + id)) << 16);
+    else
+        x = ld_ro(static_cast<const float*>(row) + id);
+    return x > kMinusInf ? fminf(x, kLargest) : kMinusInf;
+}
+
+// A score up to a factor that all chosen experts share, `lead` their largest
+// score_lead: exp(x - lead), times 1 / (1 + exp(-|x|)) for the sigmoid.  Of order
+// one for the largest, however small the scores are.
+__device__ __forceinline__ float score_lead(float x, bool sigmoid) {
+    return sigmoid ? fminf(x, 0.0f) : x;
+}
+__device__ __forceinline__ float score_ratio(float x, bool sigmoid, float lead) {
+    if (!(x > kMinusInf)) return 0.0f;
+    const float e = expf(score_lead(x, sigmoid) - lead);
+    return sigmoid ? e * rcp_approx(1.0f + expf(-fabsf(x))) : e;
+}
+
 template <int SLOTS, int LANES, bool BF16>
 __global__ void __launch_bounds__(kThreads)
     route_topk_kernel(const void* __restrict__ logits, const float* __restrict__ bias,
@@ -403,6 +430,25 @@ __global__ void __launch_bounds__(kThreads)
         float total = 0.0f;
         for (int i = l; i < sh.k; i += LANES) total += bench.chosen_score[i];
         total = team_sum<LANES>(total);
+        // Renormalised weights are ratios, which hold where the scores underflow: once
+        // more from the logits.  (A row's path does not depend on its neighbours'.)
+        const bool tiny = sh.renorm && total < kTinyTotal && t < T && bench.chosen[0] >= 0;
+        if (__any_sync(kAll, tiny)) {
+            const void* row = row_of<BF16>(logits, t, ld);
+            const int from = tiny ? l : sh.k;
+            float lead = kMinusInf, again = 0.0f;
+            for (int i = from; i < sh.k; i += LANES)
+                lead = fmaxf(lead, score_lead(logit_of<BF16>(row, bench.chosen[i]), sh.sigmoid));
+            lead = team_max<LANES>(lead);
+            for (int i = from; i < sh.k; i += LANES) {
+                const float part =
+                    score_ratio(logit_of<BF16>(row, bench.chosen[i]), sh.sigmoid, lead);
+                bench.chosen_score[i] = part;  // read by this lane alone
+                again += part;
+            }
+            again = team_sum<LANES>(again);
+            if (tiny) total = again;
+        }
         if (t < T)
             for (int i = l; i < sh.k; i += LANES) {
                 const int id = bench.chosen[i];
@@ -448,30 +494,6 @@ __device__ __forceinline__ void store_row(void* out, const float* row, int E, in
         else
             st_plain(static_cast<float*>(out) + e, row[e]);
     }
-}
-
-// The chosen expert's logit, as values() gives it; -inf for an empty slot.
-template <bool BF16>
-__device__ __forceinline__ float logit_of(const void* row, int id) {
-    if (id < 0) return kMinusInf;
-    float x;
-    if constexpr (BF16)
-        x = __uint_as_float(static_cast<uint32_t>(ld_ro(static_cast<const uint16_t*>(row) + id)) << 16);
-    else
-        x = ld_ro(static_cast<const float*>(row) + id);
-    return x > kMinusInf ? fminf(x, kLargest) : kMinusInf;
-}
-
-// A score up to a factor that all chosen experts share, `lead` their largest
-// score_lead: exp(x - lead), times 1 / (1 + exp(-|x|)) for the sigmoid.  Of order
-// one for the largest, however small the scores are.
-__device__ __forceinline__ float score_lead(float x, bool sigmoid) {
-    return sigmoid ? fminf(x, 0.0f) : x;
-}
-__device__ __forceinline__ float score_ratio(float x, bool sigmoid, float lead) {
-    if (!(x > kMinusInf)) return 0.0f;
-    const float e = expf(score_lead(x, sigmoid) - lead);
-    return sigmoid ? e * rcp_approx(1.0f + expf(-fabsf(x))) : e;
 }
 
 // Gradient of the lane's chosen logit from a = scale * dweight.  A single

@@ -336,8 +336,8 @@ tkq_status tkq_swiglu_cast_t_clamp(const void* x, const float* w, void* out, voi
  * are chosen, in falling order; ties, of groups too, go to the lowest index.
  *   ids[t, i]     the i-th chosen expert
  *   weights[t, i] = scale * score[ids[t, i]], divided by the sum of the chosen
- *                   scores with TKQ_ROUTE_RENORM (0 where that sum is 0); the
- *                   bias moves the choice only
+ *                   scores with TKQ_ROUTE_RENORM (also where the scores
+ *                   themselves underflow); the bias moves the choice only
  *   counts[e]     the number of tokens that chose e is ADDED (the caller
  *                   zeroes; NULL: not counted)
  * An expert whose logit is -inf or NaN is absent from that token: no share of

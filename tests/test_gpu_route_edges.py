@@ -104,3 +104,43 @@ def test_absent_experts_among_the_ids_have_no_part(cuda_device, kind, renorm):
     got = tkq.route_topk_backward(x.to(cuda_device), ids.to(cuda_device), dw.to(cuda_device), **args)
     ref = tkq.route_topk_backward(x.to(cuda_device), empty.to(cuda_device), dw.to(cuda_device), **args)
     assert torch.isfinite(got).all() and torch.equal(got, ref)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,groups", [(24, 5, 1), (64, 4, 4), (256, 8, 8), (1000, 32, 1)])
+def test_weights_of_tiny_scores(cuda_device, dtype, kind, E, k, groups):
+    """Experts chosen by their bias: weights are ratios of scores that are subnormal or no number."""
+    T = 29
+    x, gen = _low(T, E, 3 * E + k, dtype)
+    x[3::8] = -INF                                # rows without experts next to them
+    x[5::8, k // 2 + E // 2:] = -INF              # and rows with fewer than k low ones
+    bias = torch.zeros(E)
+    low = torch.randperm(E - E // 4, generator=gen) + E // 4
+    bias[low] = 4.0 + torch.arange(len(low)).float() * 2.0 ** -6     # any two keys far apart
+    ids, w = tkq.route_topk(x.to(cuda_device), k, kind, bias.to(cuda_device), num_groups=groups,
+                            topk_groups=groups, scale=2.5)
+    ref_ids, ref_w = B.route(x.double(), k, kind, bias.double(), groups=groups, topk_groups=groups, scale=2.5)
+    full = (ref_ids >= E // 4).all(1) | (ref_ids < 0).all(1)         # no expert near 0 among the chosen
+    assert full.sum() > T // 2
+    assert torch.equal(ids.cpu()[full], ref_ids[full])
+    tol = ((2 * _spread(x) + 64) * U * ref_w + 2.0 ** -60)
+    assert (w.cpu().double() - ref_w)[full].abs().le(tol[full]).all()
+    # a row's result does not depend on the rows that share its warp
+    for t in range(T):
+        a, b = tkq.route_topk(x[t:t + 1].to(cuda_device), k, kind, bias.to(cuda_device),
+                              num_groups=groups, topk_groups=groups, scale=2.5)
+        assert torch.equal(a[0], ids[t]) and torch.equal(b[0], w[t])
+
+
+def test_lowest_finite_logits_are_experts_that_are_there(cuda_device):
+    """The type's lowest value in the place of -inf: all experts of a row alike share the weight, with
+    either kind of score."""
+    for dtype in (torch.bfloat16, torch.float32):
+        x = torch.full((3, 16), torch.finfo(dtype).min, dtype=dtype, device=cuda_device)
+        for kind in ("softmax", "sigmoid"):
+            ids, w = tkq.route_topk(x, 4, kind)
+            assert ids.tolist() == [[0, 1, 2, 3]] * 3 and (w == 0.25).all()
+            d = tkq.route_topk_backward(x, ids, torch.tensor([[1.0, 0, 0, 0]] * 3, device=cuda_device), kind)
+            want = torch.tensor([0.1875] + [-0.0625] * 3 + [0.0] * 12, device=cuda_device)
+            assert torch.equal(d.float(), want.expand(3, 16))
