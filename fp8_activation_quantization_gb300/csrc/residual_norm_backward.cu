@@ -148,7 +148,9 @@ __global__ void __launch_bounds__(THREADS)
         if (POST || has_dx) cta_sum(sum, turn);
         const float c1 = -q * q * inv_c * sum[0];              // dr = G + c1 r'
         float c2 = 0.0f;                                       // dh = p (..) + c2 h
-        if constexpr (POST) c2 = -p * p * p * inv_c * (sum[1] + c1 * sum[2]);
+        // p p p would be no binary32 number from a root mean square of 1.4e-13 down;
+        // one p scales the sum, to the order of G, before the other two.
+        if constexpr (POST) c2 = (-p * p) * (p * inv_c * (sum[1] + c1 * sum[2]));
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const Place<EXACT> place(i, pitch, vecs);
