@@ -22,7 +22,7 @@
 // follows is taken of the binary32 value before that rounding.
 //
 // Both directions are bound by memory.  8192 x 7168, bf16 stream, gate: forward
-// 86 us (6.1 TB/s, 92 % of a copy's rate), backward 161 us (5.8 TB/s, 87 %; moving
+// 87 us (6.1 TB/s, 91 % of a copy's rate), backward 162 us (5.8 TB/s, 87 %; moving
 // its rows with one barrier each and no arithmetic takes 149 us).
 #include <type_traits>
 
@@ -84,7 +84,7 @@ __device__ __forceinline__ void cast_rows(const ResidualNorm& a, const SfLayout&
 //   up to 4096 channels   one vector a thread, 64 registers, 1024 threads an SM:
 //                         4096: 101 us, 159 us with the 128 registers below (one
 //                         CTA an SM); 1024: 51 us, 58 us
-//   up to 8192            two vectors, 128 registers: 7168: 88 us, 95 us with one
+//   up to 8192            two vectors, 128 registers: 7168: 87 us, 95 us with one
 //                         vector and 896 threads; 5120: 73 us, 76 us
 //   up to 16384           two vectors, 64 registers, the weights read again for
 //                         each row: 16384: 137 us, 148 us with four and 512 threads

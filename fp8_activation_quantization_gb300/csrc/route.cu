@@ -28,12 +28,14 @@
 // (LANES, `with_lanes`), and 4 or 2 tokens share a warp's instructions; and the
 // choice is made in two steps: the k-th largest of the lanes' maxima bounds the
 // k-th largest key from below; the few keys that reach it are gathered and ranked
-// by counting.  8 of 256 experts at 16384 tokens: 12.0 us; in 8 groups of which 4
-// are searched, with a bias, 18.3 us (35.0 us with k rounds over all keys).
+// by counting.  8 of 256 experts at 16384 tokens, sigmoid: 12.8 us, in 8 groups of
+// which 4 are searched, with a bias, 17.9 us (35.0 us with k rounds over all keys);
+// from memory 13.8 and 18.8 us.
 // The backward has one warp per token and writes each row through shared memory,
-// so that it leaves as 16-byte vectors: 9.5 us (3.6 TB/s) for the softmax at
-// 16384 x 256, 6.9 us for the sigmoid, which reads the chosen logits alone;
-// 18.9 us with scalar accesses.
+// so that it leaves as 16-byte vectors.  16384 x 256 fp32, softmax: 6.5 us with
+// renormalised weights, for which the chosen logits are read alone, 7.5 us without;
+// sigmoid: 7.0 and 5.0 us.  These are with 70 MB of inputs and outputs, which stay
+// in L2; with 1 GB of them in turn 8.7, 9.2, 9.0 and 7.5 us.
 #include <type_traits>
 
 #include <cuda_runtime.h>

@@ -15,8 +15,11 @@
 // Bytes for each element of y: forward 4 in, 1 + 2 out; backward 2 + 2 in,
 // 4 (bf16) or 2 out and 2 for y; scales add 1 / 32 for each cast matrix.
 // Measured at 65536 x 2048: forward 156 us (6.1 TB/s, 91 % of a copy's rate);
-// backward with FP8 gradients, dw and y 183 us (6.0 TB/s, 89 %), where the ALU
-// pipe (conversions, maxima) is as busy as memory, with bf16 gradients 186 us.
+// backward with FP8 gradients, dw and y 185 us (5.9 TB/s, 88 %), where the ALU
+// pipe (conversions, maxima) is as busy as memory; with bf16 gradients and dw 187 us
+// (87 %), with y too 254 us (79 %).  Each thread has the registers that its CTAs an
+// SM leave it (64 and 80), for which the forward spills one to three values, the
+// backward with y two to eight.
 #include <type_traits>
 
 #include <cuda_runtime.h>

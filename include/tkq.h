@@ -344,6 +344,11 @@ tkq_status tkq_swiglu_cast_t_clamp(const void* x, const float* w, void* out, voi
  * the softmax, never chosen; one whose bias is -inf or NaN is never chosen.
  * Where fewer than k experts can be chosen, the remaining ids are -1 and their
  * weights 0.  A logit of +inf counts as the largest finite number.
+ * Scores, keys and sums of keys are binary32 and carry a few roundings: keys that
+ * are nearer than about 1e-6 of their size may come in either order, and logits
+ * whose scores are one number are ties, which the lowest index wins (sigmoids of
+ * logits above 17 are 1, below -88 they are 0; so are softmax shares 104 below the
+ * row's largest logit).
  *   logits : [T, E], dtype TKQ_OUT_F32 or TKQ_OUT_BF16, rows ld elements apart
  *            (E <= ld <= 2^28), aligned to its element
  *   bias : fp32 [E] or NULL;  ids : int32 [T, k];  weights : fp32 [T, k];
