@@ -18,6 +18,7 @@ import contextlib
 import ctypes
 import os
 import threading
+import typing
 
 __all__ = [
     "TkqError", "library_path", "load_library", "tkq_per_token_cast", "tkq_swiglu_cast",
@@ -34,6 +35,10 @@ __all__ = [
     "tkq_swiglu_checkpoint_backward_cast", "swiglu_forward_cast_and_checkpoint",
     "swiglu_backward_from_checkpoint", "tkq_residual_norm_cast", "tkq_residual_norm_workspace",
     "tkq_residual_norm_backward", "residual_norm_and_cast", "residual_norm_backward",
+    "tkq_expert_rows", "tkq_expert_order", "tkq_expert_gather", "tkq_expert_reduce",
+    "tkq_expert_reduce_backward", "tkq_expert_product", "tkq_expert_weight_grad", "ExpertOrder",
+    "expert_order", "expert_gather", "expert_reduce", "expert_reduce_backward", "expert_product",
+    "expert_weight_grad",
 ]
 
 FMT_E4M3 = 0
@@ -156,6 +161,20 @@ def _open(path):
         lib.tkq_residual_norm_workspace.restype = i64
         lib.tkq_residual_norm_backward.argtypes = [p] * 15 + [i64, i64, u, f32, p]
         lib.tkq_residual_norm_backward.restype = i
+        lib.tkq_expert_rows.argtypes = [i64, i, i64, i]
+        lib.tkq_expert_rows.restype = i64
+        lib.tkq_expert_order.argtypes = [p, p, p, p, i64, i, i64, i, i64, p]
+        lib.tkq_expert_order.restype = i
+        lib.tkq_expert_gather.argtypes = [p] * 9 + [i64, i64, i, i, i64, i64, i, i, p]
+        lib.tkq_expert_gather.restype = i
+        lib.tkq_expert_reduce.argtypes = [p] * 6 + [i64, i64, i, i, i64, i, p]
+        lib.tkq_expert_reduce.restype = i
+        lib.tkq_expert_reduce_backward.argtypes = [p] * 9 + [i64, i64, i, i, i64, i64, i, i, p]
+        lib.tkq_expert_reduce_backward.restype = i
+        lib.tkq_expert_product.argtypes = [p] * 6 + [i64] * 4 + [i, i, i, p]
+        lib.tkq_expert_product.restype = i
+        lib.tkq_expert_weight_grad.argtypes = [p] * 6 + [i64] * 4 + [i, i, i, i, p]
+        lib.tkq_expert_weight_grad.restype = i
         lib.tkq_checked_build.argtypes = []
         lib.tkq_checked_build.restype = i
         lib.tkq_read_check_address.argtypes = [ctypes.POINTER(ctypes.c_uint64), i]
@@ -366,6 +385,54 @@ def tkq_residual_norm_backward(dr, dx, r, h, w_post, gate, w_pre, rstd_post, rst
     return (_lib or load_library()).tkq_residual_norm_backward(
         dr, dx, r, h, w_post, gate, w_pre, rstd_post, rstd_pre, dr_out, dh, dgate, dw_post, dw_pre,
         workspace, T, C, norm_flags, res_scale, stream)
+
+
+ROWS_BF16 = 0   # forms of tkq_expert_gather
+ROWS_CAST = 1
+ROWS_CODES = 2
+
+
+def tkq_expert_rows(T, k, E, align=GROUP) -> int:
+    return (_lib or load_library()).tkq_expert_rows(T, k, E, align)
+
+
+def tkq_expert_order(ids, slots, rows, offsets, T, k, E, align, R, stream=None) -> int:
+    return (_lib or load_library()).tkq_expert_order(ids, slots, rows, offsets, T, k, E, align, R,
+                                                     stream)
+
+
+def tkq_expert_gather(x, x_sf, slots, rows, offsets, weights, out, out_sf, row_weights, T, C, k, E,
+                      R, group=GROUP, form=ROWS_BF16, fmt=FMT_E4M3, stream=None) -> int:
+    return (_lib or load_library()).tkq_expert_gather(x, x_sf, slots, rows, offsets, weights, out,
+                                                      out_sf, row_weights, T, C, group, k, E, R,
+                                                      form, fmt, stream)
+
+
+def tkq_expert_reduce(y, slots, weights, row_values, out, values, T, C, k, R, group=GROUP,
+                      out_dtype=OUT_BF16, stream=None) -> int:
+    return (_lib or load_library()).tkq_expert_reduce(y, slots, weights, row_values, out, values,
+                                                      T, C, group, k, R, out_dtype, stream)
+
+
+def tkq_expert_reduce_backward(dout, y, slots, rows, offsets, weights, dy, dy_sf, dweights, T, C,
+                               k, E, R, group=GROUP, form=ROWS_BF16, fmt=FMT_E4M3,
+                               stream=None) -> int:
+    return (_lib or load_library()).tkq_expert_reduce_backward(
+        dout, y, slots, rows, offsets, weights, dy, dy_sf, dweights, T, C, group, k, E, R, form,
+        fmt, stream)
+
+
+def tkq_expert_product(a, a_sf, w, w_sf, offsets, out, R, E, N, K, group=GROUP, fmt_a=FMT_E4M3,
+                       fmt_w=FMT_E4M3, stream=None) -> int:
+    return (_lib or load_library()).tkq_expert_product(a, a_sf, w, w_sf, offsets, out, R, E, N, K,
+                                                       group, fmt_a, fmt_w, stream)
+
+
+def tkq_expert_weight_grad(dy_t, dy_sf, x_t, x_sf, offsets, dw, R, E, N, K, group=GROUP,
+                           fmt_dy=FMT_E4M3, fmt_x=FMT_E4M3, out_dtype=0, stream=None) -> int:
+    return (_lib or load_library()).tkq_expert_weight_grad(dy_t, dy_sf, x_t, x_sf, offsets, dw, R,
+                                                           E, N, K, group, fmt_dy, fmt_x,
+                                                           out_dtype, stream)
 
 
 def _sf_shape(T: int, groups_per_row: int, sf_flags: int):
@@ -1037,6 +1104,294 @@ def residual_norm_backward(dr, r, h=None, dx=None, w_post=None, gate=None, w_pre
     if st:
         raise TkqError(st, "tkq_residual_norm_backward")
     return dr_out, dh, dgate, dw_post, dw_pre
+
+
+class ExpertOrder(typing.NamedTuple):
+    """Where the routed pairs' rows are (``expert_order``)."""
+    slots: object     # int32 [T, k]: the row of each pair, -1 for an empty slot
+    rows: object      # int32 [R]: the pair t * k + j of each row, -1 where there is none
+    offsets: object   # int32 [E + 1]: the first row of each expert, and the end of the last one
+
+
+def expert_order(ids, num_experts: int, align: int = GROUP, slots=None, rows=None, offsets=None):
+    """Places for the rows of routed tokens: ids int32 [T, k] (``route_topk``'s) -> ExpertOrder.
+
+    The rows of an expert are those of its pairs (t, j) in rising order and start at a
+    multiple of ``align`` (128 for the transposed casts and ``expert_weight_grad``, 1
+    where padding rows would only cost time).  An id outside [0, num_experts) is an
+    empty slot.  The number of rows allocated is the most that T * k pairs can need;
+    those in use end at ``offsets[-1]``."""
+    import torch
+    if not isinstance(ids, torch.Tensor) or not ids.is_cuda or ids.dim() != 2:
+        raise TypeError("ids must be a contiguous int32 [T, k] CUDA tensor")
+    T, k = ids.shape
+    dev = ids.device
+    _check_like(ids, "ids", (T, k), (torch.int32,), dev)
+    E, align = int(num_experts), int(align)
+    lib = _lib or load_library()
+    R = lib.tkq_expert_rows(T, k, E, align)
+    if R < 0:
+        raise TkqError(2, "tkq_expert_rows")
+    if slots is None:
+        slots = torch.empty((T, k), dtype=torch.int32, device=dev)
+    else:
+        _check_like(slots, "slots", (T, k), (torch.int32,), dev)
+    if rows is None:
+        rows = torch.empty((R,), dtype=torch.int32, device=dev)
+    else:
+        _check_out(rows, "rows", ids, 4 * R, dtype=torch.int32)
+        R = rows.numel()
+    if offsets is None:
+        offsets = torch.empty((E + 1,), dtype=torch.int32, device=dev)
+    else:
+        _check_like(offsets, "offsets", (E + 1,), (torch.int32,), dev)
+    with _device_ctx(dev):
+        st = lib.tkq_expert_order(_ptr(ids), _ptr(slots), _ptr(rows), _ptr(offsets), T, k, E, align, R,
+                                  _stream_handle(dev))
+    if st:
+        raise TkqError(st, "tkq_expert_order")
+    return ExpertOrder(slots, rows, offsets)
+
+
+def _check_order(order, dev, T=None):
+    """T, k, R and E of an ExpertOrder on `dev` (of T tokens, if given)."""
+    import torch
+    try:
+        slots, rows, offsets = order
+    except (TypeError, ValueError):
+        raise TypeError("order must be an ExpertOrder (slots, rows, offsets)") from None
+    i32 = (torch.int32,)
+    if not (isinstance(slots, torch.Tensor) and slots.dim() == 2 and isinstance(rows, torch.Tensor)
+            and rows.dim() == 1 and isinstance(offsets, torch.Tensor) and offsets.dim() == 1
+            and offsets.numel() >= 2):
+        raise TypeError("order must be an ExpertOrder of slots [T, k], rows [R] and offsets [E + 1]")
+    if T is None:
+        T = slots.shape[0]
+    k, R, E = slots.shape[1], rows.shape[0], offsets.shape[0] - 1
+    _check_like(slots, "order.slots", (T, k), i32, dev)
+    _check_like(rows, "order.rows", (R,), i32, dev)
+    _check_like(offsets, "order.offsets", (E + 1,), i32, dev)
+    return T, k, R, E
+
+
+def _codes_fmt(x, name):
+    """The format code of a contiguous CUDA tensor of FP8 codes."""
+    import torch
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or not x.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous CUDA tensor of FP8 codes")
+    if x.dtype == torch.float8_e4m3fn:
+        return FMT_E4M3
+    if x.dtype == torch.float8_e5m2:
+        return FMT_E5M2
+    raise TypeError(f"{name} must be float8_e4m3fn or float8_e5m2")
+
+
+def _rows_out(out, out_sf, R, C, form, f, x):
+    """The [R, C] rows of a call in `form` and their scales, allocated or checked."""
+    import torch
+    dt = torch.bfloat16 if form == ROWS_BF16 else _fp8_dtype(f)
+    dev = x.device
+    if out is None:
+        out = torch.empty((R, C), dtype=dt, device=dev)
+    else:
+        _check_like(out, "out", (R, C), (dt,) if form == ROWS_BF16 else (dt, torch.uint8), dev)
+    if form == ROWS_BF16:
+        if out_sf is not None:
+            raise ValueError("bf16 rows have no out_sf")
+    elif out_sf is None:
+        out_sf = torch.empty((R, C // GROUP), dtype=torch.float32, device=dev)
+    else:
+        _check_like(out_sf, "out_sf", (R, C // GROUP), (torch.float32,), dev)
+    return out, out_sf
+
+
+def expert_gather(x, order, fmt=None, x_sf=None, weights=None, out=None, out_sf=None,
+                  row_weights=None):
+    """The tokens' rows in expert order -> (rows [R, C], scales, row weights).
+
+    x: bf16 [T, C], copied (``fmt`` None) or cast per token to ``fmt`` on the way, bit for
+    bit as ``per_token_cast`` does; or FP8 codes [T, C] with their scales ``x_sf`` (fp32
+    [T, C/128]), both copied.  With ``weights`` (fp32 [T, k]) the third result holds the
+    weight of each row (fp32 [R]), as the SwiGLU casts take it.  Rows that pad an expert's
+    are zeros with weight 0; rows from ``order.offsets[-1]`` on are not written.  What is
+    not there is None.  The gradient is ``expert_reduce(dout, order, row_values=...)``."""
+    import torch
+    if x_sf is not None:
+        form, f = ROWS_CODES, _codes_fmt(x, "x")
+        if fmt is not None:
+            raise ValueError("x is cast already: fmt and x_sf exclude one another")
+        if x.dim() != 2:
+            raise TypeError("x must be 2-D")
+    else:
+        _check_input(x)
+        form, f = (ROWS_BF16, FMT_E4M3) if fmt is None else (ROWS_CAST, _fmt_code(fmt))
+    T, C = x.shape
+    dev = x.device
+    T, k, R, E = _check_order(order, dev, T)
+    if x_sf is not None:
+        _check_like(x_sf, "x_sf", (T, C // GROUP), (torch.float32,), dev)
+    if weights is not None:
+        _check_like(weights, "weights", (T, k), (torch.float32,), dev)
+        if row_weights is None:
+            row_weights = torch.empty((R,), dtype=torch.float32, device=dev)
+        else:
+            _check_like(row_weights, "row_weights", (R,), (torch.float32,), dev)
+    elif row_weights is not None:
+        raise ValueError("row_weights needs weights")
+    out, out_sf = _rows_out(out, out_sf, R, C, form, f, x)
+    lib = _lib or load_library()
+    with _device_ctx(dev):
+        st = lib.tkq_expert_gather(_ptr(x), _ptr(x_sf), _ptr(order[0]), _ptr(order[1]), _ptr(order[2]),
+                                   _ptr(weights), _ptr(out), _ptr(out_sf), _ptr(row_weights), T, C, GROUP,
+                                   k, E, R, form, f, _stream_handle(dev))
+    if st:
+        raise TkqError(st, "tkq_expert_gather")
+    return out, out_sf, row_weights
+
+
+def expert_reduce(y, order, weights=None, row_values=None, out_dtype=None, out=None):
+    """The rows in expert order back at their tokens: y bf16 [R, C] -> (out, values).
+
+    out[t] = sum over j of y[slots[t, j]], times ``weights[t, j]`` (fp32 [T, k]) if given, in
+    bf16 or (``out_dtype`` torch.float32) fp32 [T, C]; summed in fp32 in the order of j.
+    ``row_values`` (fp32 [R], the gradients of the row weights, say) come back as values [T,
+    k], 0 for empty slots; None without."""
+    import torch
+    _check_input(y, "y")
+    dev = y.device
+    T, k, R, _ = _check_order(order, dev)
+    if y.shape[0] != R:
+        raise ValueError(f"y must have the order's {R} rows")
+    C = y.shape[1]
+    if weights is not None:
+        _check_like(weights, "weights", (T, k), (torch.float32,), dev)
+    values = None
+    if row_values is not None:
+        _check_like(row_values, "row_values", (R,), (torch.float32,), dev)
+        values = torch.empty((T, k), dtype=torch.float32, device=dev)
+    out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("out_dtype must be torch.float32 or torch.bfloat16")
+    if out is None:
+        out = torch.empty((T, C), dtype=out_dtype, device=dev)
+    else:
+        _check_like(out, "out", (T, C), (out_dtype,), dev)
+    lib = _lib or load_library()
+    with _device_ctx(dev):
+        st = lib.tkq_expert_reduce(_ptr(y), _ptr(order[0]), _ptr(weights), _ptr(row_values), _ptr(out),
+                                   _ptr(values), T, C, GROUP, k, R,
+                                   OUT_F32 if out_dtype == torch.float32 else OUT_BF16,
+                                   _stream_handle(dev))
+    if st:
+        raise TkqError(st, "tkq_expert_reduce")
+    return out, values
+
+
+def expert_reduce_backward(dout, y, order, weights, fmt=None, out=None, out_sf=None):
+    """Gradient of ``expert_reduce`` with weights: dout bf16 [T, C], the forward's y bf16 [R, C]
+    -> (dy, dy scales, dweights fp32 [T, k]).
+
+    dy is bf16 [R, C] with scales None, or (``fmt``) its per-token cast for the next
+    product.  Rows that pad an expert's are zeros; rows from ``order.offsets[-1]`` on are
+    not written.  (Without weights the gradient is ``expert_gather(dout, order, fmt)``.)"""
+    import torch
+    _check_input(dout, "dout")
+    _check_input(y, "y")
+    T, C = dout.shape
+    dev = dout.device
+    T, k, R, E = _check_order(order, dev, T)
+    _check_like(y, "y", (R, C), (torch.bfloat16,), dev)
+    _check_like(weights, "weights", (T, k), (torch.float32,), dev)
+    form, f = (ROWS_BF16, FMT_E4M3) if fmt is None else (ROWS_CAST, _fmt_code(fmt))
+    out, out_sf = _rows_out(out, out_sf, R, C, form, f, dout)
+    dweights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    lib = _lib or load_library()
+    with _device_ctx(dev):
+        st = lib.tkq_expert_reduce_backward(_ptr(dout), _ptr(y), _ptr(order[0]), _ptr(order[1]),
+                                            _ptr(order[2]), _ptr(weights), _ptr(out), _ptr(out_sf),
+                                            _ptr(dweights), T, C, GROUP, k, E, R, form, f,
+                                            _stream_handle(dev))
+    if st:
+        raise TkqError(st, "tkq_expert_reduce_backward")
+    return out, out_sf, dweights
+
+
+def _check_offsets(offsets, dev):
+    import torch
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.numel() < 2:
+        raise TypeError("offsets must be an int32 [E + 1] CUDA tensor")
+    _check_like(offsets, "offsets", tuple(offsets.shape), (torch.int32,), dev)
+    return offsets.shape[0] - 1
+
+
+def expert_product(a, a_sf, w, w_sf, offsets, out=None):
+    """Rows in expert order times their experts' matrices: FP8 codes a [R, K] with scales
+    fp32 [R, K/128] (``per_token_cast``, ``expert_gather``, the SwiGLU casts) and codes w
+    [E, N, K] with scales fp32 [E, N/128, K/128] (``per_block_cast`` of each matrix) ->
+    bf16 [R, N].
+
+    Rows [offsets[e], offsets[e + 1]) are expert e's (int32 [E + 1], ``ExpertOrder``'s; any
+    rising offsets will do); rows of no expert are not written.  The gradient of the rows
+    is the same call with the transposed matrices' codes and scales."""
+    import torch
+    fa, fw = _codes_fmt(a, "a"), _codes_fmt(w, "w")
+    if a.dim() != 2 or w.dim() != 3:
+        raise TypeError("a must be [R, K] and w [E, N, K]")
+    R, K = a.shape
+    dev = a.device
+    E, f32 = _check_offsets(offsets, dev), (torch.float32,)
+    N = w.shape[1]
+    _check_like(w, "w", (E, N, K), (w.dtype,), dev)
+    _check_like(a_sf, "a_sf", (R, K // GROUP), f32, dev)
+    _check_like(w_sf, "w_sf", (E, N // GROUP, K // GROUP), f32, dev)
+    if out is None:
+        out = torch.empty((R, N), dtype=torch.bfloat16, device=dev)
+    else:
+        _check_like(out, "out", (R, N), (torch.bfloat16,), dev)
+    lib = _lib or load_library()
+    with _device_ctx(dev):
+        st = lib.tkq_expert_product(_ptr(a), _ptr(a_sf), _ptr(w), _ptr(w_sf), _ptr(offsets), _ptr(out), R, E,
+                                    N, K, GROUP, fa, fw, _stream_handle(dev))
+    if st:
+        raise TkqError(st, "tkq_expert_product")
+    return out
+
+
+def expert_weight_grad(dy_t, dy_sf, x_t, x_sf, offsets, out_dtype=None, out=None):
+    """Gradient of the experts' matrices: the transposed casts of the rows' gradients (codes
+    [N, R], scales fp32 [N, R/128]) and of the rows (codes [K, R], scales fp32 [K, R/128]),
+    as ``per_channel_cast(transpose=True)`` and the transposed SwiGLU cast give them ->
+    dw [E, N, K], fp32 or (``out_dtype``) bf16; zeros for an expert without rows.
+
+    The offsets (int32 [E + 1]) are multiples of 128, and the rows that pad an expert's are
+    zeros, as ``expert_order`` and ``expert_gather`` leave them."""
+    import torch
+    fy, fx = _codes_fmt(dy_t, "dy_t"), _codes_fmt(x_t, "x_t")
+    if dy_t.dim() != 2 or x_t.dim() != 2:
+        raise TypeError("dy_t must be [N, R] and x_t [K, R]")
+    N, R = dy_t.shape
+    K = x_t.shape[0]
+    dev = dy_t.device
+    E, f32 = _check_offsets(offsets, dev), (torch.float32,)
+    _check_like(x_t, "x_t", (K, R), (x_t.dtype,), dev)
+    _check_like(dy_sf, "dy_sf", (N, R // GROUP), f32, dev)
+    _check_like(x_sf, "x_sf", (K, R // GROUP), f32, dev)
+    out_dtype = torch.float32 if out_dtype is None else out_dtype
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("out_dtype must be torch.float32 or torch.bfloat16")
+    if out is None:
+        out = torch.empty((E, N, K), dtype=out_dtype, device=dev)
+    else:
+        _check_like(out, "out", (E, N, K), (out_dtype,), dev)
+    lib = _lib or load_library()
+    with _device_ctx(dev):
+        st = lib.tkq_expert_weight_grad(_ptr(dy_t), _ptr(dy_sf), _ptr(x_t), _ptr(x_sf), _ptr(offsets),
+                                        _ptr(out), R, E, N, K, GROUP, fy, fx,
+                                        OUT_F32 if out_dtype == torch.float32 else OUT_BF16,
+                                        _stream_handle(dev))
+    if st:
+        raise TkqError(st, "tkq_expert_weight_grad")
+    return out
 
 
 def swiglu_values(x, topk_weights=None):

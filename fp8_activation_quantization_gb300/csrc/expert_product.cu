@@ -1,0 +1,368 @@
+// expert_product.cu -- the experts' products of FP8 codes and scales on the tensor
+// cores: rows in expert order times the weights of their experts
+// (tkq_expert_product), and the weights' gradient, a sum over an expert's rows
+// (tkq_expert_weight_grad).
+//
+//   out[r, n]   = sum_g sa[r, g] sw[e, n/128, g]  sum_{k in g} a[r, k] w[e, n, k]
+//   dw[e, n, k] = sum_g sy[n, g] sx[k, g]         sum_{r in g} dyt[n, r] xt[k, r]
+//
+// g: groups of 128 along the contracted axis.  A scale belongs to a row and a group,
+// so the products of one group are added up by the tensor core (four MMAs of 32), and
+// the groups' sums in registers, each times its scales: binary32 throughout.
+//
+// A CTA works on tiles of 128 x 256 of the result.  One warp's lane copies boxes of
+// 128 bytes x 128 and x 256 rows into a ring of kStages stages (TMA, 128-byte swizzle);
+// one lane of another issues the MMAs into one of two TMEM accumulators of 256 columns;
+// eight warps take an accumulator out (32 lanes x 128 columns a warp, a lane one row),
+// multiply it by its scales and add it to their registers while the tensor core fills
+// the other one.
+#include <cuda_runtime.h>
+
+#include "tkq_async.cuh"
+#include "tkq_device.cuh"
+#include "tkq_internal.h"
+#include "tkq_tensor.cuh"
+
+namespace tkq {
+namespace {
+
+constexpr int kBM = 128, kBN = 256, kBK = 128;
+constexpr int kStages = 4;
+constexpr int kEpilogueWarps = 8;
+constexpr int kThreads = (kEpilogueWarps + 2) * 32;
+constexpr uint32_t kBytesA = kBM * kBK, kBytesB = kBN * kBK;
+constexpr uint32_t kStageBytes = kBytesA + kBytesB;
+constexpr uint32_t kTmemCols = 2 * kBN;
+constexpr int kMaxExperts = 1024;
+
+struct Smem {
+    uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
+    uint32_t tmem;
+    int abort;
+    int start[kMaxExperts + 1];  // first row of each expert
+    int tile[kMaxExperts + 1];   // rows' product: row tiles before each expert
+    alignas(16) float sx[2][kBN];  // gradient: a group's column scales
+};
+
+struct Args {
+    const float *a_sf, *b_sf;
+    const int32_t* offsets;
+    void* out;
+    int R, N, K, E;
+    uint32_t idesc;
+    unsigned int* status;
+};
+
+// One tile of the walk: its expert, where its rows (of A) and columns (rows of B) start,
+// and its groups.
+struct Tile {
+    int e, row, col, g0, groups;
+};
+
+// The walk over the tiles, the same for every role.  Rows' product: the tiles of one
+// expert in turn, its row tiles fastest, so that the CTAs at work share its weights and
+// rows in L2.  Gradient: expert by expert, the tiles of dw by rows of N.
+template <bool GRAD>
+struct Walk {
+    int at, e, n_col, per_expert;
+    __device__ __forceinline__ Walk(const Args& a) {
+        at = blockIdx.x;
+        e = 0;
+        n_col = ((GRAD ? a.K : a.N) + kBN - 1) / kBN;
+        per_expert = GRAD ? (a.N / kBM) * n_col : 0;
+    }
+    __device__ __forceinline__ bool get(const Args& a, const Smem& sm, Tile& t) {
+        if constexpr (GRAD) {
+            e = at / per_expert;
+            if (e >= a.E) return false;
+            const int local = at - e * per_expert;
+            const int r = local / n_col;
+            t.e = e;
+            t.row = r * kBM;
+            t.col = (local - r * n_col) * kBN;
+            t.g0 = sm.start[e] / kBK;
+            t.groups = sm.start[e + 1] / kBK - t.g0;
+        } else {
+            while (e < a.E && at >= sm.tile[e + 1] * n_col) ++e;
+            if (e >= a.E) return false;
+            const int rows = sm.tile[e + 1] - sm.tile[e];
+            const int local = at - sm.tile[e] * n_col;
+            const int c = local / rows;
+            t.e = e;
+            t.row = sm.start[e] + (local - c * rows) * kBM;
+            t.col = c * kBN;
+            t.g0 = 0;
+            t.groups = a.K / kBK;
+        }
+        return true;
+    }
+    __device__ __forceinline__ void next() { at += gridDim.x; }
+};
+
+template <bool GRAD, bool F32>
+__global__ void __launch_bounds__(kThreads, 1)
+    product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                   const Args a) {
+    extern __shared__ uint8_t raw[];
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t{1023});
+    Smem& sm = *reinterpret_cast<Smem*>(ring + kStages * kStageBytes);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&sm.acc_full[b], 1);
+            mbar_init(&sm.acc_empty[b], kEpilogueWarps);
+        }
+        sm.abort = 0;
+        fence_barrier_init();
+    }
+    __syncwarp();
+    if (warp == 0) tmem_alloc(&sm.tmem, kTmemCols);
+    // starts of the experts' rows, kept within the rows there are and in rising order
+    if (warp == 1) {
+        int from = 0, tiles = 0;
+        for (int e0 = 0; e0 <= a.E; e0 += 32) {
+            const int e = e0 + lane;
+            int v = e <= a.E ? ld_ro(a.offsets + e) : 0;
+            v = v < 0 ? 0 : v > a.R ? a.R : v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v = v > x ? v : x;
+            }
+            v = v > from ? v : from;
+            if (e <= a.E) sm.start[e] = v;
+            if constexpr (!GRAD) {
+                int prev = __shfl_up_sync(0xffffffffu, v, 1);
+                if (lane == 0) prev = e0 ? from : v;
+                int n = e <= a.E ? (v - prev + kBM - 1) / kBM : 0;  // tiles of expert e - 1
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int x = __shfl_up_sync(0xffffffffu, n, o);
+                    if (lane >= o) n += x;
+                }
+                if (e <= a.E) sm.tile[e] = tiles + n;
+                tiles += __shfl_sync(0xffffffffu, n, 31);
+            }
+            from = __shfl_sync(0xffffffffu, v, 31);
+        }
+    }
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = sm.tmem;
+    Walk<GRAD> walk(a);
+    Tile t;
+
+    if (warp == kEpilogueWarps) {
+        // ------------------------------------------------------------ copies
+        if (lane == 0) {
+            RingPos<kStages> pos;
+            uint32_t issued = 0;
+            bool ok = true;
+            for (; ok && walk.get(a, sm, t); walk.next()) {
+                const int row_a = t.row, row_b = GRAD ? t.col : t.e * a.N + t.col;
+                for (int g = 0; g < t.groups; ++g) {
+                    if (!mbar_wait_bounded(&sm.empty[pos.stage], pos.phase ^ 1u, &sm.abort, a.status)) {
+                        *static_cast<volatile int*>(&sm.abort) = 1;
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* dst = ring + pos.stage * kStageBytes;
+                    const int x = (t.g0 + g) * kBK;
+                    mbar_arrive_expect_tx(&sm.full[pos.stage], kStageBytes);
+                    tma_load_2d(dst, &map_a, x, row_a, &sm.full[pos.stage]);
+                    tma_load_2d(dst + kBytesA, &map_b, x, row_b, &sm.full[pos.stage]);
+                    pos.advance();
+                    ++issued;
+                }
+            }
+            // every copy this CTA issued has landed before it may leave
+            const uint32_t first = issued > kStages ? issued - kStages : 0;
+            for (uint32_t k = first; k < issued; ++k)
+                mbar_wait_bounded(&sm.full[k % kStages], (k / kStages) & 1u, nullptr, a.status);
+        }
+    } else if (warp == kEpilogueWarps + 1) {
+        // -------------------------------------------------------------- MMAs
+        if (lane == 0) {
+            RingPos<kStages> pos;
+            RingPos<2> acc;
+            bool ok = true;
+            for (; ok && walk.get(a, sm, t); walk.next()) {
+                for (int g = 0; g < t.groups; ++g) {
+                    if (!mbar_wait_bounded(&sm.full[pos.stage], pos.phase, &sm.abort, a.status) ||
+                        !mbar_wait_bounded(&sm.acc_empty[acc.stage], acc.phase ^ 1u, &sm.abort, a.status)) {
+                        *static_cast<volatile int*>(&sm.abort) = 1;
+                        ok = false;
+                        break;
+                    }
+                    tmem_fence_after();
+                    const uint32_t at = smem_u32(ring + pos.stage * kStageBytes);
+                    const uint64_t da = smem_desc_k128(at), db = smem_desc_k128(at + kBytesA);
+                    const uint32_t d = tmem + acc.stage * kBN;
+#pragma unroll
+                    for (int k = 0; k < kBK / 32; ++k)  // 32 bytes further in the swizzled row
+                        mma_f8(d, da + 2 * k, db + 2 * k, a.idesc, k > 0);
+                    mma_commit(&sm.empty[pos.stage]);
+                    mma_commit(&sm.acc_full[acc.stage]);
+                    pos.advance();
+                    acc.advance();
+                }
+            }
+            // the MMAs issued have ended before the accumulators are given back
+            for (int b = 0; b < 2; ++b) {
+                mbar_wait_bounded(&sm.acc_full[acc.stage], acc.phase ^ 1u, nullptr, a.status);
+                acc.advance();
+            }
+        }
+    } else {
+        // ---------------------------------------------------- scales and sums
+        const int quarter = warp & 3, half = warp >> 2;  // TMEM lanes, columns
+        const int row_in = quarter * 32 + lane;
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * 128;
+        const int groups_all = GRAD ? a.R / kBK : a.K / kBK;
+        RingPos<2> acc;
+        bool ok = true;      // no wait of this warp has given up
+        bool stop = false;   // gradient: nor one of any of the eight, which leave together
+        for (; !stop && walk.get(a, sm, t); walk.next()) {
+            const int row = t.row + row_in;
+            const int col = t.col + half * 128;
+            const int rows_end = GRAD ? a.N : sm.start[t.e + 1];
+            const int cols_end = GRAD ? a.K : a.N;
+            const bool live = row < rows_end && col < cols_end;
+            // scales of rows and columns beyond the edges: any that can be read
+            const float* sa = a.a_sf + static_cast<int64_t>(row < rows_end ? row : rows_end - 1) * groups_all + t.g0;
+            const float* sb;
+            if constexpr (GRAD) {
+                const int c = t.col + static_cast<int>(threadIdx.x);
+                sb = a.b_sf + static_cast<int64_t>(c < a.K ? c : a.K - 1) * groups_all + t.g0;
+            } else {
+                const int c = col < a.N ? col : a.N - 1;
+                sb = a.b_sf + (static_cast<int64_t>(t.e) * (a.N / 128) + c / 128) * groups_all;
+            }
+            float2 sum[64];
+#pragma unroll
+            for (int i = 0; i < 64; ++i) sum[i] = make_float2(0.f, 0.f);
+            float next_a = 0.f, next_b = 0.f;
+            if (t.groups > 0) {
+                next_a = ld_ro(sa);
+                next_b = ld_ro(sb);
+            }
+            for (int g = 0; g < t.groups; ++g) {
+                const float s = GRAD ? next_a : next_a * next_b;
+                const float2 s2 = make_float2(s, s);
+                if constexpr (GRAD) {
+                    sm.sx[g & 1][threadIdx.x] = next_b;
+                    stop = named_bar_or(1, kEpilogueWarps * 32, !ok);
+                    if (stop) break;
+                }
+                if (g + 1 < t.groups) {
+                    next_a = ld_ro(sa + g + 1);
+                    next_b = ld_ro(sb + g + 1);
+                }
+                if (ok) ok = mbar_wait_bounded(&sm.acc_full[acc.stage], acc.phase, &sm.abort, a.status);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    if (lane == 0) *static_cast<volatile int*>(&sm.abort) = 1;
+                    ok = false;
+                    if constexpr (!GRAD) {
+                        stop = true;
+                        break;
+                    }
+                }
+                if (ok) {
+                    tmem_fence_after();
+                    const uint32_t from = lane_base + acc.stage * kBN;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t v[32];
+                        tmem_load32(from + c * 32, v);
+                        tmem_load_wait(v);
+                        if (c == 3) {
+                            tmem_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&sm.acc_empty[acc.stage]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float2 p = make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                            if constexpr (GRAD) {
+                                const float2 x = *reinterpret_cast<const float2*>(
+                                    &sm.sx[g & 1][half * 128 + c * 32 + 2 * i]);
+                                p = mul2(p, x);
+                            }
+                            sum[c * 16 + i] = fma2(p, s2, sum[c * 16 + i]);
+                        }
+                    }
+                }
+                acc.advance();
+            }
+            if (!ok || !live) continue;
+            const float* f = reinterpret_cast<const float*>(sum);
+            const int64_t at = GRAD ? (static_cast<int64_t>(t.e) * a.N + row) * a.K + col
+                                    : static_cast<int64_t>(row) * a.N + col;
+            if constexpr (F32) {
+                float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    st_plain(o + i, make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]));
+            } else {
+                uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) st_stream(o + i, pack8_bf16(f + 8 * i));
+            }
+        }
+    }
+    __syncwarp();
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    if (warp == 0) tmem_free(tmem, kTmemCols);
+}
+
+template <bool GRAD, bool F32>
+cudaError_t launch(const ExpertProduct& p, int64_t tiles, cudaStream_t stream) {
+    CUtensorMap map_a, map_b;
+    const bool made =
+        GRAD ? encode_u8_2d_swizzled(&map_a, p.a, p.R, p.N, kBM) && encode_u8_2d_swizzled(&map_b, p.b, p.R, p.K, kBN)
+             : encode_u8_2d_swizzled(&map_a, p.a, p.K, p.R, kBM) &&
+                   encode_u8_2d_swizzled(&map_b, p.b, p.K, p.E * p.N, kBN);
+    if (!made) return cudaErrorInvalidValue;
+    Args a = {};
+    a.a_sf = p.a_sf;
+    a.b_sf = p.b_sf;
+    a.offsets = p.offsets;
+    a.out = p.out;
+    a.R = static_cast<int>(p.R);
+    a.N = static_cast<int>(p.N);
+    a.K = static_cast<int>(p.K);
+    a.E = p.E;
+    a.idesc = mma_f8_desc(p.fmt_a, p.fmt_b, kBM, kBN);
+    a.status = device_status_word();
+    auto* k = &product_kernel<GRAD, F32>;
+    const size_t smem = kStages * kStageBytes + sizeof(Smem) + 1024;
+    const int grid = persistent_grid(reinterpret_cast<const void*>(k), kThreads, smem, tiles);
+    if (const cudaError_t e = upload_checks(stream)) return e;
+    k<<<grid, kThreads, smem, stream>>>(map_a, map_b, a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_expert_product(const ExpertProduct& p, cudaStream_t stream) {
+    // at most this many row tiles: every expert's last one may be partial
+    const int64_t most = p.R / kBM + (p.E < p.R ? p.E : p.R);
+    return launch<false, false>(p, most * ((p.N + kBN - 1) / kBN), stream);
+}
+
+cudaError_t launch_expert_weight_grad(const ExpertProduct& p, cudaStream_t stream) {
+    if (p.R == 0)  // no rows: no gradient
+        return cudaMemsetAsync(p.out, 0, p.E * p.N * p.K * (p.out_f32 ? 4 : 2), stream);
+    const int64_t tiles = p.E * (p.N / kBM) * ((p.K + kBN - 1) / kBN);
+    return p.out_f32 ? launch<true, true>(p, tiles, stream) : launch<true, false>(p, tiles, stream);
+}
+
+}  // namespace tkq

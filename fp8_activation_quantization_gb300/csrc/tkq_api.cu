@@ -111,7 +111,8 @@ EncodeTiledFn encode_tiled() {
 
 namespace {
 bool encode_2d(CUtensorMap* map, CUtensorMapDataType type, int64_t elem_bytes, const void* base,
-               int64_t cols, int64_t rows, uint32_t box_cols, uint32_t box_rows) {
+               int64_t cols, int64_t rows, uint32_t box_cols, uint32_t box_rows,
+               CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_NONE) {
     EncodeTiledFn enc = encode_tiled();
     if (!enc) return false;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
@@ -119,7 +120,7 @@ bool encode_2d(CUtensorMap* map, CUtensorMapDataType type, int64_t elem_bytes, c
     const cuuint32_t box[2] = {box_cols, box_rows};
     const cuuint32_t estr[2] = {1, 1};
     return enc(map, type, 2, const_cast<void*>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -129,6 +130,12 @@ bool encode_bf16_2d(CUtensorMap* map, const void* base, int64_t cols, int64_t ro
                     uint32_t box_cols, uint32_t box_rows) {
     return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, cols, rows, box_cols,
                      box_rows);
+}
+
+bool encode_u8_2d_swizzled(CUtensorMap* map, const void* base, int64_t cols, int64_t rows,
+                           uint32_t box_rows) {
+    return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, cols, rows, 128, box_rows,
+                     CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 
@@ -818,6 +825,178 @@ tkq_status tkq_residual_norm_backward(const void* dr, const void* dx, const void
                                      workspace, T, C, res_scale, post, rb == 4};
     return launch_status(
         tkq::launch_residual_norm_backward(a, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+// The pairs and rows of tokens in expert order.
+tkq_status check_pairs(int64_t T, int k, int64_t E, int64_t R) {
+    if (T < 0 || k <= 0 || k > 32 || T > (int64_t{1} << 30) / k || E <= 0 || E > 1024 || R < 0 ||
+        R > INT32_MAX)
+        return TKQ_ERR_SHAPE;
+    return TKQ_OK;
+}
+
+tkq_status check_row_channels(int64_t C, int group) {
+    if (group != 128) return TKQ_ERR_GROUP;
+    return C <= 0 || C % 128 || C > (int64_t{1} << 20) ? TKQ_ERR_SHAPE : TKQ_OK;
+}
+
+bool fp8_fmt(int fmt) { return fmt == TKQ_FMT_E4M3 || fmt == TKQ_FMT_E5M2; }
+}  // namespace
+
+int64_t tkq_expert_rows(int64_t T, int k, int64_t E, int align) {
+    if (check_pairs(T, k, E, 0) != TKQ_OK || align <= 0 || align > 1024) return -1;
+    const int64_t P = T * k;
+    return (P + (E < P ? E : P) * (align - 1)) / align * align;
+}
+
+tkq_status tkq_expert_order(const int32_t* ids, int32_t* slots, int32_t* rows, int32_t* offsets,
+                            int64_t T, int k, int64_t E, int align, int64_t R,
+                            tkq_stream_t stream) {
+    tkq_status st = check_pairs(T, k, E, R);
+    if (st != TKQ_OK) return st;
+    const int64_t need = tkq_expert_rows(T, k, E, align);
+    if (need < 0 || R < need) return TKQ_ERR_SHAPE;
+    if ((T && (!ids || !slots)) || (R && !rows) || !offsets) return TKQ_ERR_NULL;
+    const Buffer in[] = {{ids, T * k * 4, 4}};
+    const Buffer out[] = {{slots, T * k * 4, 4}, {rows, R * 4, 4}, {offsets, (E + 1) * 4, 4}};
+    if ((st = check_buffers(in, out)) != TKQ_OK) return st;
+    return launch_status(tkq::launch_expert_order(ids, slots, rows, offsets, T * k,
+                                                  static_cast<int>(E), align, R,
+                                                  static_cast<cudaStream_t>(stream)));
+}
+
+tkq_status tkq_expert_gather(const void* x, const float* x_sf, const int32_t* slots,
+                             const int32_t* rows, const int32_t* offsets, const float* weights,
+                             void* out, float* out_sf, float* row_weights, int64_t T, int64_t C,
+                             int group, int k, int64_t E, int64_t R, int form, int fmt,
+                             tkq_stream_t stream) {
+    tkq_status st = check_pairs(T, k, E, R);
+    if (st != TKQ_OK || (st = check_row_channels(C, group)) != TKQ_OK) return st;
+    if (form != TKQ_ROWS_BF16 && form != TKQ_ROWS_CAST && form != TKQ_ROWS_CODES)
+        return TKQ_ERR_FLAGS;
+    if (!fp8_fmt(fmt)) return TKQ_ERR_FMT;
+    if (T == 0 || R == 0) return TKQ_OK;
+    const bool codes_in = form == TKQ_ROWS_CODES, codes_out = form != TKQ_ROWS_BF16;
+    if (!x || !slots || !rows || !offsets || !out || codes_in != !!x_sf || codes_out != !!out_sf ||
+        !weights != !row_weights)
+        return TKQ_ERR_NULL;
+    const int64_t G = C / 128;
+    const Buffer in[] = {{x, T * C * (codes_in ? 1 : 2), 16}, {x_sf, T * G * 4, 4},
+                         {slots, T * k * 4, 4},               {rows, R * 4, 4},
+                         {offsets, (E + 1) * 4, 4},           {weights, T * k * 4, 4}};
+    const Buffer outs[] = {{out, R * C * (codes_out ? 1 : 2), 16},
+                           {out_sf, R * G * 4, 4},
+                           {row_weights, R * 4, 4}};
+    if ((st = check_buffers(in, outs)) != TKQ_OK) return st;
+    const tkq::ExpertGather a = {x, x_sf, slots, rows, offsets, weights, out, out_sf, row_weights,
+                                 T, C, R, k, static_cast<int>(E), form, fmt};
+    return launch_status(tkq::launch_expert_gather(a, static_cast<cudaStream_t>(stream)));
+}
+
+tkq_status tkq_expert_reduce(const void* y, const int32_t* slots, const float* weights,
+                             const float* row_values, void* out, float* values, int64_t T,
+                             int64_t C, int group, int k, int64_t R, int out_dtype,
+                             tkq_stream_t stream) {
+    tkq_status st = check_pairs(T, k, 1, R);
+    if (st != TKQ_OK || (st = check_row_channels(C, group)) != TKQ_OK) return st;
+    if (out_dtype != TKQ_OUT_F32 && out_dtype != TKQ_OUT_BF16) return TKQ_ERR_FMT;
+    if (T == 0) return TKQ_OK;
+    if ((R && !y) || !slots || !out || (R && !row_values != !values)) return TKQ_ERR_NULL;
+    const bool f32 = out_dtype == TKQ_OUT_F32;
+    const Buffer in[] = {{y, R * C * 2, 16},
+                         {slots, T * k * 4, 4},
+                         {weights, T * k * 4, 4},
+                         {row_values, R * 4, 4}};
+    const Buffer outs[] = {{out, T * C * (f32 ? 4 : 2), 16}, {values, T * k * 4, 4}};
+    if ((st = check_buffers(in, outs)) != TKQ_OK) return st;
+    return launch_status(tkq::launch_expert_reduce(y, slots, weights, row_values, out, values, T, C,
+                                                   k, R, f32, static_cast<cudaStream_t>(stream)));
+}
+
+tkq_status tkq_expert_reduce_backward(const void* dout, const void* y, const int32_t* slots,
+                                      const int32_t* rows, const int32_t* offsets,
+                                      const float* weights, void* dy, float* dy_sf,
+                                      float* dweights, int64_t T, int64_t C, int group, int k,
+                                      int64_t E, int64_t R, int form, int fmt,
+                                      tkq_stream_t stream) {
+    tkq_status st = check_pairs(T, k, E, R);
+    if (st != TKQ_OK || (st = check_row_channels(C, group)) != TKQ_OK) return st;
+    if (form != TKQ_ROWS_BF16 && form != TKQ_ROWS_CAST) return TKQ_ERR_FLAGS;
+    if (!fp8_fmt(fmt)) return TKQ_ERR_FMT;
+    if (T == 0) return TKQ_OK;
+    const bool cast = form == TKQ_ROWS_CAST;
+    if (!dout || !slots || !offsets || !weights || !dweights ||
+        (R && (!y || !rows || !dy || cast != !!dy_sf)))
+        return TKQ_ERR_NULL;
+    const int64_t G = C / 128;
+    const Buffer in[] = {{dout, T * C * 2, 16}, {y, R * C * 2, 16},        {slots, T * k * 4, 4},
+                         {rows, R * 4, 4},      {offsets, (E + 1) * 4, 4}, {weights, T * k * 4, 4}};
+    const Buffer outs[] = {{dy, R * C * (cast ? 1 : 2), 16},
+                           {cast ? dy_sf : nullptr, R * G * 4, 4},
+                           {dweights, T * k * 4, 4}};
+    if ((st = check_buffers(in, outs)) != TKQ_OK) return st;
+    const tkq::ExpertReduceGrad a = {dout, y, slots, rows, offsets, weights, dy, dy_sf, dweights,
+                                     T, C, R, k, static_cast<int>(E), cast ? fmt : 2};
+    return launch_status(tkq::launch_expert_reduce_backward(a, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+// Sizes of the experts' products; E * N * K stays far from 2^63.
+tkq_status check_product(int64_t R, int64_t E, int64_t N, int64_t K, int group) {
+    if (group != 128) return TKQ_ERR_GROUP;
+    const int64_t most = int64_t{1} << 20;
+    if (R < 0 || R > INT32_MAX - 1024 || E <= 0 || E > 1024 || N <= 0 || N > most || N % 128 || K <= 0 ||
+        K > most || K % 128 || E * N > INT32_MAX - 1024 ||
+        E * (N / 128) * ((K + 255) / 256) > INT32_MAX / 2 ||
+        (R / 128 + E) * ((N + 255) / 256) > INT32_MAX / 2)
+        return TKQ_ERR_SHAPE;
+    return TKQ_OK;
+}
+}  // namespace
+
+tkq_status tkq_expert_product(const void* a, const float* a_sf, const void* w, const float* w_sf,
+                              const int32_t* offsets, void* out, int64_t R, int64_t E, int64_t N,
+                              int64_t K, int group, int fmt_a, int fmt_w, tkq_stream_t stream) {
+    tkq_status st = check_product(R, E, N, K, group);
+    if (st != TKQ_OK) return st;
+    if (!fp8_fmt(fmt_a) || !fp8_fmt(fmt_w)) return TKQ_ERR_FMT;
+    if (R == 0) return TKQ_OK;
+    if (!a || !a_sf || !w || !w_sf || !offsets || !out) return TKQ_ERR_NULL;
+    const Buffer in[] = {{a, R * K, 16},
+                         {a_sf, R * (K / 128) * 4, 4},
+                         {w, E * N * K, 16},
+                         {w_sf, E * (N / 128) * (K / 128) * 4, 4},
+                         {offsets, (E + 1) * 4, 4}};
+    const Buffer outs[] = {{out, R * N * 2, 16}};
+    if ((st = check_buffers(in, outs)) != TKQ_OK) return st;
+    const tkq::ExpertProduct p = {a, a_sf, w, w_sf, offsets, out, R, N, K, static_cast<int>(E),
+                                  fmt_a, fmt_w, false};
+    return launch_status(tkq::launch_expert_product(p, static_cast<cudaStream_t>(stream)));
+}
+
+tkq_status tkq_expert_weight_grad(const void* dy_t, const float* dy_sf, const void* x_t,
+                                  const float* x_sf, const int32_t* offsets, void* dw, int64_t R,
+                                  int64_t E, int64_t N, int64_t K, int group, int fmt_dy,
+                                  int fmt_x, int out_dtype, tkq_stream_t stream) {
+    tkq_status st = check_product(R, E, N, K, group);
+    if (st != TKQ_OK) return st;
+    if (R % 128) return TKQ_ERR_SHAPE;
+    if (!fp8_fmt(fmt_dy) || !fp8_fmt(fmt_x) ||
+        (out_dtype != TKQ_OUT_F32 && out_dtype != TKQ_OUT_BF16))
+        return TKQ_ERR_FMT;
+    if ((R && (!dy_t || !dy_sf || !x_t || !x_sf)) || !offsets || !dw) return TKQ_ERR_NULL;
+    const bool f32 = out_dtype == TKQ_OUT_F32;
+    const Buffer in[] = {{dy_t, N * R, 16},
+                         {dy_sf, N * (R / 128) * 4, 4},
+                         {x_t, K * R, 16},
+                         {x_sf, K * (R / 128) * 4, 4},
+                         {offsets, (E + 1) * 4, 4}};
+    const Buffer outs[] = {{dw, E * N * K * (f32 ? 4 : 2), 16}};
+    if ((st = check_buffers(in, outs)) != TKQ_OK) return st;
+    const tkq::ExpertProduct p = {dy_t, dy_sf, x_t, x_sf, offsets, dw, R, N, K, static_cast<int>(E),
+                                  fmt_dy, fmt_x, f32};
+    return launch_status(tkq::launch_expert_weight_grad(p, static_cast<cudaStream_t>(stream)));
 }
 
 tkq_status tkq_swiglu_values(const void* x, const float* w, float* y, int64_t T, int64_t H,

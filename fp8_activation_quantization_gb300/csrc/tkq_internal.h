@@ -213,4 +213,72 @@ struct ResidualNormGrad {
 int64_t residual_norm_parts(int64_t T, int64_t C);
 cudaError_t launch_residual_norm_backward(const ResidualNormGrad& a, cudaStream_t stream);
 
+// Tokens in the order of their experts and back (expert_rows.cu).  P = T * k pairs.
+cudaError_t launch_expert_order(const int32_t* ids, int32_t* slots, int32_t* rows, int32_t* offsets,
+                                int64_t P, int E, int align, int64_t R, cudaStream_t stream);
+
+struct ExpertGather {
+    const void* x;                     // [T, C] bf16 or codes
+    const float* x_sf;                 // codes
+    const int32_t *slots, *rows, *offsets;
+    const float* weights;              // [T, k] or null
+    void* out;
+    float *out_sf, *row_weights;       // may be null
+    int64_t T, C, R;
+    int k, E, form, fmt;               // form: 0 bf16, 1 cast in fmt, 2 codes
+};
+cudaError_t launch_expert_gather(const ExpertGather& a, cudaStream_t stream);
+
+cudaError_t launch_expert_reduce(const void* y, const int32_t* slots, const float* weights,
+                                 const float* row_values, void* out, float* values, int64_t T, int64_t C,
+                                 int k, int64_t R, bool out_f32, cudaStream_t stream);
+
+struct ExpertReduceGrad {
+    const void *dout, *y;
+    const int32_t *slots, *rows, *offsets;
+    const float* weights;
+    void* dy;
+    float *dy_sf, *dweights;
+    int64_t T, C, R;
+    int k, E, fmt;                     // fmt: an FP8 format, or 2 for bf16 rows
+};
+cudaError_t launch_expert_reduce_backward(const ExpertReduceGrad& a, cudaStream_t stream);
+
+// The experts' products of FP8 codes and scales (expert_product.cu): the rows' product
+// with the weights of their experts, and the weights' gradient.
+struct ExpertProduct {
+    const void* a;                     // rows' product: [R, K]; gradient: [N, R] (dy transposed)
+    const float* a_sf;                 // [R, K/128];                [N, R/128]
+    const void* b;                     // [E, N, K];                 [K, R] (x transposed)
+    const float* b_sf;                 // [E, N/128, K/128];         [K, R/128]
+    const int32_t* offsets;            // [E + 1]
+    void* out;                         // bf16 [R, N];               [E, N, K]
+    int64_t R, N, K;
+    int E, fmt_a, fmt_b;
+    bool out_f32;                      // gradient only
+};
+cudaError_t launch_expert_product(const ExpertProduct& p, cudaStream_t stream);
+cudaError_t launch_expert_weight_grad(const ExpertProduct& p, cudaStream_t stream);
+
+// Products of few rows with 4-bit weights (w4_product.cu).
+struct W4Product {
+    const void* x;                     // codes [M, K] (M = T, or T k with a row each)
+    const float* x_sf;                 // [M, K/128]
+    const void* w;                     // [E, N, K/2]
+    const void* w_sf;                  // [E, N, K/32] UE8M0 or [E, N, K/128] fp32
+    const int32_t* ids;                // [T, k] or null
+    void* out;                         // bf16 [T k, N]
+    int64_t T, N, K;
+    int k, E, group, fmt;
+    bool each;                         // a row of x for each pair
+};
+cudaError_t launch_w4_product(const W4Product& p, cudaStream_t stream);
+cudaError_t launch_w4_cast(const void* w, void* codes, void* sf, int64_t N, int64_t K, int group,
+                           cudaStream_t stream);
+
+// Tensor map of a row-major matrix of bytes [rows, cols] for boxes of 128 bytes x
+// box_rows in the 128-byte swizzle, out-of-range elements read as zero.
+bool encode_u8_2d_swizzled(CUtensorMap* map, const void* base, int64_t cols, int64_t rows,
+                           uint32_t box_rows);
+
 }  // namespace tkq

@@ -480,6 +480,122 @@ tkq_status tkq_residual_norm_backward(const void* dr, const void* dx, const void
                                       float res_scale, tkq_stream_t stream);
 
 /*
+ * Tokens in the order of their experts, and back
+ * ----------------------------------------------
+ * A pair p = t * k + j is token t's j-th expert, ids[t, j] (as tkq_route_topk gives
+ * them).  tkq_expert_order places the pairs: the rows of expert e start at
+ * offsets[e], a multiple of `align`, in the order of their pairs; offsets[E] is the
+ * end of the last one.
+ *   slots[t, j] : the row of the pair, -1 where ids[t, j] is outside [0, E)
+ *   rows[r]     : the pair of the row, -1 where there is none (behind an expert's
+ *                 rows up to the next multiple of align, and from offsets[E] on)
+ *   offsets     : int32 [E + 1]
+ * A token may name an expert twice: each pair has a row of its own.
+ * R is the length of `rows`, at least tkq_expert_rows(T, k, E, align), which is the
+ * most rows that T * k pairs can need (-1 for invalid arguments).
+ *   ids : int32 [T, k];  slots : int32 [T, k];  rows : int32 [R]
+ * T >= 0; 0 < k <= 32; 0 < E <= 1024; 0 < align <= 1024; T * k <= 2^30 and
+ * R < 2^31, else TKQ_ERR_SHAPE.  T == 0: offsets and rows are written (no pairs).
+ */
+int64_t tkq_expert_rows(int64_t T, int k, int64_t E, int align);
+tkq_status tkq_expert_order(const int32_t* ids, int32_t* slots, int32_t* rows, int32_t* offsets,
+                            int64_t T, int k, int64_t E, int align, int64_t R,
+                            tkq_stream_t stream);
+
+/*
+ * The tokens' rows in that order, each token read once:
+ *   form TKQ_ROWS_BF16  : x bf16 [T, C] -> out bf16 [R, C] (x_sf, out_sf NULL)
+ *   form TKQ_ROWS_CAST  : x bf16 [T, C] -> out codes [R, C], out_sf fp32 [R, C/128]:
+ *                         the rows of tkq_per_token_cast(x) in fmt, bit for bit
+ *   form TKQ_ROWS_CODES : x codes [T, C], x_sf fp32 [T, C/128] -> copies of both
+ * With weights (fp32 [T, k]) row_weights[r] (fp32 [R]) is the weight of the row's
+ * pair; both or neither are given.  Rows without a pair below offsets[E] are zeros
+ * (a cast one has the smallest scale, a copied one the scale 0), their weight 0;
+ * rows from offsets[E] on are left as they were.
+ *   slots, rows, offsets : as tkq_expert_order gives them; a slot outside [0, R) is
+ *   an empty one.  The gradient of this call is tkq_expert_reduce without weights.
+ * T >= 0, T * k <= 2^30; C > 0, C % 128 == 0, C <= 2^20; k, E and R as above.
+ * Alignment: x, out 16 bytes, else 4.
+ */
+#define TKQ_ROWS_BF16 0
+#define TKQ_ROWS_CAST 1
+#define TKQ_ROWS_CODES 2
+tkq_status tkq_expert_gather(const void* x, const float* x_sf, const int32_t* slots,
+                             const int32_t* rows, const int32_t* offsets, const float* weights,
+                             void* out, float* out_sf, float* row_weights, int64_t T, int64_t C,
+                             int group, int k, int64_t E, int64_t R, int form, int fmt,
+                             tkq_stream_t stream);
+
+/*
+ * The rows back at their tokens, in binary32 in the order of j, rounded once:
+ *   out[t] = sum_j [weights[t, j]] y[slots[t, j]]      empty slots count nothing
+ *   values[t, j] = row_values[slots[t, j]], 0 for an empty slot (both or neither
+ *                  are given): the rows' gradients at their pairs
+ *   y : bf16 [R, C];  weights : fp32 [T, k] or NULL (ones);  out : [T, C] of
+ *   out_dtype (TKQ_OUT_F32 or TKQ_OUT_BF16);  row_values : fp32 [R];
+ *   values : fp32 [T, k]
+ */
+tkq_status tkq_expert_reduce(const void* y, const int32_t* slots, const float* weights,
+                             const float* row_values, void* out, float* values, int64_t T,
+                             int64_t C, int group, int k, int64_t R, int out_dtype,
+                             tkq_stream_t stream);
+
+/*
+ * Gradient of tkq_expert_reduce with weights:
+ *   dy[slots[t, j]] = weights[t, j] * dout[t]           (binary32, rounded once)
+ *   dweights[t, j]  = sum_c dout[t, c] * y[slots[t, j], c]   (binary32, fixed order),
+ *                     0 for an empty slot
+ * dy is bf16 [R, C] (form TKQ_ROWS_BF16, dy_sf NULL), or its per-token cast in fmt
+ * (TKQ_ROWS_CAST, exact quotient).  Rows without a pair are as in
+ * tkq_expert_gather.
+ *   dout : bf16 [T, C];  y : bf16 [R, C];  weights, dweights : fp32 [T, k]
+ */
+tkq_status tkq_expert_reduce_backward(const void* dout, const void* y, const int32_t* slots,
+                                      const int32_t* rows, const int32_t* offsets,
+                                      const float* weights, void* dy, float* dy_sf,
+                                      float* dweights, int64_t T, int64_t C, int group, int k,
+                                      int64_t E, int64_t R, int form, int fmt,
+                                      tkq_stream_t stream);
+
+/*
+ * The experts' products of FP8 codes and scales, on the tensor cores: row r of
+ * expert e, offsets[e] <= r < offsets[e + 1], times the expert's matrix,
+ *   out[r, n] = sum_g a_sf[r, g] w_sf[e, n / 128, g] sum_{k in group g} a[r, k] w[e, n, k]
+ * with the sums and the scales' products in binary32, rounded once to bf16.  The
+ * offsets need no alignment; they are taken as rising and within [0, R], and are
+ * brought into that range where they are not.  Rows of no expert are left as they
+ * were.  The gradient of the rows is the same call on the gradient's codes, with the
+ * transposed matrices [E, K, N] and scales [E, K/128, N/128] as weights.
+ *   a : codes [R, K] in fmt_a;  a_sf : fp32 [R, K/128] (tkq_per_token_cast)
+ *   w : codes [E, N, K] in fmt_w;  w_sf : fp32 [E, N/128, K/128] (tkq_per_block_cast)
+ *   offsets : int32 [E + 1];  out : bf16 [R, N]
+ * R >= 0, R < 2^31; 0 < E <= 1024; N, K > 0, multiples of 128, at most 2^20,
+ * E * N < 2^31.  Alignment: a, w, out 16 bytes, else 4.  NaN codes and infinite
+ * scales give unspecified values in their own rows and columns.
+ */
+tkq_status tkq_expert_product(const void* a, const float* a_sf, const void* w, const float* w_sf,
+                              const int32_t* offsets, void* out, int64_t R, int64_t E, int64_t N,
+                              int64_t K, int group, int fmt_a, int fmt_w, tkq_stream_t stream);
+
+/*
+ * Gradient of the experts' matrices, from the transposed casts of the rows'
+ * gradients and of the rows (tkq_per_channel_cast with transpose,
+ * tkq_swiglu_cast_t), whose groups are 128 rows:
+ *   dw[e, n, k] = sum_g dy_sf[n, g] x_sf[k, g] sum_{r in group g} dy_t[n, r] x_t[k, r]
+ * over the groups of rows [offsets[e], offsets[e + 1]): the offsets are multiples of
+ * 128 (others are rounded down to one), rising and within [0, R].  An expert without
+ * rows gets zeros.
+ *   dy_t : codes [N, R] in fmt_dy;  dy_sf : fp32 [N, R/128]
+ *   x_t  : codes [K, R] in fmt_x;   x_sf : fp32 [K, R/128]
+ *   dw   : [E, N, K] of out_dtype (TKQ_OUT_F32 or TKQ_OUT_BF16)
+ * R >= 0, a multiple of 128, R < 2^31; N, K, E, alignment as above.
+ */
+tkq_status tkq_expert_weight_grad(const void* dy_t, const float* dy_sf, const void* x_t,
+                                  const float* x_sf, const int32_t* offsets, void* dw, int64_t R,
+                                  int64_t E, int64_t N, int64_t K, int group, int fmt_dy,
+                                  int fmt_x, int out_dtype, tkq_stream_t stream);
+
+/*
  * Diagnostic (not an operation of the source pages): the fp32 SwiGLU values
  *   y[t, c] = silu(x[t, c]) * x[t, H + c] [* w[t]]
  * computed exactly as tkq_swiglu_cast and tkq_swiglu_cast_t compute them
