@@ -38,7 +38,7 @@ __all__ = [
     "tkq_expert_rows", "tkq_expert_order", "tkq_expert_gather", "tkq_expert_reduce",
     "tkq_expert_reduce_backward", "tkq_expert_product", "tkq_expert_weight_grad", "ExpertOrder",
     "expert_order", "expert_gather", "expert_reduce", "expert_reduce_backward", "expert_product",
-    "expert_weight_grad",
+    "expert_weight_grad", "tkq_w4_product", "tkq_w4_cast", "w4_product", "w4_cast",
 ]
 
 FMT_E4M3 = 0
@@ -175,6 +175,10 @@ def _open(path):
         lib.tkq_expert_product.restype = i
         lib.tkq_expert_weight_grad.argtypes = [p] * 6 + [i64] * 4 + [i, i, i, i, p]
         lib.tkq_expert_weight_grad.restype = i
+        lib.tkq_w4_product.argtypes = [p] * 6 + [i64, i, i64, i64, i64, i64, i, i, i, p]
+        lib.tkq_w4_product.restype = i
+        lib.tkq_w4_cast.argtypes = [p, p, p, i64, i64, i, p]
+        lib.tkq_w4_cast.restype = i
         lib.tkq_checked_build.argtypes = []
         lib.tkq_checked_build.restype = i
         lib.tkq_read_check_address.argtypes = [ctypes.POINTER(ctypes.c_uint64), i]
@@ -433,6 +437,16 @@ def tkq_expert_weight_grad(dy_t, dy_sf, x_t, x_sf, offsets, dw, R, E, N, K, grou
     return (_lib or load_library()).tkq_expert_weight_grad(dy_t, dy_sf, x_t, x_sf, offsets, dw, R,
                                                            E, N, K, group, fmt_dy, fmt_x,
                                                            out_dtype, stream)
+
+
+def tkq_w4_product(x, x_sf, w, w_sf, ids, out, T, k, rows, E, N, K, group=GROUP, w_group=32,
+                   fmt=FMT_E4M3, stream=None) -> int:
+    return (_lib or load_library()).tkq_w4_product(x, x_sf, w, w_sf, ids, out, T, k, rows, E, N, K,
+                                                   group, w_group, fmt, stream)
+
+
+def tkq_w4_cast(w, codes, sf, N, K, w_group=32, stream=None) -> int:
+    return (_lib or load_library()).tkq_w4_cast(w, codes, sf, N, K, w_group, stream)
 
 
 def _sf_shape(T: int, groups_per_row: int, sf_flags: int):
@@ -1392,6 +1406,73 @@ def expert_weight_grad(dy_t, dy_sf, x_t, x_sf, offsets, out_dtype=None, out=None
     if st:
         raise TkqError(st, "tkq_expert_weight_grad")
     return out
+
+
+def w4_product(x, x_sf, w, w_sf, ids=None, out=None):
+    """Products of few rows with 4-bit weights: FP8 codes x with scales fp32 [rows, K/128]
+    (``per_token_cast``, the SwiGLU casts) and E2M1 codes w (uint8, two in a byte) with scales
+    w_sf, UE8M0 (uint8, groups of 32) or fp32 (groups of 128), as ``w4_cast`` gives both.
+
+    With ids (int32 [T, k], ``route_topk``'s), w [E, N, K/2], w_sf [E, N, K/32 or K/128] and x of
+    T rows (a token's pairs share its row) or T * k rows (one each) -> bf16 [T * k, N], row t * k
+    + j the product with the matrix of expert ids[t, j], zeros where that is outside [0, E).
+    Without, w [N, K/2] and x [T, K] -> bf16 [T, N].  T * k is at most 1024."""
+    import torch
+    f = _codes_fmt(x, "x")
+    if x.dim() != 2 or not isinstance(w, torch.Tensor) or w.dim() != (2 if ids is None else 3):
+        raise TypeError("x must be [rows, K] and w [N, K/2], or [E, N, K/2] with ids")
+    rows, K = x.shape
+    dev = x.device
+    lead = tuple(w.shape[:-1])
+    E, N = lead if ids is not None else (1, lead[0])
+    if K % GROUP:
+        raise ValueError(f"x must have a multiple of {GROUP} channels")
+    _check_like(x_sf, "x_sf", (rows, K // GROUP), (torch.float32,), dev)
+    _check_like(w, "w", (*lead, K // 2), (torch.uint8,), dev)
+    w_group = 32 if isinstance(w_sf, torch.Tensor) and w_sf.dtype == torch.uint8 else GROUP
+    _check_like(w_sf, "w_sf", (*lead, K // w_group), (torch.uint8, torch.float32), dev)
+    T, k = rows, 1
+    if ids is not None:
+        if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+            raise TypeError("ids must be an int32 [T, k] tensor")
+        T, k = ids.shape
+        _check_like(ids, "ids", (T, k), (torch.int32,), dev)
+        if rows not in (T, T * k):
+            raise ValueError(f"x must have {T} or {T * k} rows for these ids")
+    if out is None:
+        out = torch.empty((T * k, N), dtype=torch.bfloat16, device=dev)
+    else:
+        _check_like(out, "out", (T * k, N), (torch.bfloat16,), dev)
+    lib = _lib or load_library()
+    with _device_ctx(dev):
+        st = lib.tkq_w4_product(_ptr(x), _ptr(x_sf), _ptr(w), _ptr(w_sf), _ptr(ids), _ptr(out), T, k, rows,
+                                E, N, K, GROUP, w_group, f, _stream_handle(dev))
+    if st:
+        raise TkqError(st, "tkq_w4_product")
+    return out
+
+
+def w4_cast(w, group: int = 32):
+    """Weights for ``w4_product``: bf16 [N, K] or [E, N, K] -> (E2M1 codes uint8 [..., K/2], scales of
+    ``group`` channels: UE8M0 (uint8 [..., K/32]) for 32, fp32 [..., K/128] for 128)."""
+    import torch
+    if (not isinstance(w, torch.Tensor) or not w.is_cuda or w.dtype != torch.bfloat16
+            or w.dim() not in (2, 3) or not w.is_contiguous()):
+        raise TypeError("w must be a contiguous bfloat16 [N, K] or [E, N, K] CUDA tensor")
+    lead, K = tuple(w.shape[:-1]), w.shape[-1]
+    dev = w.device
+    codes = torch.empty((*lead, K // 2), dtype=torch.uint8, device=dev)
+    sf = torch.empty((*lead, K // max(group, 1)), dtype=torch.uint8 if group == 32 else torch.float32,
+                     device=dev)
+    n = 1
+    for d in lead:
+        n *= d
+    lib = _lib or load_library()
+    with _device_ctx(dev):
+        st = lib.tkq_w4_cast(_ptr(w), _ptr(codes), _ptr(sf), n, K, group, _stream_handle(dev))
+    if st:
+        raise TkqError(st, "tkq_w4_cast")
+    return codes, sf
 
 
 def swiglu_values(x, topk_weights=None):

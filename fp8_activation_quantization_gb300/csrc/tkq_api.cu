@@ -999,6 +999,43 @@ tkq_status tkq_expert_weight_grad(const void* dy_t, const float* dy_sf, const vo
     return launch_status(tkq::launch_expert_weight_grad(p, static_cast<cudaStream_t>(stream)));
 }
 
+tkq_status tkq_w4_product(const void* x, const float* x_sf, const void* w, const void* w_sf,
+                          const int32_t* ids, void* out, int64_t T, int k, int64_t rows, int64_t E,
+                          int64_t N, int64_t K, int group, int w_group, int fmt,
+                          tkq_stream_t stream) {
+    tkq_status st = check_product(0, E, N, K, group);
+    if (st != TKQ_OK || (st = check_pairs(T, k, E, 0)) != TKQ_OK) return st;
+    if (w_group != 32 && w_group != 128) return TKQ_ERR_GROUP;
+    if (T * k > 1024 || (rows != T && rows != T * k) || (!ids && (k != 1 || E != 1)))
+        return TKQ_ERR_SHAPE;
+    if (!fp8_fmt(fmt)) return TKQ_ERR_FMT;
+    if (T == 0) return TKQ_OK;
+    if (!x || !x_sf || !w || !w_sf || !out) return TKQ_ERR_NULL;
+    const Buffer in[] = {{x, rows * K, 16},
+                         {x_sf, rows * (K / 128) * 4, 4},
+                         {w, E * N * (K / 2), 16},
+                         {w_sf, E * N * (K / 128) * 4, 4},  // four bytes or one fp32 a block
+                         {ids, T * k * 4, 4}};
+    const Buffer outs[] = {{out, T * k * N * 2, 16}};
+    if ((st = check_buffers(in, outs)) != TKQ_OK) return st;
+    const tkq::W4Product p = {x, x_sf, w, w_sf, ids, out, T, N, K, k, static_cast<int>(E), w_group,
+                              fmt, rows != T};
+    return launch_status(tkq::launch_w4_product(p, static_cast<cudaStream_t>(stream)));
+}
+
+tkq_status tkq_w4_cast(const void* w, void* codes, void* sf, int64_t N, int64_t K, int w_group,
+                       tkq_stream_t stream) {
+    if (N < 0 || N > INT32_MAX || K <= 0 || K % 128 || K > (int64_t{1} << 20)) return TKQ_ERR_SHAPE;
+    if (w_group != 32 && w_group != 128) return TKQ_ERR_GROUP;
+    if (N == 0) return TKQ_OK;
+    if (!w || !codes || !sf) return TKQ_ERR_NULL;
+    const Buffer in[] = {{w, N * K * 2, 16}};
+    const Buffer outs[] = {{codes, N * (K / 2), 4}, {sf, N * (K / 128) * 4, 4}};
+    if (const tkq_status st = check_buffers(in, outs)) return st;
+    return launch_status(
+        tkq::launch_w4_cast(w, codes, sf, N, K, w_group, static_cast<cudaStream_t>(stream)));
+}
+
 tkq_status tkq_swiglu_values(const void* x, const float* w, float* y, int64_t T, int64_t H,
                              tkq_stream_t stream) {
     tkq_status st = check_common(T, H, 128, TKQ_FMT_E4M3);

@@ -1,0 +1,453 @@
+// w4_product.cu -- products of few rows with 4-bit weights (tkq_w4_product): FP8 rows
+// with 1x128 scales times E2M1 matrices with a scale per 1x32 (UE8M0) or 1x128 (fp32)
+// group, of one matrix or of each row's expert; and the cast that makes such weights
+// (tkq_w4_cast).
+//
+//   out[p, n] = sum_g xs[p, g] sum_{h in g} ws[e, n, h] sum_{k in h} x[p, k] w[e, n, k]
+//
+// g: groups of 128 channels, h: the weights' groups within them.  Every E2M1 and FP8
+// value is a binary16 value, so the tensor core (m16n8k16, binary32 sums) adds exact
+// products; a group's sum is then multiplied by its scales in binary32.
+//
+// Reading the weights bounds this: a few rows do 2 to 32 operations for each half byte.
+// Weights take the place of the MMA's 16-row operand and up to eight rows of x that of
+// the eight columns, so the weights go from memory to the tensor core once however many
+// rows there are.  (tcgen05 would want 128 of either, and its operands in shared memory
+// in 8 bits: the weights would have to be widened and stored there first.)
+// A warp takes 32 rows of a matrix, 128 channels at a time, from a ring of its own in
+// shared memory, filled by asynchronous copies; S warps share those rows, each taking
+// every S-th block of 128 channels, where there are too few rows to occupy the machine.
+// No warp waits for another but at the end of shared rows.
+#include <cuda_runtime.h>
+
+#include "tkq_async.cuh"
+#include "tkq_device.cuh"
+#include "tkq_internal.h"
+
+namespace tkq {
+namespace {
+
+constexpr int kWarps = 16;
+constexpr int kThreads = kWarps * 32;
+constexpr int kRows = 32;        // rows of a matrix a warp takes
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxPairs = 1024;
+
+// One stage of a warp's ring: 128 channels of 32 rows of weights and of 8 NT rows of x,
+// with their scales.  The 16-byte pieces of a row are permuted so that eight rows' equal
+// pieces, and four rows' equal 32 bytes of x, lie in different banks.
+template <int NT>
+struct Stage {
+    uint8_t w[kRows * 64];
+    uint8_t x[8 * NT * 128];
+    uint32_t ws[kRows];
+    float xs[8 * NT];
+};
+template <int NT>
+constexpr int kDepth = NT == 1 ? 4 : 3;  // stages: what fits 227 KB
+
+// What a CTA knows of the rows: the pairs of each expert in turn, cut into runs of at
+// most 8 NT.
+struct Plan {
+    int count[kMaxExperts];
+    int first[kMaxExperts];       // first of its pairs in `pair`
+    int sums[2][kWarps];
+    int runs;
+    uint16_t pair[kMaxPairs];
+    uint16_t run_first[kMaxPairs];
+    uint16_t run_expert[kMaxPairs];
+    uint8_t run_rows[kMaxPairs];
+};
+
+struct Args {
+    const uint8_t* x;        // [M, K]
+    const float* xs;         // [M, K/128]
+    const uint8_t* w;        // [E, N, K/2]
+    const uint32_t* ws;      // [E, N, K/128] words: four UE8M0 bytes or one fp32
+    const int32_t* ids;      // [P] or null
+    uint16_t* out;           // [P, N]
+    int P, N, K, E, share;   // x's row of pair p is p / share
+    int S;
+};
+
+// Eight E2M1 weights of a word as four binary16 pairs, the low nibble first.
+__device__ __forceinline__ void decode_e2m1(uint32_t v, uint32_t (&h)[4]) {
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(v));
+}
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The scale 2^(b - 127) of a UE8M0 byte.
+__device__ __forceinline__ float ue8m0(uint32_t b) {
+    return __uint_as_float(b ? b << 23 : 0x00400000u);
+}
+
+// A position in a warp's work: run of pairs, 32 rows of its matrix, block of channels.
+struct Cursor {
+    int run, block_row, kb;
+    int expert, first, rows;
+};
+
+template <int NT>
+__device__ void make_plan(Plan& pl, const Args& a) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int e = tid; e < a.E; e += kThreads) pl.count[e] = 0;
+    __syncthreads();
+    for (int p = tid; p < a.P; p += kThreads) {
+        const int e = a.ids ? ld_ro(a.ids + p) : 0;
+        if (e >= 0 && e < a.E) atomicAdd(&pl.count[e], 1);
+    }
+    __syncthreads();
+    // first pairs and runs of the experts: a scan over two experts a thread
+    const int e0 = 2 * tid;
+    int n0 = e0 < a.E ? pl.count[e0] : 0, n1 = e0 + 1 < a.E ? pl.count[e0 + 1] : 0;
+    int r0 = (n0 + 8 * NT - 1) / (8 * NT), r1 = (n1 + 8 * NT - 1) / (8 * NT);
+    int n = n0 + n1, r = r0 + r1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int un = __shfl_up_sync(0xffffffffu, n, o), ur = __shfl_up_sync(0xffffffffu, r, o);
+        if (lane >= o) {
+            n += un;
+            r += ur;
+        }
+    }
+    if (lane == 31) {
+        pl.sums[0][warp] = n;
+        pl.sums[1][warp] = r;
+    }
+    __syncthreads();
+    int bn = 0, br = 0;
+    for (int w = 0; w < warp; ++w) {
+        bn += pl.sums[0][w];
+        br += pl.sums[1][w];
+    }
+    if (tid == kThreads - 1) pl.runs = br + r;
+    const int at_n = bn + n - n0 - n1, at_r = br + r - r0 - r1;
+    const auto runs_of = [&](int e, int c, int f, int q) {
+        if (e < a.E) pl.first[e] = f;
+        for (int i = 0; i < c; i += 8 * NT, ++q) {
+            pl.run_first[q] = static_cast<uint16_t>(f + i);
+            pl.run_expert[q] = static_cast<uint16_t>(e);
+            pl.run_rows[q] = static_cast<uint8_t>(c - i < 8 * NT ? c - i : 8 * NT);
+        }
+    };
+    runs_of(e0, n0, at_n, at_r);
+    runs_of(e0 + 1, n1, at_n + n0, at_r + r0);
+    __syncthreads();
+    // an expert's pairs in rising order, by one warp, so that every CTA cuts them into the
+    // same runs
+    if (warp == 0)
+        for (int p0 = 0; p0 < a.P; p0 += 32) {
+            const int p = p0 + lane;
+            const int e = p < a.P ? (a.ids ? ld_ro(a.ids + p) : 0) : -1;
+            const bool live = e >= 0 && e < a.E;
+            const unsigned same = __match_any_sync(0xffffffffu, e);
+            const int at = live ? pl.first[e] : 0;
+            __syncwarp();
+            if (live) {
+                pl.pair[at + __popc(same & ((1u << lane) - 1u))] = static_cast<uint16_t>(p);
+                if (lane == __ffs(same) - 1) pl.first[e] = at + __popc(same);
+            }
+            __syncwarp();
+        }
+    __syncthreads();
+}
+
+template <int NT, bool G32, int FMT>
+__global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
+    extern __shared__ __align__(16) uint8_t raw[];
+    using St = Stage<NT>;
+    constexpr int D = kDepth<NT>;
+    Plan& pl = *reinterpret_cast<Plan*>(raw);
+    float* parts = reinterpret_cast<float*>(raw + (sizeof(Plan) + 15) / 16 * 16);  // [kWarps][4][32]
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    St* ring = reinterpret_cast<St*>(reinterpret_cast<uint8_t*>(parts) + kWarps * 4 * 32 * 4) + warp * D;
+    const int g = lane >> 2, t = lane & 3;
+    make_plan<NT>(pl, a);
+
+    const int KB = a.K / 128, NB = a.N / kRows;
+    const int team = warp / a.S, of_team = warp - team * a.S, teams = kWarps / a.S;
+    const int items = pl.runs * NB;
+    const int step = gridDim.x * teams;
+
+    const auto place = [&](Cursor& c, int item) {
+        c.run = item / NB;
+        c.block_row = item - c.run * NB;
+        c.kb = of_team;
+        if (item < items) {
+            c.expert = pl.run_expert[c.run];
+            c.first = pl.run_first[c.run];
+            c.rows = pl.run_rows[c.run];
+        }
+    };
+    int load_item = blockIdx.x * teams + team, item = load_item;
+    Cursor ld, at;
+    ld.expert = ld.first = ld.rows = at.expert = at.first = at.rows = 0;
+    place(ld, load_item);
+    int slot_in = 0, slot = 0;
+
+    // issues the copies of the next block of this warp's work, if there is one
+    const auto load_next = [&]() {
+        while (load_item < items && ld.kb >= KB) {
+            load_item += step;
+            place(ld, load_item);
+        }
+        if (load_item < items) {
+            St& s = ring[slot_in];
+            const int64_t row0 = static_cast<int64_t>(ld.expert) * a.N + ld.block_row * kRows;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = i * 8 + (lane >> 2), c = lane & 3;
+                cp_async16(s.w + r * 64 + ((c ^ ((r >> 1) & 3)) << 4),
+                           a.w + (row0 + r) * (a.K / 2) + ld.kb * 64 + c * 16);
+            }
+            cp_async4(&s.ws[lane], a.ws + (row0 + lane) * KB + ld.kb);
+#pragma unroll
+            for (int i = 0; i < 2 * NT; ++i) {
+                const int j = i * 4 + (lane >> 3), c = lane & 7;
+                if (j < ld.rows) {
+                    const int64_t xr = pl.pair[ld.first + j] / a.share;
+                    cp_async16(s.x + j * 128 + ((((c >> 1) ^ (j & 3)) << 1 | (c & 1)) << 4),
+                               a.x + xr * a.K + ld.kb * 128 + c * 16);
+                }
+            }
+            if (lane < ld.rows) {
+                const int64_t xr = pl.pair[ld.first + lane] / a.share;
+                cp_async4(&s.xs[lane], a.xs + xr * KB + ld.kb);
+            }
+            ld.kb += a.S;
+        }
+        cp_async_commit();
+        slot_in = slot_in + 1 == D ? 0 : slot_in + 1;
+    };
+#pragma unroll
+    for (int i = 0; i < D - 1; ++i) load_next();
+
+    for (; item < items; item += step) {
+        place(at, item);
+        float acc[2][NT][4];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
+        for (; at.kb < KB; at.kb += a.S) {
+            load_next();
+            cp_async_wait(D);
+            __syncwarp();
+            const St& s = ring[slot];
+            slot = slot + 1 == D ? 0 : slot + 1;
+            float blk[2][NT][4];
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) blk[m][n][i] = 0.0f;
+            uint32_t ws[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) ws[q] = s.ws[q * 8 + g];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t v[4];
+                asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                             : "r"(smem_u32(s.w + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4))));
+                uint32_t h[4][4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) decode_e2m1(v[q], h[q]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const int j = n * 8 + g;
+                    const uint2 xv = *reinterpret_cast<const uint2*>(s.x + j * 128 + ((i ^ (j & 3)) << 5) + t * 8);
+                    const uint32_t b0 = fp8x2_to_f16x2<FMT>(xv.x & 0xFFFFu), b1 = fp8x2_to_f16x2<FMT>(xv.x >> 16);
+                    const uint32_t b2 = fp8x2_to_f16x2<FMT>(xv.y & 0xFFFFu), b3 = fp8x2_to_f16x2<FMT>(xv.y >> 16);
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        const uint32_t(&lo)[4] = h[2 * m], (&hi)[4] = h[2 * m + 1];
+                        if constexpr (G32) {
+                            float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                            mma_16816(p, lo[0], hi[0], lo[1], hi[1], b0, b1);
+                            mma_16816(p, lo[2], hi[2], lo[3], hi[3], b2, b3);
+                            const float s0 = ue8m0(ws[2 * m] >> (8 * i) & 0xFFu);
+                            const float s1 = ue8m0(ws[2 * m + 1] >> (8 * i) & 0xFFu);
+                            blk[m][n][0] = fmaf(p[0], s0, blk[m][n][0]);
+                            blk[m][n][1] = fmaf(p[1], s0, blk[m][n][1]);
+                            blk[m][n][2] = fmaf(p[2], s1, blk[m][n][2]);
+                            blk[m][n][3] = fmaf(p[3], s1, blk[m][n][3]);
+                        } else {
+                            mma_16816(blk[m][n], lo[0], hi[0], lo[1], hi[1], b0, b1);
+                            mma_16816(blk[m][n], lo[2], hi[2], lo[3], hi[3], b2, b3);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float2 xs = *reinterpret_cast<const float2*>(&s.xs[n * 8 + 2 * t]);
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    const float s0 = G32 ? 1.0f : __uint_as_float(ws[2 * m]);
+                    const float s1 = G32 ? 1.0f : __uint_as_float(ws[2 * m + 1]);
+                    acc[m][n][0] = fmaf(blk[m][n][0], xs.x * s0, acc[m][n][0]);
+                    acc[m][n][1] = fmaf(blk[m][n][1], xs.y * s0, acc[m][n][1]);
+                    acc[m][n][2] = fmaf(blk[m][n][2], xs.x * s1, acc[m][n][2]);
+                    acc[m][n][3] = fmaf(blk[m][n][3], xs.y * s1, acc[m][n][3]);
+                }
+            }
+            __syncwarp();  // the stage is refilled by the next copies
+        }
+        // this lane's results: rows 16 m + g (+ 8), columns 8 n + 2 t (+ 1)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                float(&v)[4] = acc[m][n];
+                if (a.S > 1) {
+                    // shared rows: the team's first warp adds the others' in their order
+                    float* mine = parts + warp * 128 + lane;
+                    named_bar_sync(1 + team, a.S * 32);
+                    if (of_team)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) mine[i * 32] = v[i];
+                    named_bar_sync(1 + team, a.S * 32);
+                    if (of_team) continue;
+                    for (int o = 1; o < a.S; ++o)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v[i] += mine[o * 128 + i * 32];
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int j = n * 8 + 2 * t + (i & 1);
+                    if (j < at.rows) {
+                        const int row = at.block_row * kRows + m * 16 + (i >> 1) * 8 + g;
+                        st_plain(a.out + static_cast<int64_t>(pl.pair[at.first + j]) * a.N + row,
+                                 static_cast<uint16_t>(pack_bf16x2(v[i], 0.0f)));
+                    }
+                }
+            }
+    }
+    // pairs of no expert get zeros
+    if (a.ids)
+        for (int p = blockIdx.x * kWarps + warp; p < a.P; p += gridDim.x * kWarps) {
+            const int e = ld_ro(a.ids + p);
+            if (e >= 0 && e < a.E) continue;
+            uint4* o = reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(p) * a.N);
+            for (int v = lane; v < a.N / 8; v += 32) st_stream(o + v, make_uint4(0, 0, 0, 0));
+        }
+}
+
+template <int NT, bool G32, int FMT>
+cudaError_t launch(Args a, int64_t items, cudaStream_t stream) {
+    auto* k = &w4_kernel<NT, G32, FMT>;
+    const size_t smem = (sizeof(Plan) + 15) / 16 * 16 + kWarps * 4 * 32 * 4 +
+                        kWarps * kDepth<NT> * sizeof(Stage<NT>);
+    static_assert((sizeof(Plan) + 15) / 16 * 16 + kWarps * 4 * 32 * 4 + kWarps * kDepth<NT> * sizeof(Stage<NT>) <=
+                      227 * 1024 && sizeof(Stage<NT>) % 16 == 0, "shared memory");
+    const int64_t warps = static_cast<int64_t>(num_sms()) * kWarps;
+    // warps that share rows: as many as leave no warp without work, at most one a block of channels
+    a.S = 1;
+    while (a.S < kWarps && a.S * 2 <= a.K / 128 && items * a.S * 2 <= warps) a.S *= 2;
+    const int64_t blocks = (items * a.S + kWarps - 1) / kWarps;
+    const int grid = persistent_grid(reinterpret_cast<const void*>(k), kThreads, smem, blocks);
+    if (const cudaError_t e = upload_checks(stream)) return e;
+    k<<<grid, kThreads, smem, stream>>>(a);
+    return cudaGetLastError();
+}
+
+template <int NT>
+cudaError_t launch_form(const Args& a, bool g32, int fmt, int64_t items, cudaStream_t stream) {
+    if (g32)
+        return fmt == kFmtE4M3 ? launch<NT, true, kFmtE4M3>(a, items, stream)
+                               : launch<NT, true, kFmtE5M2>(a, items, stream);
+    return fmt == kFmtE4M3 ? launch<NT, false, kFmtE4M3>(a, items, stream)
+                           : launch<NT, false, kFmtE5M2>(a, items, stream);
+}
+
+// ---------------------------------------------------------------------------
+// weights to 4 bits
+// ---------------------------------------------------------------------------
+// A warp takes 128 values of a row, a lane four: the largest magnitude of 8 lanes (32
+// values) or of all, the scale amax / 6 (UE8M0: the power of two not below it), and the
+// codes of the quotient, to nearest, ties to even, by the hardware conversion.
+template <bool G32>
+__global__ void __launch_bounds__(256) w4_cast_kernel(const uint2* __restrict__ w, uint16_t* __restrict__ codes,
+                                                      void* __restrict__ sf, int64_t groups) {
+    const int lane = threadIdx.x & 31;
+    for (int64_t u = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); u < groups;
+         u += static_cast<int64_t>(gridDim.x) * 8) {
+        const uint2 q = ld_ro(w + u * 32 + lane);
+        const float v[4] = {bf16_lo(q.x), bf16_hi(q.x), bf16_lo(q.y), bf16_hi(q.y)};
+        float m = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+#pragma unroll
+        for (int o = 1; o < (G32 ? 8 : 32); o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        // the smallest scale is 2^-126, so that zeros and tiny groups have one
+        float s = fmaxf(__fdiv_rn(m, 6.0f), 1.17549435e-38f);
+        if constexpr (G32) {
+            float inv;
+            pow2_scale(s, inv);
+            if ((lane & 7) == 0)
+                st_plain(static_cast<uint8_t*>(sf) + u * 4 + (lane >> 3),
+                         static_cast<uint8_t>(__float_as_uint(s) >> 23));
+        } else if (lane == 0) {
+            st_plain(static_cast<float*>(sf) + u, s);
+        }
+        uint16_t c;
+        asm("{\n\t.reg .b8 lo, hi;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 lo, %2, %1;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 hi, %4, %3;\n\t"
+            "mov.b16 %0, {lo, hi};\n\t}"
+            : "=h"(c)
+            : "f"(__fdiv_rn(v[0], s)), "f"(__fdiv_rn(v[1], s)), "f"(__fdiv_rn(v[2], s)),
+              "f"(__fdiv_rn(v[3], s)));
+        st_plain(codes + u * 32 + lane, c);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_w4_product(const W4Product& p, cudaStream_t stream) {
+    Args a = {};
+    a.x = static_cast<const uint8_t*>(p.x);
+    a.xs = p.x_sf;
+    a.w = static_cast<const uint8_t*>(p.w);
+    a.ws = static_cast<const uint32_t*>(p.w_sf);
+    a.ids = p.ids;
+    a.out = static_cast<uint16_t*>(p.out);
+    a.P = static_cast<int>(p.T * p.k);
+    a.N = static_cast<int>(p.N);
+    a.K = static_cast<int>(p.K);
+    a.E = p.E;
+    a.share = p.each ? 1 : p.k;
+    const bool g32 = p.group == 32;
+    const int64_t experts = p.ids ? (a.P < p.E ? a.P : p.E) : 1;  // at most this many have rows
+    const int64_t items = experts * (p.N / kRows);
+    return p.T <= 8 ? launch_form<1>(a, g32, p.fmt, items, stream)
+                    : launch_form<2>(a, g32, p.fmt, items, stream);
+}
+
+cudaError_t launch_w4_cast(const void* w, void* codes, void* sf, int64_t N, int64_t K, int group,
+                           cudaStream_t stream) {
+    const int64_t groups = N * (K / 128);
+    const auto k = group == 32 ? &w4_cast_kernel<true> : &w4_cast_kernel<false>;
+    const int grid = persistent_grid(reinterpret_cast<const void*>(k), 256, 0, (groups + 7) / 8);
+    if (const cudaError_t e = upload_checks(stream)) return e;
+    k<<<grid, 256, 0, stream>>>(static_cast<const uint2*>(w), static_cast<uint16_t*>(codes), sf, groups);
+    return cudaGetLastError();
+}
+
+}  // namespace tkq

@@ -596,6 +596,39 @@ tkq_status tkq_expert_weight_grad(const void* dy_t, const float* dy_sf, const vo
                                   int fmt_x, int out_dtype, tkq_stream_t stream);
 
 /*
+ * Products of few FP8 rows with 4-bit weights, one matrix or the experts'
+ *   out[p, n] = sum_g x_sf[r, g] sum_{h in g} s[e, n, h] sum_{k in h} x[r, k] w[e, n, k]
+ * for the pairs p = t * k + j of ids[t, j] = e (rows of an id outside [0, E) are
+ * zeros), or with ids NULL (k = 1, E = 1) for the rows of one matrix; sums in
+ * binary32, rounded once to bf16.
+ *   x : codes [rows, K] in fmt, x_sf : fp32 [rows, K/128] (tkq_per_token_cast):
+ *       rows is T (r = t: the pairs of a token share its row) or T * k (r = p)
+ *   w : E2M1 codes [E, N, K/2], two in a byte, the low four bits the even channel:
+ *       sign, two bits of exponent, one of mantissa: 0, 0.5, 1, 1.5, 2, 3, 4, 6
+ *   w_sf : s of groups along K, w_group 32: UE8M0 bytes [E, N, K/32], s = 2^(byte -
+ *       127) (255 gives unspecified values), or w_group 128: fp32 [E, N, K/128]
+ *   ids : int32 [T, k];  out : bf16 [T * k, N]
+ * T >= 0, 0 < k <= 32, T * k <= 1024 (a larger batch is tkq_expert_product's);
+ * 0 < E <= 1024; N, K > 0, multiples of 128, at most 2^20, else TKQ_ERR_SHAPE;
+ * w_group: TKQ_ERR_GROUP.  Alignment: x, w, out 16 bytes, else 4.
+ */
+tkq_status tkq_w4_product(const void* x, const float* x_sf, const void* w, const void* w_sf,
+                          const int32_t* ids, void* out, int64_t T, int k, int64_t rows, int64_t E,
+                          int64_t N, int64_t K, int group, int w_group, int fmt,
+                          tkq_stream_t stream);
+
+/*
+ * The weights of tkq_w4_product from bf16 [N, K] (the matrices of several experts as
+ * one of E * N rows): for each group of w_group channels
+ *   s = max(amax / 6, 2^-126), for w_group 32 rounded up to a power of two,
+ * and the codes of fl32(w / s), to nearest, ties to even, saturating.
+ *   codes : [N, K/2];  sf : UE8M0 bytes [N, K/32] or fp32 [N, K/128]
+ * N >= 0; K > 0, K % 128 == 0.  Alignment: w 16 bytes, else 4.
+ */
+tkq_status tkq_w4_cast(const void* w, void* codes, void* sf, int64_t N, int64_t K, int w_group,
+                       tkq_stream_t stream);
+
+/*
  * Diagnostic (not an operation of the source pages): the fp32 SwiGLU values
  *   y[t, c] = silu(x[t, c]) * x[t, H + c] [* w[t]]
  * computed exactly as tkq_swiglu_cast and tkq_swiglu_cast_t compute them
