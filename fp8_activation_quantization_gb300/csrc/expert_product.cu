@@ -15,7 +15,10 @@
 // one lane of another issues the MMAs into one of two TMEM accumulators of 256 columns;
 // eight warps take an accumulator out (32 lanes x 128 columns a warp, a lane one row),
 // multiply it by its scales and add it to their registers while the tensor core fills
-// the other one.
+// the other one.  Two warps bring the scales, four groups at a time, to a ring of their
+// own: read by the eight warps themselves, a group before its use, they cost more than
+// the products (2.0 ms against 1.1 with scales that are not read, 65536 rows, 32
+// matrices of 4096 x 4096).
 #include <cuda_runtime.h>
 
 #include "tkq_async.cuh"
@@ -29,19 +32,32 @@ namespace {
 constexpr int kBM = 128, kBN = 256, kBK = 128;
 constexpr int kStages = 4;
 constexpr int kEpilogueWarps = 8;
-constexpr int kThreads = (kEpilogueWarps + 2) * 32;
+// Three warpgroups: the registers of the launch, 168 a thread, are split 216 for the two
+// that hold a tile's sums (128 a thread) and 72 for the one that copies and multiplies.
+constexpr int kThreads = (kEpilogueWarps + 4) * 32;
+constexpr int kSumRegs = 216, kOtherRegs = 72;
+static_assert(2 * kSumRegs + kOtherRegs <= 3 * 168, "shares of the launch's registers");
 constexpr uint32_t kBytesA = kBM * kBK, kBytesB = kBN * kBK;
 constexpr uint32_t kStageBytes = kBytesA + kBytesB;
 constexpr uint32_t kTmemCols = 2 * kBN;
 constexpr int kMaxExperts = 1024;
 
 struct Smem {
-    uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
+    uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], sc_full[3], sc_empty[3];
     uint32_t tmem;
     int abort;
     int start[kMaxExperts + 1];  // first row of each expert
     int tile[kMaxExperts + 1];   // rows' product: row tiles before each expert
-    alignas(16) float sx[2][kBN];  // gradient: a group's column scales
+};
+
+// The scales of four groups: of a tile's rows, and of its columns (rows' product: of its
+// two blocks of 128).  Groups are 8 banks apart, so that eight rows' four groups lie in
+// different ones.
+constexpr int kUnit = 4, kUnits = 3;
+template <bool GRAD>
+struct alignas(16) Scales {
+    float a[kUnit][kBM + 8];
+    float b[kUnit][GRAD ? kBN + 8 : 4];
 };
 
 struct Args {
@@ -52,6 +68,29 @@ struct Args {
     uint32_t idesc;
     unsigned int* status;
 };
+
+// Two binary32 values in one 64-bit register, and the packed operations on them: sums
+// kept that way need no moves around each operation.
+__device__ __forceinline__ uint64_t pair64(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul64(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma64(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// Arrives on `bar` when this thread's asynchronous copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 
 // One tile of the walk: its expert, where its rows (of A) and columns (rows of B) start,
 // and its groups.
@@ -105,7 +144,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                    const Args a) {
     extern __shared__ uint8_t raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t{1023});
-    Smem& sm = *reinterpret_cast<Smem*>(ring + kStages * kStageBytes);
+    Scales<GRAD>* scales = reinterpret_cast<Scales<GRAD>*>(ring + kStages * kStageBytes);
+    Smem& sm = *reinterpret_cast<Smem*>(scales + kUnits);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
     if (threadIdx.x == 0) {
@@ -116,6 +156,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sm.acc_full[b], 1);
             mbar_init(&sm.acc_empty[b], kEpilogueWarps);
+        }
+        for (int u = 0; u < kUnits; ++u) {
+            mbar_init(&sm.sc_full[u], 64);
+            mbar_init(&sm.sc_empty[u], kEpilogueWarps);
         }
         sm.abort = 0;
         fence_barrier_init();
@@ -158,7 +202,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     Walk<GRAD> walk(a);
     Tile t;
 
-    if (warp == kEpilogueWarps) {
+    if (warp >= kEpilogueWarps) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+      if (warp == kEpilogueWarps) {
         // ------------------------------------------------------------ copies
         if (lane == 0) {
             RingPos<kStages> pos;
@@ -186,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (uint32_t k = first; k < issued; ++k)
                 mbar_wait_bounded(&sm.full[k % kStages], (k / kStages) & 1u, nullptr, a.status);
         }
-    } else if (warp == kEpilogueWarps + 1) {
+      } else if (warp == kEpilogueWarps + 1) {
         // -------------------------------------------------------------- MMAs
         if (lane == 0) {
             RingPos<kStages> pos;
@@ -219,100 +265,134 @@ __global__ void __launch_bounds__(kThreads, 1)
                 acc.advance();
             }
         }
+      } else {
+        // ------------------------------------------------------------ scales
+        const int groups_all = GRAD ? a.R / kBK : a.K / kBK;
+        const int q = lane & 3, r8 = lane >> 2, half = warp & 1;  // a warp: 8 rows' four groups
+        RingPos<kUnits> pos;
+        bool ok = true;
+        for (; ok && walk.get(a, sm, t); walk.next()) {
+            const int rows_end = GRAD ? a.N : sm.start[t.e + 1];
+            for (int g0 = 0; g0 < t.groups; g0 += kUnit) {
+                ok = mbar_wait_bounded(&sm.sc_empty[pos.stage], pos.phase ^ 1u, &sm.abort, a.status);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    if (lane == 0) *static_cast<volatile int*>(&sm.abort) = 1;
+                    ok = false;
+                    break;
+                }
+                Scales<GRAD>& sc = scales[pos.stage];
+                if (g0 + q < t.groups) {
+                    const int g = t.g0 + g0 + q;
+                    // rows and columns beyond the edges: the last scale there is
+#pragma unroll
+                    for (int i = 0; i < kBM / 16; ++i) {
+                        const int r = (2 * i + half) * 8 + r8;
+                        const int row = t.row + r < rows_end ? t.row + r : rows_end - 1;
+                        cp_async4(&sc.a[q][r], a.a_sf + static_cast<int64_t>(row) * groups_all + g);
+                    }
+                    if constexpr (GRAD) {
+#pragma unroll
+                        for (int i = 0; i < kBN / 16; ++i) {
+                            const int r = (2 * i + half) * 8 + r8;
+                            const int col = t.col + r < a.K ? t.col + r : a.K - 1;
+                            cp_async4(&sc.b[q][r], a.b_sf + static_cast<int64_t>(col) * groups_all + g);
+                        }
+                    } else if (r8 == 0) {
+                        const int c = t.col + half * 128 < a.N ? t.col / 128 + half : a.N / 128 - 1;
+                        cp_async4(&sc.b[q][half],
+                                  a.b_sf + (static_cast<int64_t>(t.e) * (a.N / 128) + c) * groups_all + g);
+                    }
+                }
+                cp_async_arrive(&sm.sc_full[pos.stage]);
+                pos.advance();
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+      }
     } else {
         // ---------------------------------------------------- scales and sums
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
         const int quarter = warp & 3, half = warp >> 2;  // TMEM lanes, columns
         const int row_in = quarter * 32 + lane;
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * 128;
-        const int groups_all = GRAD ? a.R / kBK : a.K / kBK;
         RingPos<2> acc;
-        bool ok = true;      // no wait of this warp has given up
-        bool stop = false;   // gradient: nor one of any of the eight, which leave together
-        for (; !stop && walk.get(a, sm, t); walk.next()) {
-            const int row = t.row + row_in;
-            const int col = t.col + half * 128;
-            const int rows_end = GRAD ? a.N : sm.start[t.e + 1];
-            const int cols_end = GRAD ? a.K : a.N;
-            const bool live = row < rows_end && col < cols_end;
-            // scales of rows and columns beyond the edges: any that can be read
-            const float* sa = a.a_sf + static_cast<int64_t>(row < rows_end ? row : rows_end - 1) * groups_all + t.g0;
-            const float* sb;
-            if constexpr (GRAD) {
-                const int c = t.col + static_cast<int>(threadIdx.x);
-                sb = a.b_sf + static_cast<int64_t>(c < a.K ? c : a.K - 1) * groups_all + t.g0;
-            } else {
-                const int c = col < a.N ? col : a.N - 1;
-                sb = a.b_sf + (static_cast<int64_t>(t.e) * (a.N / 128) + c / 128) * groups_all;
-            }
-            float2 sum[64];
+        RingPos<kUnits> pos;
+        bool ok = true;
+        for (; ok && walk.get(a, sm, t); walk.next()) {
+            uint64_t sum[64];  // pairs of binary32
 #pragma unroll
-            for (int i = 0; i < 64; ++i) sum[i] = make_float2(0.f, 0.f);
-            float next_a = 0.f, next_b = 0.f;
-            if (t.groups > 0) {
-                next_a = ld_ro(sa);
-                next_b = ld_ro(sb);
-            }
+            for (int i = 0; i < 64; ++i) sum[i] = 0;
             for (int g = 0; g < t.groups; ++g) {
-                const float s = GRAD ? next_a : next_a * next_b;
-                const float2 s2 = make_float2(s, s);
-                if constexpr (GRAD) {
-                    sm.sx[g & 1][threadIdx.x] = next_b;
-                    stop = named_bar_or(1, kEpilogueWarps * 32, !ok);
-                    if (stop) break;
-                }
-                if (g + 1 < t.groups) {
-                    next_a = ld_ro(sa + g + 1);
-                    next_b = ld_ro(sb + g + 1);
-                }
+                const int q = g & (kUnit - 1);
+                if (q == 0) ok = mbar_wait_bounded(&sm.sc_full[pos.stage], pos.phase, &sm.abort, a.status);
                 if (ok) ok = mbar_wait_bounded(&sm.acc_full[acc.stage], acc.phase, &sm.abort, a.status);
                 if (!__all_sync(0xffffffffu, ok)) {
                     if (lane == 0) *static_cast<volatile int*>(&sm.abort) = 1;
                     ok = false;
-                    if constexpr (!GRAD) {
-                        stop = true;
-                        break;
-                    }
+                    break;
                 }
-                if (ok) {
-                    tmem_fence_after();
-                    const uint32_t from = lane_base + acc.stage * kBN;
+                const Scales<GRAD>& sc = scales[pos.stage];
+                const float s = GRAD ? sc.a[q][row_in] : sc.a[q][row_in] * sc.b[q][half];
+                const uint64_t s2 = pair64(s, s);
+                tmem_fence_after();
+                const uint32_t from = lane_base + acc.stage * kBN;
+                // the next 16 columns are on their way while these are added
+                uint32_t v[2][16];
+                tmem_load16(from, v[0]);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t v[32];
-                        tmem_load32(from + c * 32, v);
-                        tmem_load_wait(v);
-                        if (c == 3) {
-                            tmem_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&sm.acc_empty[acc.stage]);
-                        }
+                for (int c = 0; c < 8; ++c) {
+                    tmem_load_wait(v[c & 1]);
+                    if (c < 7) {
+                        tmem_load16(from + (c + 1) * 16, v[(c + 1) & 1]);
+                    } else {
+                        tmem_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sm.acc_empty[acc.stage]);
+                    }
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float2 p = make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-                            if constexpr (GRAD) {
-                                const float2 x = *reinterpret_cast<const float2*>(
-                                    &sm.sx[g & 1][half * 128 + c * 32 + 2 * i]);
-                                p = mul2(p, x);
-                            }
-                            sum[c * 16 + i] = fma2(p, s2, sum[c * 16 + i]);
-                        }
+                    for (int i = 0; i < 8; ++i) {
+                        uint64_t p = pair64(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1]));
+                        if constexpr (GRAD)
+                            p = mul64(p, *reinterpret_cast<const uint64_t*>(&sc.b[q][half * 128 + c * 16 + 2 * i]));
+                        sum[c * 8 + i] = fma64(p, s2, sum[c * 8 + i]);
                     }
                 }
                 acc.advance();
+                if (q == kUnit - 1 || g + 1 == t.groups) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.sc_empty[pos.stage]);
+                    pos.advance();
+                }
             }
+            const int row = t.row + row_in, col = t.col + half * 128;
+            const bool live = row < (GRAD ? a.N : sm.start[t.e + 1]) && col < (GRAD ? a.K : a.N);
             if (!ok || !live) continue;
-            const float* f = reinterpret_cast<const float*>(sum);
             const int64_t at = GRAD ? (static_cast<int64_t>(t.e) * a.N + row) * a.K + col
                                     : static_cast<int64_t>(row) * a.N + col;
+            // a lane's row in whole sectors of 32 bytes
             if constexpr (F32) {
-                float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at);
+                float* o = static_cast<float*>(a.out) + at;
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    st_plain(o + i, make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]));
+                for (int i = 0; i < 16; ++i) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        w[2 * j] = static_cast<uint32_t>(sum[4 * i + j]);
+                        w[2 * j + 1] = static_cast<uint32_t>(sum[4 * i + j] >> 32);
+                    }
+                    st_sector(o + 8 * i, w);
+                }
             } else {
-                uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at);
+                uint16_t* o = static_cast<uint16_t*>(a.out) + at;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) st_stream(o + i, pack8_bf16(f + 8 * i));
+                for (int i = 0; i < 8; ++i) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        w[j] = pack_bf16x2(__uint_as_float(static_cast<uint32_t>(sum[8 * i + j])),
+                                           __uint_as_float(static_cast<uint32_t>(sum[8 * i + j] >> 32)));
+                    st_sector(o + 16 * i, w);
+                }
             }
         }
     }
@@ -343,7 +423,7 @@ cudaError_t launch(const ExpertProduct& p, int64_t tiles, cudaStream_t stream) {
     a.idesc = mma_f8_desc(p.fmt_a, p.fmt_b, kBM, kBN);
     a.status = device_status_word();
     auto* k = &product_kernel<GRAD, F32>;
-    const size_t smem = kStages * kStageBytes + sizeof(Smem) + 1024;
+    const size_t smem = kStages * kStageBytes + kUnits * sizeof(Scales<GRAD>) + sizeof(Smem) + 1024;
     const int grid = persistent_grid(reinterpret_cast<const void*>(k), kThreads, smem, tiles);
     if (const cudaError_t e = upload_checks(stream)) return e;
     k<<<grid, kThreads, smem, stream>>>(map_a, map_b, a);

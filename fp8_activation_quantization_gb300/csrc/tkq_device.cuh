@@ -195,6 +195,14 @@ __device__ __forceinline__ void st_stream(float* p, float v) {
     asm volatile("st.global.cs.f32 [%0], %1;" ::"l"(p), "f"(v) : "memory");
 }
 
+// A whole 32-byte sector (p 32-byte aligned) in one store.
+__device__ __forceinline__ void st_sector(void* p, const uint32_t* v) {
+    if (!access_ok(p, 32, true)) return;
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 // Plain stores and the counter update, checked the same way.
 __device__ __forceinline__ void st_plain(uint8_t* p, uint8_t v) {
     if (access_ok(p, 1, true)) *p = v;
