@@ -32,11 +32,19 @@ namespace {
 constexpr int kBM = 128, kBN = 256, kBK = 128;
 constexpr int kStages = 4;
 constexpr int kEpilogueWarps = 8;
-// Three warpgroups: the registers of the launch, 168 a thread, are split 216 for the two
-// that hold a tile's sums (128 a thread) and 72 for the one that copies and multiplies.
+constexpr int kCols = kBN / (kEpilogueWarps / 4);  // columns of a warp
+// Three warpgroups: the registers of the launch, 168 a thread, are split between the two
+// that hold a tile's sums (128 a thread) and the one that copies and multiplies.  The
+// splits measured, ms at 65536 rows and 4096 x 4096: rows' product 208 / 88: 0.96, 216 /
+// 72: 1.14, 224 / 56: 1.04; gradient, whose sums take the columns' scales too, 208 / 88:
+// 1.74, 216 / 72: 1.65, 224 / 56: 1.68.
 constexpr int kThreads = (kEpilogueWarps + 4) * 32;
-constexpr int kSumRegs = 216, kOtherRegs = 72;
-static_assert(2 * kSumRegs + kOtherRegs <= 3 * 168, "shares of the launch's registers");
+template <bool GRAD>
+struct Split {
+    static constexpr int kSum = GRAD ? 216 : 208, kOther = GRAD ? 72 : 88;
+    static constexpr int kUnroll = GRAD ? 2 : 8;  // scales' copies issued at a time
+    static_assert(2 * kSum + kOther <= 3 * 168, "shares of the launch's registers");
+};
 constexpr uint32_t kBytesA = kBM * kBK, kBytesB = kBN * kBK;
 constexpr uint32_t kStageBytes = kBytesA + kBytesB;
 constexpr uint32_t kTmemCols = 2 * kBN;
@@ -68,24 +76,6 @@ struct Args {
     uint32_t idesc;
     unsigned int* status;
 };
-
-// Two binary32 values in one 64-bit register, and the packed operations on them: sums
-// kept that way need no moves around each operation.
-__device__ __forceinline__ uint64_t pair64(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul64(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma64(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
 
 // Arrives on `bar` when this thread's asynchronous copies so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
@@ -203,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Tile t;
 
     if (warp >= kEpilogueWarps) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Split<GRAD>::kOther));
       if (warp == kEpilogueWarps) {
         // ------------------------------------------------------------ copies
         if (lane == 0) {
@@ -268,6 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         // ------------------------------------------------------------ scales
         const int groups_all = GRAD ? a.R / kBK : a.K / kBK;
+        constexpr int kUnroll = Split<GRAD>::kUnroll;
         const int q = lane & 3, r8 = lane >> 2, half = warp & 1;  // a warp: 8 rows' four groups
         RingPos<kUnits> pos;
         bool ok = true;
@@ -284,14 +275,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (g0 + q < t.groups) {
                     const int g = t.g0 + g0 + q;
                     // rows and columns beyond the edges: the last scale there is
-#pragma unroll
+#pragma unroll kUnroll
                     for (int i = 0; i < kBM / 16; ++i) {
                         const int r = (2 * i + half) * 8 + r8;
                         const int row = t.row + r < rows_end ? t.row + r : rows_end - 1;
                         cp_async4(&sc.a[q][r], a.a_sf + static_cast<int64_t>(row) * groups_all + g);
                     }
                     if constexpr (GRAD) {
-#pragma unroll
+#pragma unroll kUnroll
                         for (int i = 0; i < kBN / 16; ++i) {
                             const int r = (2 * i + half) * 8 + r8;
                             const int col = t.col + r < a.K ? t.col + r : a.K - 1;
@@ -311,50 +302,46 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else {
         // ---------------------------------------------------- scales and sums
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
-        const int quarter = warp & 3, half = warp >> 2;  // TMEM lanes, columns
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Split<GRAD>::kSum));
+        const int quarter = warp & 3, part = warp >> 2;  // TMEM lanes, columns
         const int row_in = quarter * 32 + lane;
-        const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * 128;
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + part * kCols;
         RingPos<2> acc;
         RingPos<kUnits> pos;
         bool ok = true;
         for (; ok && walk.get(a, sm, t); walk.next()) {
-            uint64_t sum[64];  // pairs of binary32
+            uint64_t sum[kCols / 2];  // pairs of binary32
 #pragma unroll
-            for (int i = 0; i < 64; ++i) sum[i] = 0;
+            for (int i = 0; i < kCols / 2; ++i) sum[i] = 0;
             for (int g = 0; g < t.groups; ++g) {
                 const int q = g & (kUnit - 1);
-                if (q == 0) ok = mbar_wait_bounded(&sm.sc_full[pos.stage], pos.phase, &sm.abort, a.status);
-                if (ok) ok = mbar_wait_bounded(&sm.acc_full[acc.stage], acc.phase, &sm.abort, a.status);
+                if (q == 0) ok = mbar_wait_lean(&sm.sc_full[pos.stage], pos.phase, &sm.abort, a.status);
+                if (ok) ok = mbar_wait_lean(&sm.acc_full[acc.stage], acc.phase, &sm.abort, a.status);
                 if (!__all_sync(0xffffffffu, ok)) {
                     if (lane == 0) *static_cast<volatile int*>(&sm.abort) = 1;
                     ok = false;
                     break;
                 }
                 const Scales<GRAD>& sc = scales[pos.stage];
-                const float s = GRAD ? sc.a[q][row_in] : sc.a[q][row_in] * sc.b[q][half];
-                const uint64_t s2 = pair64(s, s);
+                const float s = GRAD ? sc.a[q][row_in] : sc.a[q][row_in] * sc.b[q][part * kCols / 128];
+                const uint64_t s2 = static_cast<uint64_t>(__float_as_uint(s)) << 32 | __float_as_uint(s);
                 tmem_fence_after();
                 const uint32_t from = lane_base + acc.stage * kBN;
-                // the next 16 columns are on their way while these are added
-                uint32_t v[2][16];
-                tmem_load16(from, v[0]);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    tmem_load_wait(v[c & 1]);
-                    if (c < 7) {
-                        tmem_load16(from + (c + 1) * 16, v[(c + 1) & 1]);
-                    } else {
+                for (int c = 0; c < kCols / 16; ++c) {
+                    uint64_t v[8];
+                    tmem_read16(from + c * 16, v);
+                    if (c == kCols / 16 - 1) {
                         tmem_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&sm.acc_empty[acc.stage]);
                     }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        uint64_t p = pair64(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1]));
+                        uint64_t p = v[i];
                         if constexpr (GRAD)
-                            p = mul64(p, *reinterpret_cast<const uint64_t*>(&sc.b[q][half * 128 + c * 16 + 2 * i]));
-                        sum[c * 8 + i] = fma64(p, s2, sum[c * 8 + i]);
+                            p = mul_pair(p, *reinterpret_cast<const uint64_t*>(&sc.b[q][part * kCols + c * 16 + 2 * i]));
+                        sum[c * 8 + i] = fma_pair(p, s2, sum[c * 8 + i]);
                     }
                 }
                 acc.advance();
@@ -364,35 +351,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     pos.advance();
                 }
             }
-            const int row = t.row + row_in, col = t.col + half * 128;
+            const int row = t.row + row_in, col = t.col + part * kCols;
             const bool live = row < (GRAD ? a.N : sm.start[t.e + 1]) && col < (GRAD ? a.K : a.N);
             if (!ok || !live) continue;
             const int64_t at = GRAD ? (static_cast<int64_t>(t.e) * a.N + row) * a.K + col
                                     : static_cast<int64_t>(row) * a.N + col;
             // a lane's row in whole sectors of 32 bytes
-            if constexpr (F32) {
-                float* o = static_cast<float*>(a.out) + at;
+            const auto value = [&](int i) {
+                return static_cast<uint32_t>(i & 1 ? sum[i / 2] >> 32 : sum[i / 2]);
+            };
+            constexpr int kPer = F32 ? 8 : 16;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    uint32_t w[8];
+            for (int i = 0; i < kCols; i += kPer) {
+                uint32_t w[8];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        w[2 * j] = static_cast<uint32_t>(sum[4 * i + j]);
-                        w[2 * j + 1] = static_cast<uint32_t>(sum[4 * i + j] >> 32);
-                    }
-                    st_sector(o + 8 * i, w);
-                }
-            } else {
-                uint16_t* o = static_cast<uint16_t*>(a.out) + at;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    uint32_t w[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        w[j] = pack_bf16x2(__uint_as_float(static_cast<uint32_t>(sum[8 * i + j])),
-                                           __uint_as_float(static_cast<uint32_t>(sum[8 * i + j] >> 32)));
-                    st_sector(o + 16 * i, w);
-                }
+                for (int j = 0; j < 8; ++j)
+                    w[j] = F32 ? value(i + j)
+                               : pack_bf16x2(__uint_as_float(value(i + 2 * j)), __uint_as_float(value(i + 2 * j + 1)));
+                st_sector(static_cast<uint8_t*>(a.out) + (at + i) * (F32 ? 4 : 2), w);
             }
         }
     }

@@ -79,6 +79,17 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
     }
 }
 
+// The same with everything but the first try out of line: a kernel short of registers
+// keeps none for it.
+static __device__ __noinline__ bool mbar_wait_rest(uint64_t* bar, uint32_t parity, const volatile int* abort,
+                                                   unsigned int* status) {
+    return mbar_wait_bounded(bar, parity, abort, status);
+}
+__device__ __forceinline__ bool mbar_wait_lean(uint64_t* bar, uint32_t parity, const volatile int* abort,
+                                               unsigned int* status) {
+    return mbar_try_wait(bar, parity) || mbar_wait_rest(bar, parity, abort, status);
+}
+
 // 2-D tiled TMA load of one box into shared memory, completing on `bar`.
 // x is the innermost coordinate (elements); x * element size must be a
 // multiple of 16 bytes.
