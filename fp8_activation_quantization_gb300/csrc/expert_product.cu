@@ -383,9 +383,9 @@ template <bool GRAD, bool F32>
 cudaError_t launch(const ExpertProduct& p, int64_t tiles, cudaStream_t stream) {
     CUtensorMap map_a, map_b;
     const bool made =
-        GRAD ? encode_u8_2d_swizzled(&map_a, p.a, p.R, p.N, kBM) && encode_u8_2d_swizzled(&map_b, p.b, p.R, p.K, kBN)
-             : encode_u8_2d_swizzled(&map_a, p.a, p.K, p.R, kBM) &&
-                   encode_u8_2d_swizzled(&map_b, p.b, p.K, p.E * p.N, kBN);
+        GRAD ? encode_u8_2d_swizzled(&map_a, p.a, p.R, p.N, kBK, kBM) && encode_u8_2d_swizzled(&map_b, p.b, p.R, p.K, kBK, kBN)
+             : encode_u8_2d_swizzled(&map_a, p.a, p.K, p.R, kBK, kBM) &&
+                   encode_u8_2d_swizzled(&map_b, p.b, p.K, p.E * p.N, kBK, kBN);
     if (!made) return cudaErrorInvalidValue;
     Args a = {};
     a.a_sf = p.a_sf;

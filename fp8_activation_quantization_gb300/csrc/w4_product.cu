@@ -14,10 +14,12 @@
 // the eight columns, so the weights go from memory to the tensor core once however many
 // rows there are.  (tcgen05 would want 128 of either, and its operands in shared memory
 // in 8 bits: the weights would have to be widened and stored there first.)
-// A warp takes 32 rows of a matrix, 128 channels at a time, from a ring of its own in
-// shared memory, filled by asynchronous copies; S warps share those rows, each taking
-// every S-th block of 128 channels, where there are too few rows to occupy the machine.
-// No warp waits for another but at the end of shared rows.
+// A warp takes 64 rows of a matrix, 128 channels at a time, from a ring of its own in
+// shared memory: one TMA box of 64 rows of 64 bytes and a bulk copy for each row of x.
+// (Copies of 16 bytes a lane, 32 rows a warp, took 134 us for 48 rows of 8 of 64 matrices
+// of 4096 x 2048, 70 of them without any arithmetic.)  S warps share those rows, each
+// taking every S-th block of 128 channels, where there are too few rows to occupy the
+// machine.  No warp waits for another but at the end of shared rows.
 #include <cuda_runtime.h>
 
 #include "tkq_async.cuh"
@@ -27,32 +29,34 @@
 namespace tkq {
 namespace {
 
-constexpr int kWarps = 16;
+constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kRows = 32;        // rows of a matrix a warp takes
+constexpr int kRows = 64;        // rows of a matrix a warp takes
+constexpr int kTiles = kRows / 16;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxPairs = 1024;
+constexpr int kDepth = 4;        // stages of a warp's ring: what fits 227 KB with 16 rows of x
+constexpr int kPitch = 144;      // bytes from row to row of x: four rows' equal pieces lie in different banks
 
-// One stage of a warp's ring: 128 channels of 32 rows of weights and of 8 NT rows of x,
-// with their scales.  The 16-byte pieces of a row are permuted so that eight rows' equal
-// pieces, and four rows' equal 32 bytes of x, lie in different banks.
+// One stage of a warp's ring: 128 channels of 64 rows of weights (64-byte swizzle,
+// aligned to its 512 bytes) and, apart from them, of 8 NT rows of x, and both scales.
+constexpr int kBytesW = kRows * 64;
 template <int NT>
-struct Stage {
-    uint8_t w[kRows * 64];
-    uint8_t x[8 * NT * 128];
+struct alignas(16) Side {
+    uint8_t x[8 * NT * kPitch];
     uint32_t ws[kRows];
     float xs[8 * NT];
 };
-template <int NT>
-constexpr int kDepth = NT == 1 ? 4 : 3;  // stages: what fits 227 KB
 
 // What a CTA knows of the rows: the pairs of each expert in turn, cut into runs of at
 // most 8 NT.
 struct Plan {
-    int count[kMaxExperts];
-    int first[kMaxExperts];       // first of its pairs in `pair`
+    uint64_t full[kWarps][kDepth];
+    uint16_t count[kMaxExperts];
+    uint16_t first[kMaxExperts];  // first of its pairs in `pair`
     int sums[2][kWarps];
     int runs;
+    int abort;
     uint16_t pair[kMaxPairs];
     uint16_t run_first[kMaxPairs];
     uint16_t run_expert[kMaxPairs];
@@ -62,12 +66,12 @@ struct Plan {
 struct Args {
     const uint8_t* x;        // [M, K]
     const float* xs;         // [M, K/128]
-    const uint8_t* w;        // [E, N, K/2]
     const uint32_t* ws;      // [E, N, K/128] words: four UE8M0 bytes or one fp32
     const int32_t* ids;      // [P] or null
     uint16_t* out;           // [P, N]
     int P, N, K, E, share;   // x's row of pair p is p / share
     int S;
+    unsigned int* status;
 };
 
 // Eight E2M1 weights of a word as four binary16 pairs, the low nibble first.
@@ -101,21 +105,31 @@ struct Cursor {
     int expert, first, rows;
 };
 
+// The pairs of each expert, cut into runs, by one warp in the order of the pairs, so that
+// every CTA makes the same runs; the scan over the experts by all.
 template <int NT>
 __device__ void make_plan(Plan& pl, const Args& a) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int kPer = kMaxExperts / kThreads;  // experts of a thread, in turn
     for (int e = tid; e < a.E; e += kThreads) pl.count[e] = 0;
     __syncthreads();
-    for (int p = tid; p < a.P; p += kThreads) {
-        const int e = a.ids ? ld_ro(a.ids + p) : 0;
-        if (e >= 0 && e < a.E) atomicAdd(&pl.count[e], 1);
-    }
+    if (warp == 0)
+        for (int p0 = 0; p0 < a.P; p0 += 32) {
+            const int p = p0 + lane;
+            const int e = p < a.P ? (a.ids ? ld_ro(a.ids + p) : 0) : -1;
+            const unsigned same = __match_any_sync(0xffffffffu, e);
+            if (e >= 0 && e < a.E && lane == __ffs(same) - 1) pl.count[e] += __popc(same);
+            __syncwarp();
+        }
     __syncthreads();
-    // first pairs and runs of the experts: a scan over two experts a thread
-    const int e0 = 2 * tid;
-    int n0 = e0 < a.E ? pl.count[e0] : 0, n1 = e0 + 1 < a.E ? pl.count[e0 + 1] : 0;
-    int r0 = (n0 + 8 * NT - 1) / (8 * NT), r1 = (n1 + 8 * NT - 1) / (8 * NT);
-    int n = n0 + n1, r = r0 + r1;
+    int n = 0, r = 0, cnt[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        cnt[i] = tid * kPer + i < a.E ? pl.count[tid * kPer + i] : 0;
+        n += cnt[i];
+        r += (cnt[i] + 8 * NT - 1) / (8 * NT);
+    }
+    const int n_mine = n, r_mine = r;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int un = __shfl_up_sync(0xffffffffu, n, o), ur = __shfl_up_sync(0xffffffffu, r, o);
@@ -129,26 +143,24 @@ __device__ void make_plan(Plan& pl, const Args& a) {
         pl.sums[1][warp] = r;
     }
     __syncthreads();
-    int bn = 0, br = 0;
+    int at_n = n - n_mine, at_r = r - r_mine;
     for (int w = 0; w < warp; ++w) {
-        bn += pl.sums[0][w];
-        br += pl.sums[1][w];
+        at_n += pl.sums[0][w];
+        at_r += pl.sums[1][w];
     }
-    if (tid == kThreads - 1) pl.runs = br + r;
-    const int at_n = bn + n - n0 - n1, at_r = br + r - r0 - r1;
-    const auto runs_of = [&](int e, int c, int f, int q) {
-        if (e < a.E) pl.first[e] = f;
-        for (int i = 0; i < c; i += 8 * NT, ++q) {
-            pl.run_first[q] = static_cast<uint16_t>(f + i);
-            pl.run_expert[q] = static_cast<uint16_t>(e);
-            pl.run_rows[q] = static_cast<uint8_t>(c - i < 8 * NT ? c - i : 8 * NT);
+    if (tid == kThreads - 1) pl.runs = at_r + r_mine;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int e = tid * kPer + i;
+        if (e < a.E) pl.first[e] = static_cast<uint16_t>(at_n);
+        for (int k = 0; k < cnt[i]; k += 8 * NT, ++at_r) {
+            pl.run_first[at_r] = static_cast<uint16_t>(at_n + k);
+            pl.run_expert[at_r] = static_cast<uint16_t>(e);
+            pl.run_rows[at_r] = static_cast<uint8_t>(cnt[i] - k < 8 * NT ? cnt[i] - k : 8 * NT);
         }
-    };
-    runs_of(e0, n0, at_n, at_r);
-    runs_of(e0 + 1, n1, at_n + n0, at_r + r0);
+        at_n += cnt[i];
+    }
     __syncthreads();
-    // an expert's pairs in rising order, by one warp, so that every CTA cuts them into the
-    // same runs
     if (warp == 0)
         for (int p0 = 0; p0 < a.P; p0 += 32) {
             const int p = p0 + lane;
@@ -159,7 +171,7 @@ __device__ void make_plan(Plan& pl, const Args& a) {
             __syncwarp();
             if (live) {
                 pl.pair[at + __popc(same & ((1u << lane) - 1u))] = static_cast<uint16_t>(p);
-                if (lane == __ffs(same) - 1) pl.first[e] = at + __popc(same);
+                if (lane == __ffs(same) - 1) pl.first[e] = static_cast<uint16_t>(at + __popc(same));
             }
             __syncwarp();
         }
@@ -167,15 +179,23 @@ __device__ void make_plan(Plan& pl, const Args& a) {
 }
 
 template <int NT, bool G32, int FMT>
-__global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
-    extern __shared__ __align__(16) uint8_t raw[];
-    using St = Stage<NT>;
-    constexpr int D = kDepth<NT>;
-    Plan& pl = *reinterpret_cast<Plan*>(raw);
-    float* parts = reinterpret_cast<float*>(raw + (sizeof(Plan) + 15) / 16 * 16);  // [kWarps][4][32]
+__global__ void __launch_bounds__(kThreads, 1)
+    w4_kernel(const __grid_constant__ CUtensorMap map_w, const Args a) {
+    extern __shared__ uint8_t raw[];
+    using St = Side<NT>;
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 511) & ~uintptr_t{511});
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    St* ring = reinterpret_cast<St*>(reinterpret_cast<uint8_t*>(parts) + kWarps * 4 * 32 * 4) + warp * D;
+    uint8_t* ring_w = base + warp * kDepth * kBytesW;
+    St* ring = reinterpret_cast<St*>(base + kWarps * kDepth * kBytesW) + warp * kDepth;
+    uint8_t* rest = base + kWarps * kDepth * (kBytesW + sizeof(St));
+    Plan& pl = *reinterpret_cast<Plan*>(rest);
+    float* parts = reinterpret_cast<float*>(rest + (sizeof(Plan) + 15) / 16 * 16);  // [kWarps][4][32]
+    uint64_t* full = pl.full[warp];
     const int g = lane >> 2, t = lane & 3;
+    if (lane == 0)
+        for (int i = 0; i < kDepth; ++i) mbar_init(&full[i], 1);
+    if (threadIdx.x == 0) pl.abort = 0;
+    fence_barrier_init();
     make_plan<NT>(pl, a);
 
     const int KB = a.K / 128, NB = a.N / kRows;
@@ -197,7 +217,9 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
     Cursor ld, at;
     ld.expert = ld.first = ld.rows = at.expert = at.first = at.rows = 0;
     place(ld, load_item);
-    int slot_in = 0, slot = 0;
+    RingPos<kDepth> in, out;
+    int on_way = 0;      // stages asked for and not yet waited for
+    bool dead = false;   // a wait gave up: nothing is asked for or waited for any more
 
     // issues the copies of the next block of this warp's work, if there is one
     const auto load_next = [&]() {
@@ -205,93 +227,107 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
             load_item += step;
             place(ld, load_item);
         }
-        if (load_item < items) {
-            St& s = ring[slot_in];
-            const int64_t row0 = static_cast<int64_t>(ld.expert) * a.N + ld.block_row * kRows;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = i * 8 + (lane >> 2), c = lane & 3;
-                cp_async16(s.w + r * 64 + ((c ^ ((r >> 1) & 3)) << 4),
-                           a.w + (row0 + r) * (a.K / 2) + ld.kb * 64 + c * 16);
-            }
-            cp_async4(&s.ws[lane], a.ws + (row0 + lane) * KB + ld.kb);
-#pragma unroll
-            for (int i = 0; i < 2 * NT; ++i) {
-                const int j = i * 4 + (lane >> 3), c = lane & 7;
-                if (j < ld.rows) {
-                    const int64_t xr = pl.pair[ld.first + j] / a.share;
-                    cp_async16(s.x + j * 128 + ((((c >> 1) ^ (j & 3)) << 1 | (c & 1)) << 4),
-                               a.x + xr * a.K + ld.kb * 128 + c * 16);
-                }
-            }
+        if (load_item < items && !dead) {
+            St& s = ring[in.stage];
+            uint64_t* bar = &full[in.stage];
+            const int row0 = ld.expert * a.N + ld.block_row * kRows;
+            if (lane == 0) mbar_arrive_expect_tx(bar, kBytesW + ld.rows * 128);
+            __syncwarp();
+            if (lane == 0) tma_load_2d(ring_w + in.stage * kBytesW, &map_w, ld.kb * 64, row0, bar);
             if (lane < ld.rows) {
                 const int64_t xr = pl.pair[ld.first + lane] / a.share;
+                if (access_ok(a.x + xr * a.K + ld.kb * 128, 128, false))
+                    bulk_load(s.x + lane * kPitch, a.x + xr * a.K + ld.kb * 128, 128, bar);
                 cp_async4(&s.xs[lane], a.xs + xr * KB + ld.kb);
             }
+#pragma unroll
+            for (int i = 0; i < kRows / 32; ++i)
+                cp_async4(&s.ws[i * 32 + lane], a.ws + static_cast<int64_t>(row0 + i * 32 + lane) * KB + ld.kb);
             ld.kb += a.S;
+            in.advance();
+            ++on_way;
         }
         cp_async_commit();
-        slot_in = slot_in + 1 == D ? 0 : slot_in + 1;
     };
 #pragma unroll
-    for (int i = 0; i < D - 1; ++i) load_next();
+    for (int i = 0; i < kDepth - 1; ++i) load_next();
 
     for (; item < items; item += step) {
         place(at, item);
-        float acc[2][NT][4];
+        float acc[kTiles][NT][4];
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < kTiles; ++m)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
         for (; at.kb < KB; at.kb += a.S) {
             load_next();
-            cp_async_wait(D);
+            if (!dead) {
+                const bool ok = mbar_wait_bounded(&full[out.stage], out.phase, &pl.abort, a.status);
+                dead = !__all_sync(0xffffffffu, ok);
+                if (dead && lane == 0) *static_cast<volatile int*>(&pl.abort) = 1;
+            }
+            if (dead) continue;
+            cp_async_wait(kDepth);
             __syncwarp();
-            const St& s = ring[slot];
-            slot = slot + 1 == D ? 0 : slot + 1;
-            float blk[2][NT][4];
+            const St& s = ring[out.stage];
+            const uint8_t* w = ring_w + out.stage * kBytesW;
+            out.advance();
+            --on_way;
+            float blk[kTiles][NT][4];
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
+            for (int m = 0; m < kTiles; ++m)
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) blk[m][n][i] = 0.0f;
-            uint32_t ws[4];
+            uint32_t ws[2 * kTiles];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) ws[q] = s.ws[q * 8 + g];
+            for (int q = 0; q < 2 * kTiles; ++q) ws[q] = s.ws[q * 8 + g];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                uint32_t v[4];
-                asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                             : "r"(smem_u32(s.w + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4))));
-                uint32_t h[4][4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) decode_e2m1(v[q], h[q]);
+                uint32_t b[NT][4];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    const int j = n * 8 + g;
-                    const uint2 xv = *reinterpret_cast<const uint2*>(s.x + j * 128 + ((i ^ (j & 3)) << 5) + t * 8);
-                    const uint32_t b0 = fp8x2_to_f16x2<FMT>(xv.x & 0xFFFFu), b1 = fp8x2_to_f16x2<FMT>(xv.x >> 16);
-                    const uint32_t b2 = fp8x2_to_f16x2<FMT>(xv.y & 0xFFFFu), b3 = fp8x2_to_f16x2<FMT>(xv.y >> 16);
+                    const uint2 xv = *reinterpret_cast<const uint2*>(s.x + (n * 8 + g) * kPitch + i * 32 + t * 8);
+                    b[n][0] = fp8x2_to_f16x2<FMT>(xv.x & 0xFFFFu);
+                    b[n][1] = fp8x2_to_f16x2<FMT>(xv.x >> 16);
+                    b[n][2] = fp8x2_to_f16x2<FMT>(xv.y & 0xFFFFu);
+                    b[n][3] = fp8x2_to_f16x2<FMT>(xv.y >> 16);
+                }
 #pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        const uint32_t(&lo)[4] = h[2 * m], (&hi)[4] = h[2 * m + 1];
+                for (int m2 = 0; m2 < kTiles / 2; ++m2) {
+                    uint32_t v[4];
+                    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                                 : "r"(smem_u32(w + (m2 * 32 + lane) * 64 + ((i ^ ((lane >> 1) & 3)) << 4))));
+                    uint32_t h[4][4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) decode_e2m1(v[q], h[q]);
+#pragma unroll
+                    for (int mm = 0; mm < 2; ++mm) {
+                        const int m = 2 * m2 + mm;
+                        const uint32_t(&lo)[4] = h[2 * mm], (&hi)[4] = h[2 * mm + 1];
+                        float s0 = 0.0f, s1 = 0.0f;
                         if constexpr (G32) {
-                            float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                            mma_16816(p, lo[0], hi[0], lo[1], hi[1], b0, b1);
-                            mma_16816(p, lo[2], hi[2], lo[3], hi[3], b2, b3);
-                            const float s0 = ue8m0(ws[2 * m] >> (8 * i) & 0xFFu);
-                            const float s1 = ue8m0(ws[2 * m + 1] >> (8 * i) & 0xFFu);
-                            blk[m][n][0] = fmaf(p[0], s0, blk[m][n][0]);
-                            blk[m][n][1] = fmaf(p[1], s0, blk[m][n][1]);
-                            blk[m][n][2] = fmaf(p[2], s1, blk[m][n][2]);
-                            blk[m][n][3] = fmaf(p[3], s1, blk[m][n][3]);
-                        } else {
-                            mma_16816(blk[m][n], lo[0], hi[0], lo[1], hi[1], b0, b1);
-                            mma_16816(blk[m][n], lo[2], hi[2], lo[3], hi[3], b2, b3);
+                            s0 = ue8m0(ws[2 * m] >> (8 * i) & 0xFFu);
+                            s1 = ue8m0(ws[2 * m + 1] >> (8 * i) & 0xFFu);
+                        }
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            if constexpr (G32) {
+                                float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                                mma_16816(p, lo[0], hi[0], lo[1], hi[1], b[n][0], b[n][1]);
+                                mma_16816(p, lo[2], hi[2], lo[3], hi[3], b[n][2], b[n][3]);
+                                blk[m][n][0] = fmaf(p[0], s0, blk[m][n][0]);
+                                blk[m][n][1] = fmaf(p[1], s0, blk[m][n][1]);
+                                blk[m][n][2] = fmaf(p[2], s1, blk[m][n][2]);
+                                blk[m][n][3] = fmaf(p[3], s1, blk[m][n][3]);
+                            } else {
+                                mma_16816(blk[m][n], lo[0], hi[0], lo[1], hi[1], b[n][0], b[n][1]);
+                                mma_16816(blk[m][n], lo[2], hi[2], lo[3], hi[3], b[n][2], b[n][3]);
+                            }
                         }
                     }
                 }
@@ -300,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
             for (int n = 0; n < NT; ++n) {
                 const float2 xs = *reinterpret_cast<const float2*>(&s.xs[n * 8 + 2 * t]);
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
+                for (int m = 0; m < kTiles; ++m) {
                     const float s0 = G32 ? 1.0f : __uint_as_float(ws[2 * m]);
                     const float s1 = G32 ? 1.0f : __uint_as_float(ws[2 * m + 1]);
                     acc[m][n][0] = fmaf(blk[m][n][0], xs.x * s0, acc[m][n][0]);
@@ -309,13 +345,15 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
                     acc[m][n][3] = fmaf(blk[m][n][3], xs.y * s1, acc[m][n][3]);
                 }
             }
-            __syncwarp();  // the stage is refilled by the next copies
+            // the stage is refilled by the next copies, made in the async proxy
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
         }
         // this lane's results: rows 16 m + g (+ 8), columns 8 n + 2 t (+ 1)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
+            for (int m = 0; m < kTiles; ++m) {
                 float(&v)[4] = acc[m][n];
                 if (a.S > 1) {
                     // shared rows: the team's first warp adds the others' in their order
@@ -333,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int j = n * 8 + 2 * t + (i & 1);
-                    if (j < at.rows) {
+                    if (j < at.rows && !dead) {
                         const int row = at.block_row * kRows + m * 16 + (i >> 1) * 8 + g;
                         st_plain(a.out + static_cast<int64_t>(pl.pair[at.first + j]) * a.N + row,
                                  static_cast<uint16_t>(pack_bf16x2(v[i], 0.0f)));
@@ -341,6 +379,9 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
                 }
             }
     }
+    // after a wait that gave up, copies still on their way land before the CTA leaves
+    for (; on_way > 0; --on_way, out.advance())
+        mbar_wait_bounded(&full[out.stage], out.phase, nullptr, a.status);
     // pairs of no expert get zeros
     if (a.ids)
         for (int p = blockIdx.x * kWarps + warp; p < a.P; p += gridDim.x * kWarps) {
@@ -352,12 +393,11 @@ __global__ void __launch_bounds__(kThreads, 1) w4_kernel(const Args a) {
 }
 
 template <int NT, bool G32, int FMT>
-cudaError_t launch(Args a, int64_t items, cudaStream_t stream) {
+cudaError_t launch(const CUtensorMap& map, Args a, int64_t items, cudaStream_t stream) {
     auto* k = &w4_kernel<NT, G32, FMT>;
-    const size_t smem = (sizeof(Plan) + 15) / 16 * 16 + kWarps * 4 * 32 * 4 +
-                        kWarps * kDepth<NT> * sizeof(Stage<NT>);
-    static_assert((sizeof(Plan) + 15) / 16 * 16 + kWarps * 4 * 32 * 4 + kWarps * kDepth<NT> * sizeof(Stage<NT>) <=
-                      227 * 1024 && sizeof(Stage<NT>) % 16 == 0, "shared memory");
+    constexpr size_t smem =
+        kWarps * kDepth * (kBytesW + sizeof(Side<NT>)) + (sizeof(Plan) + 15) / 16 * 16 + kWarps * 4 * 32 * 4 + 512;
+    static_assert(smem <= 227 * 1024, "shared memory");
     const int64_t warps = static_cast<int64_t>(num_sms()) * kWarps;
     // warps that share rows: as many as leave no warp without work, at most one a block of channels
     a.S = 1;
@@ -365,17 +405,17 @@ cudaError_t launch(Args a, int64_t items, cudaStream_t stream) {
     const int64_t blocks = (items * a.S + kWarps - 1) / kWarps;
     const int grid = persistent_grid(reinterpret_cast<const void*>(k), kThreads, smem, blocks);
     if (const cudaError_t e = upload_checks(stream)) return e;
-    k<<<grid, kThreads, smem, stream>>>(a);
+    k<<<grid, kThreads, smem, stream>>>(map, a);
     return cudaGetLastError();
 }
 
 template <int NT>
-cudaError_t launch_form(const Args& a, bool g32, int fmt, int64_t items, cudaStream_t stream) {
+cudaError_t launch_form(const CUtensorMap& map, const Args& a, bool g32, int fmt, int64_t items, cudaStream_t stream) {
     if (g32)
-        return fmt == kFmtE4M3 ? launch<NT, true, kFmtE4M3>(a, items, stream)
-                               : launch<NT, true, kFmtE5M2>(a, items, stream);
-    return fmt == kFmtE4M3 ? launch<NT, false, kFmtE4M3>(a, items, stream)
-                           : launch<NT, false, kFmtE5M2>(a, items, stream);
+        return fmt == kFmtE4M3 ? launch<NT, true, kFmtE4M3>(map, a, items, stream)
+                               : launch<NT, true, kFmtE5M2>(map, a, items, stream);
+    return fmt == kFmtE4M3 ? launch<NT, false, kFmtE4M3>(map, a, items, stream)
+                           : launch<NT, false, kFmtE5M2>(map, a, items, stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -424,7 +464,6 @@ cudaError_t launch_w4_product(const W4Product& p, cudaStream_t stream) {
     Args a = {};
     a.x = static_cast<const uint8_t*>(p.x);
     a.xs = p.x_sf;
-    a.w = static_cast<const uint8_t*>(p.w);
     a.ws = static_cast<const uint32_t*>(p.w_sf);
     a.ids = p.ids;
     a.out = static_cast<uint16_t*>(p.out);
@@ -433,11 +472,14 @@ cudaError_t launch_w4_product(const W4Product& p, cudaStream_t stream) {
     a.K = static_cast<int>(p.K);
     a.E = p.E;
     a.share = p.each ? 1 : p.k;
+    a.status = device_status_word();
+    CUtensorMap map;
+    if (!encode_u8_2d_swizzled(&map, p.w, p.K / 2, p.E * p.N, 64, kRows)) return cudaErrorInvalidValue;
     const bool g32 = p.group == 32;
     const int64_t experts = p.ids ? (a.P < p.E ? a.P : p.E) : 1;  // at most this many have rows
     const int64_t items = experts * (p.N / kRows);
-    return p.T <= 8 ? launch_form<1>(a, g32, p.fmt, items, stream)
-                    : launch_form<2>(a, g32, p.fmt, items, stream);
+    return p.T <= 8 ? launch_form<1>(map, a, g32, p.fmt, items, stream)
+                    : launch_form<2>(map, a, g32, p.fmt, items, stream);
 }
 
 cudaError_t launch_w4_cast(const void* w, void* codes, void* sf, int64_t N, int64_t K, int group,
