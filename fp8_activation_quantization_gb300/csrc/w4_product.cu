@@ -17,9 +17,10 @@
 // A warp takes 64 rows of a matrix, 128 channels at a time, from a ring of its own in
 // shared memory: one TMA box of 64 rows of 64 bytes and a bulk copy for each row of x.
 // (Copies of 16 bytes a lane, 32 rows a warp, took 134 us for 48 rows of 8 of 64 matrices
-// of 4096 x 2048, 70 of them without any arithmetic.)  S warps share those rows, each
-// taking every S-th block of 128 channels, where there are too few rows to occupy the
-// machine.  No warp waits for another but at the end of shared rows.
+// of 4096 x 2048, 70 of them without any arithmetic.)  A CTA takes an equal share of all
+// rows' blocks, one after another; S of its warps share those of a block, each taking
+// every S-th 128 channels, where otherwise some of the eight would have none left at the
+// end.  No warp waits for another but at the end of shared rows.
 #include <cuda_runtime.h>
 
 #include "tkq_async.cuh"
@@ -52,8 +53,6 @@ struct alignas(16) Side {
 // most 8 NT.
 struct Plan {
     uint64_t full[kWarps][kDepth];
-    uint16_t count[kMaxExperts];
-    uint16_t first[kMaxExperts];  // first of its pairs in `pair`
     int sums[2][kWarps];
     int runs;
     int abort;
@@ -61,6 +60,13 @@ struct Plan {
     uint16_t run_first[kMaxPairs];
     uint16_t run_expert[kMaxPairs];
     uint8_t run_rows[kMaxPairs];
+    union {
+        struct {
+            uint16_t count[kMaxExperts];
+            uint16_t first[kMaxExperts];  // first of its pairs in `pair`
+        };
+        float parts[kWarps][8][32];       // sums of shared rows, after the plan is made
+    };
 };
 
 struct Args {
@@ -70,7 +76,6 @@ struct Args {
     const int32_t* ids;      // [P] or null
     uint16_t* out;           // [P, N]
     int P, N, K, E, share;   // x's row of pair p is p / share
-    int S;
     unsigned int* status;
 };
 
@@ -96,7 +101,7 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
 
 // The scale 2^(b - 127) of a UE8M0 byte.
 __device__ __forceinline__ float ue8m0(uint32_t b) {
-    return __uint_as_float(b ? b << 23 : 0x00400000u);
+    return __uint_as_float(max(b << 23, 0x00400000u));
 }
 
 // A position in a warp's work: run of pairs, 32 rows of its matrix, block of channels.
@@ -178,6 +183,83 @@ __device__ void make_plan(Plan& pl, const Args& a) {
     __syncthreads();
 }
 
+// acc += one stage's products, 8 NV columns of them.
+template <int NV, int NT, bool G32, int FMT>
+__device__ __forceinline__ void multiply(const uint8_t* w, const Side<NT>& s, float (&acc)[kTiles][NT][4],
+                                         int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    float blk[kTiles][NV][4];
+#pragma unroll
+    for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) blk[m][n][i] = 0.0f;
+    uint32_t ws[2 * kTiles];
+#pragma unroll
+    for (int q = 0; q < 2 * kTiles; ++q) ws[q] = s.ws[q * 8 + g];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t b[NV][4];
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const uint2 xv = *reinterpret_cast<const uint2*>(s.x + (n * 8 + g) * kPitch + i * 32 + t * 8);
+            b[n][0] = fp8x2_to_f16x2<FMT>(xv.x & 0xFFFFu);
+            b[n][1] = fp8x2_to_f16x2<FMT>(xv.x >> 16);
+            b[n][2] = fp8x2_to_f16x2<FMT>(xv.y & 0xFFFFu);
+            b[n][3] = fp8x2_to_f16x2<FMT>(xv.y >> 16);
+        }
+#pragma unroll
+        for (int m2 = 0; m2 < kTiles / 2; ++m2) {
+            uint32_t v[4];
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                         : "r"(smem_u32(w + (m2 * 32 + lane) * 64 + ((i ^ ((lane >> 1) & 3)) << 4))));
+            uint32_t h[4][4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) decode_e2m1(v[q], h[q]);
+#pragma unroll
+            for (int mm = 0; mm < 2; ++mm) {
+                const int m = 2 * m2 + mm;
+                const uint32_t(&lo)[4] = h[2 * mm], (&hi)[4] = h[2 * mm + 1];
+                float s0 = 0.0f, s1 = 0.0f;
+                if constexpr (G32) {
+                    s0 = ue8m0(ws[2 * m] >> (8 * i) & 0xFFu);
+                    s1 = ue8m0(ws[2 * m + 1] >> (8 * i) & 0xFFu);
+                }
+#pragma unroll
+                for (int n = 0; n < NV; ++n) {
+                    if constexpr (G32) {
+                        float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                        mma_16816(p, lo[0], hi[0], lo[1], hi[1], b[n][0], b[n][1]);
+                        mma_16816(p, lo[2], hi[2], lo[3], hi[3], b[n][2], b[n][3]);
+                        blk[m][n][0] = fmaf(p[0], s0, blk[m][n][0]);
+                        blk[m][n][1] = fmaf(p[1], s0, blk[m][n][1]);
+                        blk[m][n][2] = fmaf(p[2], s1, blk[m][n][2]);
+                        blk[m][n][3] = fmaf(p[3], s1, blk[m][n][3]);
+                    } else {
+                        mma_16816(blk[m][n], lo[0], hi[0], lo[1], hi[1], b[n][0], b[n][1]);
+                        mma_16816(blk[m][n], lo[2], hi[2], lo[3], hi[3], b[n][2], b[n][3]);
+                    }
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+        const float2 xs = *reinterpret_cast<const float2*>(&s.xs[n * 8 + 2 * t]);
+#pragma unroll
+        for (int m = 0; m < kTiles; ++m) {
+            const float s0 = G32 ? 1.0f : __uint_as_float(ws[2 * m]);
+            const float s1 = G32 ? 1.0f : __uint_as_float(ws[2 * m + 1]);
+            acc[m][n][0] = fmaf(blk[m][n][0], xs.x * s0, acc[m][n][0]);
+            acc[m][n][1] = fmaf(blk[m][n][1], xs.y * s0, acc[m][n][1]);
+            acc[m][n][2] = fmaf(blk[m][n][2], xs.x * s1, acc[m][n][2]);
+            acc[m][n][3] = fmaf(blk[m][n][3], xs.y * s1, acc[m][n][3]);
+        }
+    }
+}
+
 template <int NT, bool G32, int FMT>
 __global__ void __launch_bounds__(kThreads, 1)
     w4_kernel(const __grid_constant__ CUtensorMap map_w, const Args a) {
@@ -189,7 +271,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     St* ring = reinterpret_cast<St*>(base + kWarps * kDepth * kBytesW) + warp * kDepth;
     uint8_t* rest = base + kWarps * kDepth * (kBytesW + sizeof(St));
     Plan& pl = *reinterpret_cast<Plan*>(rest);
-    float* parts = reinterpret_cast<float*>(rest + (sizeof(Plan) + 15) / 16 * 16);  // [kWarps][4][32]
     uint64_t* full = pl.full[warp];
     const int g = lane >> 2, t = lane & 3;
     if (lane == 0)
@@ -199,21 +280,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     make_plan<NT>(pl, a);
 
     const int KB = a.K / 128, NB = a.N / kRows;
-    const int team = warp / a.S, of_team = warp - team * a.S, teams = kWarps / a.S;
+    // this CTA's share of the row blocks, and the warps that share one: the fewest with
+    // which at least nine tenths of the warps' time is used, else the most
     const int items = pl.runs * NB;
-    const int step = gridDim.x * teams;
+    const int64_t grid = gridDim.x;
+    const int begin = static_cast<int>(items * static_cast<int64_t>(blockIdx.x) / grid);
+    const int end = static_cast<int>(items * (static_cast<int64_t>(blockIdx.x) + 1) / grid);
+    const int most = static_cast<int>((items + grid - 1) / grid);
+    int S = 1;
+    while (S < kWarps && 2 * S <= KB) {
+        const int teams = kWarps / S;
+        if (10 * most >= 9 * ((most + teams - 1) / teams * teams)) break;
+        S *= 2;
+    }
+    const int team = warp / S, of_team = warp - team * S, teams = kWarps / S;
 
     const auto place = [&](Cursor& c, int item) {
         c.run = item / NB;
         c.block_row = item - c.run * NB;
         c.kb = of_team;
-        if (item < items) {
+        if (item < end) {
             c.expert = pl.run_expert[c.run];
             c.first = pl.run_first[c.run];
             c.rows = pl.run_rows[c.run];
         }
     };
-    int load_item = blockIdx.x * teams + team, item = load_item;
+    int load_item = begin + team, item = load_item;
     Cursor ld, at;
     ld.expert = ld.first = ld.rows = at.expert = at.first = at.rows = 0;
     place(ld, load_item);
@@ -223,11 +315,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // issues the copies of the next block of this warp's work, if there is one
     const auto load_next = [&]() {
-        while (load_item < items && ld.kb >= KB) {
-            load_item += step;
+        while (load_item < end && ld.kb >= KB) {
+            load_item += teams;
             place(ld, load_item);
         }
-        if (load_item < items && !dead) {
+        if (load_item < end && !dead) {
             St& s = ring[in.stage];
             uint64_t* bar = &full[in.stage];
             const int row0 = ld.expert * a.N + ld.block_row * kRows;
@@ -243,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < kRows / 32; ++i)
                 cp_async4(&s.ws[i * 32 + lane], a.ws + static_cast<int64_t>(row0 + i * 32 + lane) * KB + ld.kb);
-            ld.kb += a.S;
+            ld.kb += S;
             in.advance();
             ++on_way;
         }
@@ -252,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int i = 0; i < kDepth - 1; ++i) load_next();
 
-    for (; item < items; item += step) {
+    for (; item < end; item += teams) {
         place(at, item);
         float acc[kTiles][NT][4];
 #pragma unroll
@@ -261,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
-        for (; at.kb < KB; at.kb += a.S) {
+        for (; at.kb < KB; at.kb += S) {
             load_next();
             if (!dead) {
                 const bool ok = mbar_wait_bounded(&full[out.stage], out.phase, &pl.abort, a.status);
@@ -275,108 +367,45 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint8_t* w = ring_w + out.stage * kBytesW;
             out.advance();
             --on_way;
-            float blk[kTiles][NT][4];
-#pragma unroll
-            for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) blk[m][n][i] = 0.0f;
-            uint32_t ws[2 * kTiles];
-#pragma unroll
-            for (int q = 0; q < 2 * kTiles; ++q) ws[q] = s.ws[q * 8 + g];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t b[NT][4];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const uint2 xv = *reinterpret_cast<const uint2*>(s.x + (n * 8 + g) * kPitch + i * 32 + t * 8);
-                    b[n][0] = fp8x2_to_f16x2<FMT>(xv.x & 0xFFFFu);
-                    b[n][1] = fp8x2_to_f16x2<FMT>(xv.x >> 16);
-                    b[n][2] = fp8x2_to_f16x2<FMT>(xv.y & 0xFFFFu);
-                    b[n][3] = fp8x2_to_f16x2<FMT>(xv.y >> 16);
-                }
-#pragma unroll
-                for (int m2 = 0; m2 < kTiles / 2; ++m2) {
-                    uint32_t v[4];
-                    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                                 : "r"(smem_u32(w + (m2 * 32 + lane) * 64 + ((i ^ ((lane >> 1) & 3)) << 4))));
-                    uint32_t h[4][4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) decode_e2m1(v[q], h[q]);
-#pragma unroll
-                    for (int mm = 0; mm < 2; ++mm) {
-                        const int m = 2 * m2 + mm;
-                        const uint32_t(&lo)[4] = h[2 * mm], (&hi)[4] = h[2 * mm + 1];
-                        float s0 = 0.0f, s1 = 0.0f;
-                        if constexpr (G32) {
-                            s0 = ue8m0(ws[2 * m] >> (8 * i) & 0xFFu);
-                            s1 = ue8m0(ws[2 * m + 1] >> (8 * i) & 0xFFu);
-                        }
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            if constexpr (G32) {
-                                float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                                mma_16816(p, lo[0], hi[0], lo[1], hi[1], b[n][0], b[n][1]);
-                                mma_16816(p, lo[2], hi[2], lo[3], hi[3], b[n][2], b[n][3]);
-                                blk[m][n][0] = fmaf(p[0], s0, blk[m][n][0]);
-                                blk[m][n][1] = fmaf(p[1], s0, blk[m][n][1]);
-                                blk[m][n][2] = fmaf(p[2], s1, blk[m][n][2]);
-                                blk[m][n][3] = fmaf(p[3], s1, blk[m][n][3]);
-                            } else {
-                                mma_16816(blk[m][n], lo[0], hi[0], lo[1], hi[1], b[n][0], b[n][1]);
-                                mma_16816(blk[m][n], lo[2], hi[2], lo[3], hi[3], b[n][2], b[n][3]);
-                            }
-                        }
-                    }
-                }
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const float2 xs = *reinterpret_cast<const float2*>(&s.xs[n * 8 + 2 * t]);
-#pragma unroll
-                for (int m = 0; m < kTiles; ++m) {
-                    const float s0 = G32 ? 1.0f : __uint_as_float(ws[2 * m]);
-                    const float s1 = G32 ? 1.0f : __uint_as_float(ws[2 * m + 1]);
-                    acc[m][n][0] = fmaf(blk[m][n][0], xs.x * s0, acc[m][n][0]);
-                    acc[m][n][1] = fmaf(blk[m][n][1], xs.y * s0, acc[m][n][1]);
-                    acc[m][n][2] = fmaf(blk[m][n][2], xs.x * s1, acc[m][n][2]);
-                    acc[m][n][3] = fmaf(blk[m][n][3], xs.y * s1, acc[m][n][3]);
-                }
-            }
+            // columns without rows are left out, eight at a time
+            if (NT == 1 || at.rows <= 8)
+                multiply<1, NT, G32, FMT>(w, s, acc, lane);
+            else
+                multiply<NT, NT, G32, FMT>(w, s, acc, lane);
             // the stage is refilled by the next copies, made in the async proxy
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
         }
+        // shared rows: the team's first warp adds the others' in their order
+        if (S > 1)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                if (n * 8 >= at.rows) break;
+#pragma unroll
+                for (int m = 0; m < kTiles; m += 2) {
+                    named_bar_sync(1 + team, S * 32);
+                    if (of_team)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) pl.parts[warp][i][lane] = acc[m + i / 4][n][i & 3];
+                    named_bar_sync(1 + team, S * 32);
+                    if (of_team == 0)
+                        for (int o = 1; o < S; ++o)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) acc[m + i / 4][n][i & 3] += pl.parts[warp + o][i][lane];
+                }
+            }
+        if (of_team || dead) continue;
         // this lane's results: rows 16 m + g (+ 8), columns 8 n + 2 t (+ 1)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int m = 0; m < kTiles; ++m) {
-                float(&v)[4] = acc[m][n];
-                if (a.S > 1) {
-                    // shared rows: the team's first warp adds the others' in their order
-                    float* mine = parts + warp * 128 + lane;
-                    named_bar_sync(1 + team, a.S * 32);
-                    if (of_team)
+            for (int i = 0; i < 2; ++i) {
+                const int j = n * 8 + 2 * t + i;
+                if (j >= at.rows) continue;
+                uint16_t* o = a.out + static_cast<int64_t>(pl.pair[at.first + j]) * a.N + at.block_row * kRows + g;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) mine[i * 32] = v[i];
-                    named_bar_sync(1 + team, a.S * 32);
-                    if (of_team) continue;
-                    for (int o = 1; o < a.S; ++o)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) v[i] += mine[o * 128 + i * 32];
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int j = n * 8 + 2 * t + (i & 1);
-                    if (j < at.rows && !dead) {
-                        const int row = at.block_row * kRows + m * 16 + (i >> 1) * 8 + g;
-                        st_plain(a.out + static_cast<int64_t>(pl.pair[at.first + j]) * a.N + row,
-                                 static_cast<uint16_t>(pack_bf16x2(v[i], 0.0f)));
-                    }
-                }
+                for (int m = 0; m < 2 * kTiles; ++m)
+                    st_plain(o + m * 8, static_cast<uint16_t>(pack_bf16x2(acc[m / 2][n][2 * (m & 1) + i], 0.0f)));
             }
     }
     // after a wait that gave up, copies still on their way land before the CTA leaves
@@ -396,14 +425,9 @@ template <int NT, bool G32, int FMT>
 cudaError_t launch(const CUtensorMap& map, Args a, int64_t items, cudaStream_t stream) {
     auto* k = &w4_kernel<NT, G32, FMT>;
     constexpr size_t smem =
-        kWarps * kDepth * (kBytesW + sizeof(Side<NT>)) + (sizeof(Plan) + 15) / 16 * 16 + kWarps * 4 * 32 * 4 + 512;
+        kWarps * kDepth * (kBytesW + sizeof(Side<NT>)) + sizeof(Plan) + 512;
     static_assert(smem <= 227 * 1024, "shared memory");
-    const int64_t warps = static_cast<int64_t>(num_sms()) * kWarps;
-    // warps that share rows: as many as leave no warp without work, at most one a block of channels
-    a.S = 1;
-    while (a.S < kWarps && a.S * 2 <= a.K / 128 && items * a.S * 2 <= warps) a.S *= 2;
-    const int64_t blocks = (items * a.S + kWarps - 1) / kWarps;
-    const int grid = persistent_grid(reinterpret_cast<const void*>(k), kThreads, smem, blocks);
+    const int grid = persistent_grid(reinterpret_cast<const void*>(k), kThreads, smem, items);
     if (const cudaError_t e = upload_checks(stream)) return e;
     k<<<grid, kThreads, smem, stream>>>(map, a);
     return cudaGetLastError();
