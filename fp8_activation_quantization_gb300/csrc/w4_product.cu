@@ -57,13 +57,14 @@ struct Plan {
     int runs;
     int abort;
     uint16_t pair[kMaxPairs];
-    uint16_t run_first[kMaxPairs];
+    uint16_t xrow[kMaxPairs];         // its row of x
+    uint16_t run_first[kMaxPairs + 2];  // and the end of the last run
     uint16_t run_expert[kMaxPairs];
-    uint8_t run_rows[kMaxPairs];
     union {
         struct {
             uint16_t count[kMaxExperts];
             uint16_t first[kMaxExperts];  // first of its pairs in `pair`
+            int16_t expert[kMaxPairs];    // of each pair, -1 for none
         };
         float parts[kWarps][8][32];       // sums of shared rows, after the plan is made
     };
@@ -99,9 +100,19 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The scale 2^(b - 127) of a UE8M0 byte.
-__device__ __forceinline__ float ue8m0(uint32_t b) {
-    return __uint_as_float(max(b << 23, 0x00400000u));
+// The scales 2^(b - 127) of a word's four UE8M0 bytes.
+__device__ __forceinline__ void decode_ue8m0(uint32_t v, float (&s)[4]) {
+    uint32_t lo, hi;
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "mov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.bf16x2.ue8m0x2 %0, a;\n\t"
+        "cvt.rn.bf16x2.ue8m0x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(v));
+    s[0] = bf16_lo(lo);
+    s[1] = bf16_hi(lo);
+    s[2] = bf16_lo(hi);
+    s[3] = bf16_hi(hi);
 }
 
 // A position in a warp's work: run of pairs, 32 rows of its matrix, block of channels.
@@ -117,13 +128,17 @@ __device__ void make_plan(Plan& pl, const Args& a) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int kPer = kMaxExperts / kThreads;  // experts of a thread, in turn
     for (int e = tid; e < a.E; e += kThreads) pl.count[e] = 0;
+    for (int p = tid; p < a.P; p += kThreads) {
+        const int e = a.ids ? ld_ro(a.ids + p) : 0;
+        pl.expert[p] = static_cast<int16_t>(e >= 0 && e < a.E ? e : -1);
+    }
     __syncthreads();
     if (warp == 0)
         for (int p0 = 0; p0 < a.P; p0 += 32) {
             const int p = p0 + lane;
-            const int e = p < a.P ? (a.ids ? ld_ro(a.ids + p) : 0) : -1;
+            const int e = p < a.P ? pl.expert[p] : -1;
             const unsigned same = __match_any_sync(0xffffffffu, e);
-            if (e >= 0 && e < a.E && lane == __ffs(same) - 1) pl.count[e] += __popc(same);
+            if (e >= 0 && lane == __ffs(same) - 1) pl.count[e] += __popc(same);
             __syncwarp();
         }
     __syncthreads();
@@ -153,7 +168,10 @@ __device__ void make_plan(Plan& pl, const Args& a) {
         at_n += pl.sums[0][w];
         at_r += pl.sums[1][w];
     }
-    if (tid == kThreads - 1) pl.runs = at_r + r_mine;
+    if (tid == kThreads - 1) {
+        pl.runs = at_r + r_mine;
+        pl.run_first[at_r + r_mine] = static_cast<uint16_t>(at_n + n_mine);
+    }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int e = tid * kPer + i;
@@ -161,7 +179,6 @@ __device__ void make_plan(Plan& pl, const Args& a) {
         for (int k = 0; k < cnt[i]; k += 8 * NT, ++at_r) {
             pl.run_first[at_r] = static_cast<uint16_t>(at_n + k);
             pl.run_expert[at_r] = static_cast<uint16_t>(e);
-            pl.run_rows[at_r] = static_cast<uint8_t>(cnt[i] - k < 8 * NT ? cnt[i] - k : 8 * NT);
         }
         at_n += cnt[i];
     }
@@ -169,13 +186,15 @@ __device__ void make_plan(Plan& pl, const Args& a) {
     if (warp == 0)
         for (int p0 = 0; p0 < a.P; p0 += 32) {
             const int p = p0 + lane;
-            const int e = p < a.P ? (a.ids ? ld_ro(a.ids + p) : 0) : -1;
-            const bool live = e >= 0 && e < a.E;
+            const int e = p < a.P ? pl.expert[p] : -1;
+            const bool live = e >= 0;
             const unsigned same = __match_any_sync(0xffffffffu, e);
             const int at = live ? pl.first[e] : 0;
             __syncwarp();
             if (live) {
-                pl.pair[at + __popc(same & ((1u << lane) - 1u))] = static_cast<uint16_t>(p);
+                const int to = at + __popc(same & ((1u << lane) - 1u));
+                pl.pair[to] = static_cast<uint16_t>(p);
+                pl.xrow[to] = static_cast<uint16_t>(p / a.share);
                 if (lane == __ffs(same) - 1) pl.first[e] = static_cast<uint16_t>(at + __popc(same));
             }
             __syncwarp();
@@ -195,9 +214,14 @@ __device__ __forceinline__ void multiply(const uint8_t* w, const Side<NT>& s, fl
         for (int n = 0; n < NV; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) blk[m][n][i] = 0.0f;
-    uint32_t ws[2 * kTiles];
+    float ws[2 * kTiles][G32 ? 4 : 1];
 #pragma unroll
-    for (int q = 0; q < 2 * kTiles; ++q) ws[q] = s.ws[q * 8 + g];
+    for (int q = 0; q < 2 * kTiles; ++q) {
+        if constexpr (G32)
+            decode_ue8m0(s.ws[q * 8 + g], ws[q]);
+        else
+            ws[q][0] = __uint_as_float(s.ws[q * 8 + g]);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         uint32_t b[NV][4];
@@ -224,8 +248,8 @@ __device__ __forceinline__ void multiply(const uint8_t* w, const Side<NT>& s, fl
                 const uint32_t(&lo)[4] = h[2 * mm], (&hi)[4] = h[2 * mm + 1];
                 float s0 = 0.0f, s1 = 0.0f;
                 if constexpr (G32) {
-                    s0 = ue8m0(ws[2 * m] >> (8 * i) & 0xFFu);
-                    s1 = ue8m0(ws[2 * m + 1] >> (8 * i) & 0xFFu);
+                    s0 = ws[2 * m][i];
+                    s1 = ws[2 * m + 1][i];
                 }
 #pragma unroll
                 for (int n = 0; n < NV; ++n) {
@@ -250,8 +274,8 @@ __device__ __forceinline__ void multiply(const uint8_t* w, const Side<NT>& s, fl
         const float2 xs = *reinterpret_cast<const float2*>(&s.xs[n * 8 + 2 * t]);
 #pragma unroll
         for (int m = 0; m < kTiles; ++m) {
-            const float s0 = G32 ? 1.0f : __uint_as_float(ws[2 * m]);
-            const float s1 = G32 ? 1.0f : __uint_as_float(ws[2 * m + 1]);
+            const float s0 = G32 ? 1.0f : ws[2 * m][0];
+            const float s1 = G32 ? 1.0f : ws[2 * m + 1][0];
             acc[m][n][0] = fmaf(blk[m][n][0], xs.x * s0, acc[m][n][0]);
             acc[m][n][1] = fmaf(blk[m][n][1], xs.y * s0, acc[m][n][1]);
             acc[m][n][2] = fmaf(blk[m][n][2], xs.x * s1, acc[m][n][2]);
@@ -302,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (item < end) {
             c.expert = pl.run_expert[c.run];
             c.first = pl.run_first[c.run];
-            c.rows = pl.run_rows[c.run];
+            c.rows = pl.run_first[c.run + 1] - c.first;
         }
     };
     int load_item = begin + team, item = load_item;
@@ -327,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) tma_load_2d(ring_w + in.stage * kBytesW, &map_w, ld.kb * 64, row0, bar);
             if (lane < ld.rows) {
-                const int64_t xr = pl.pair[ld.first + lane] / a.share;
+                const int64_t xr = pl.xrow[ld.first + lane];
                 if (access_ok(a.x + xr * a.K + ld.kb * 128, 128, false))
                     bulk_load(s.x + lane * kPitch, a.x + xr * a.K + ld.kb * 128, 128, bar);
                 cp_async4(&s.xs[lane], a.xs + xr * KB + ld.kb);
