@@ -30,30 +30,34 @@
 namespace tkq {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kRows = 64;        // rows of a matrix a warp takes
-constexpr int kTiles = kRows / 16;
+// What a warp takes: with up to eight rows of x (NT = 1 columns of eight) 32 rows of the
+// matrix, 16 warps a CTA; with up to 16 (NT = 2) 64 rows, 8 warps.
+template <int NT>
+struct Shape {
+    static constexpr int kWarps = NT == 1 ? 16 : 8, kThreads = kWarps * 32;
+    static constexpr int kRows = NT == 1 ? 32 : 64, kTiles = kRows / 16;
+    static constexpr int kPart = kTiles * 2;  // sums of a lane that shared rows exchange at a time
+};
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxPairs = 1024;
 constexpr int kDepth = 4;        // stages of a warp's ring: what fits 227 KB with 16 rows of x
 constexpr int kPitch = 144;      // bytes from row to row of x: four rows' equal pieces lie in different banks
 
-// One stage of a warp's ring: 128 channels of 64 rows of weights (64-byte swizzle,
+// One stage of a warp's ring: 128 channels of 32 or 64 rows of weights (64-byte swizzle,
 // aligned to its 512 bytes) and, apart from them, of 8 NT rows of x, and both scales.
-constexpr int kBytesW = kRows * 64;
 template <int NT>
 struct alignas(16) Side {
     uint8_t x[8 * NT * kPitch];
-    uint32_t ws[kRows];
+    uint32_t ws[Shape<NT>::kRows];
     float xs[8 * NT];
 };
 
 // What a CTA knows of the rows: the pairs of each expert in turn, cut into runs of at
 // most 8 NT.
+template <int NT>
 struct Plan {
-    uint64_t full[kWarps][kDepth];
-    int sums[2][kWarps];
+    uint64_t full[Shape<NT>::kWarps][kDepth];
+    int sums[2][Shape<NT>::kWarps];
     int runs;
     int abort;
     uint16_t pair[kMaxPairs];
@@ -66,7 +70,7 @@ struct Plan {
             uint16_t first[kMaxExperts];  // first of its pairs in `pair`
             int16_t expert[kMaxPairs];    // of each pair, -1 for none
         };
-        float parts[kWarps][8][32];       // sums of shared rows, after the plan is made
+        float parts[Shape<NT>::kWarps][Shape<NT>::kPart][32];  // sums of shared rows, after the plan is made
     };
 };
 
@@ -124,7 +128,8 @@ struct Cursor {
 // The pairs of each expert, cut into runs, by one warp in the order of the pairs, so that
 // every CTA makes the same runs; the scan over the experts by all.
 template <int NT>
-__device__ void make_plan(Plan& pl, const Args& a) {
+__device__ void make_plan(Plan<NT>& pl, const Args& a) {
+    constexpr int kThreads = Shape<NT>::kThreads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int kPer = kMaxExperts / kThreads;  // experts of a thread, in turn
     for (int e = tid; e < a.E; e += kThreads) pl.count[e] = 0;
@@ -204,8 +209,9 @@ __device__ void make_plan(Plan& pl, const Args& a) {
 
 // acc += one stage's products, 8 NV columns of them.
 template <int NV, int NT, bool G32, int FMT>
-__device__ __forceinline__ void multiply(const uint8_t* w, const Side<NT>& s, float (&acc)[kTiles][NT][4],
-                                         int lane) {
+__device__ __forceinline__ void multiply(const uint8_t* w, const Side<NT>& s,
+                                         float (&acc)[Shape<NT>::kTiles][NT][4], int lane) {
+    constexpr int kTiles = Shape<NT>::kTiles;
     const int g = lane >> 2, t = lane & 3;
     float blk[kTiles][NV][4];
 #pragma unroll
@@ -285,16 +291,17 @@ __device__ __forceinline__ void multiply(const uint8_t* w, const Side<NT>& s, fl
 }
 
 template <int NT, bool G32, int FMT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
     w4_kernel(const __grid_constant__ CUtensorMap map_w, const Args a) {
-    extern __shared__ uint8_t raw[];
+    extern __shared__ __align__(512) uint8_t base[];
     using St = Side<NT>;
-    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 511) & ~uintptr_t{511});
+    constexpr int kWarps = Shape<NT>::kWarps, kRows = Shape<NT>::kRows, kTiles = Shape<NT>::kTiles;
+    constexpr int kBytesW = kRows * 64, kPart = Shape<NT>::kPart;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint8_t* ring_w = base + warp * kDepth * kBytesW;
     St* ring = reinterpret_cast<St*>(base + kWarps * kDepth * kBytesW) + warp * kDepth;
     uint8_t* rest = base + kWarps * kDepth * (kBytesW + sizeof(St));
-    Plan& pl = *reinterpret_cast<Plan*>(rest);
+    Plan<NT>& pl = *reinterpret_cast<Plan<NT>*>(rest);
     uint64_t* full = pl.full[warp];
     const int g = lane >> 2, t = lane & 3;
     if (lane == 0)
@@ -305,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const int KB = a.K / 128, NB = a.N / kRows;
     // this CTA's share of the row blocks, and the warps that share one: the fewest with
-    // which at least nine tenths of the warps' time is used, else the most
+    // which at least seven eighths of the warps' time is used, else the most
     const int items = pl.runs * NB;
     const int64_t grid = gridDim.x;
     const int begin = static_cast<int>(items * static_cast<int64_t>(blockIdx.x) / grid);
@@ -314,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int S = 1;
     while (S < kWarps && 2 * S <= KB) {
         const int teams = kWarps / S;
-        if (10 * most >= 9 * ((most + teams - 1) / teams * teams)) break;
+        if (8 * most >= 7 * ((most + teams - 1) / teams * teams)) break;
         S *= 2;
     }
     const int team = warp / S, of_team = warp - team * S, teams = kWarps / S;
@@ -406,16 +413,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int n = 0; n < NT; ++n) {
                 if (n * 8 >= at.rows) break;
 #pragma unroll
-                for (int m = 0; m < kTiles; m += 2) {
+                for (int m = 0; m < kTiles; m += kPart / 4) {
                     named_bar_sync(1 + team, S * 32);
                     if (of_team)
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) pl.parts[warp][i][lane] = acc[m + i / 4][n][i & 3];
+                        for (int i = 0; i < kPart; ++i) pl.parts[warp][i][lane] = acc[m + i / 4][n][i & 3];
                     named_bar_sync(1 + team, S * 32);
                     if (of_team == 0)
                         for (int o = 1; o < S; ++o)
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) acc[m + i / 4][n][i & 3] += pl.parts[warp + o][i][lane];
+                            for (int i = 0; i < kPart; ++i) acc[m + i / 4][n][i & 3] += pl.parts[warp + o][i][lane];
                 }
             }
         if (of_team || dead) continue;
@@ -448,8 +455,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int NT, bool G32, int FMT>
 cudaError_t launch(const CUtensorMap& map, Args a, int64_t items, cudaStream_t stream) {
     auto* k = &w4_kernel<NT, G32, FMT>;
-    constexpr size_t smem =
-        kWarps * kDepth * (kBytesW + sizeof(Side<NT>)) + sizeof(Plan) + 512;
+    constexpr int kThreads = Shape<NT>::kThreads;
+    constexpr size_t smem = Shape<NT>::kWarps * kDepth * (Shape<NT>::kRows * 64 + sizeof(Side<NT>)) +
+                            sizeof(Plan<NT>);
     static_assert(smem <= 227 * 1024, "shared memory");
     const int grid = persistent_grid(reinterpret_cast<const void*>(k), kThreads, smem, items);
     if (const cudaError_t e = upload_checks(stream)) return e;
@@ -458,7 +466,13 @@ cudaError_t launch(const CUtensorMap& map, Args a, int64_t items, cudaStream_t s
 }
 
 template <int NT>
-cudaError_t launch_form(const CUtensorMap& map, const Args& a, bool g32, int fmt, int64_t items, cudaStream_t stream) {
+cudaError_t launch_form(const W4Product& p, const Args& a, int64_t experts, cudaStream_t stream) {
+    constexpr int kRows = Shape<NT>::kRows;
+    CUtensorMap map;
+    if (!encode_u8_2d_swizzled(&map, p.w, p.K / 2, p.E * p.N, 64, kRows)) return cudaErrorInvalidValue;
+    const bool g32 = p.group == 32;
+    const int fmt = p.fmt;
+    const int64_t items = experts * (p.N / kRows);
     if (g32)
         return fmt == kFmtE4M3 ? launch<NT, true, kFmtE4M3>(map, a, items, stream)
                                : launch<NT, true, kFmtE5M2>(map, a, items, stream);
@@ -521,13 +535,8 @@ cudaError_t launch_w4_product(const W4Product& p, cudaStream_t stream) {
     a.E = p.E;
     a.share = p.each ? 1 : p.k;
     a.status = device_status_word();
-    CUtensorMap map;
-    if (!encode_u8_2d_swizzled(&map, p.w, p.K / 2, p.E * p.N, 64, kRows)) return cudaErrorInvalidValue;
-    const bool g32 = p.group == 32;
     const int64_t experts = p.ids ? (a.P < p.E ? a.P : p.E) : 1;  // at most this many have rows
-    const int64_t items = experts * (p.N / kRows);
-    return p.T <= 8 ? launch_form<1>(map, a, g32, p.fmt, items, stream)
-                    : launch_form<2>(map, a, g32, p.fmt, items, stream);
+    return a.P <= 8 * experts ? launch_form<1>(p, a, experts, stream) : launch_form<2>(p, a, experts, stream);
 }
 
 cudaError_t launch_w4_cast(const void* w, void* codes, void* sf, int64_t N, int64_t K, int group,
