@@ -26,22 +26,26 @@ constexpr unsigned kAll = 0xffffffffu;
 // A stable counting sort in one launch of one cluster: a warp counts the experts
 // of its run of pairs, the warps' counts are added up within the CTA, the CTAs'
 // read through distributed shared memory, and the warp then walks its run again,
-// 32 pairs at a time, the lanes of one expert in pair order (a match within the
-// warp), so that equal experts keep the order of their pairs and the result does
-// not depend on the launch.  A cluster of at most eight CTAs (the portable size)
-// replaces the second launch and the workspace that a grid of CTAs would need.
+// 32 pairs at a time, the lanes of one expert in pair order, so that equal experts
+// keep the order of their pairs and the result does not depend on the launch.  A cluster of at most eight CTAs (the portable size)
+// replaces the second launch and the workspace that a grid of CTAs would need; it
+// is bound by the latency of its steps, not by the few bytes it moves.  Each lane
+// asks for kBatch of its ids at once.
 constexpr int kOrderThreads = 1024;
 constexpr int kOrderWarps = kOrderThreads / 32;
 constexpr int kOrderMaxExperts = 1024;
+constexpr int kBatch = 8;
 
 struct OrderSmem {
-    int total[kOrderMaxExperts];     // pairs of each expert in this CTA
+    int total[kOrderMaxExperts];      // pairs of each expert in this CTA
     int start[kOrderMaxExperts + 1];  // first row of each expert
-    int below[kOrderMaxExperts];     // of them in the CTAs before this one
-    int all[kOrderMaxExperts];       // pairs of each expert in all CTAs
+    int below[kOrderMaxExperts];      // pairs of it in the CTAs before this one, then first place of this CTA's
+    int all[kOrderMaxExperts];        // pairs of each expert in all CTAs
     int warp_sum[kOrderWarps];
 };
 
+// CLUSTER: more than one CTA.
+template <bool CLUSTER>
 __global__ void __launch_bounds__(kOrderThreads, 1)
     order_kernel(const int32_t* __restrict__ ids, int32_t* __restrict__ slots,
                  int32_t* __restrict__ rows, int32_t* __restrict__ offsets, int P, int E, int align,
@@ -49,58 +53,71 @@ __global__ void __launch_bounds__(kOrderThreads, 1)
     extern __shared__ int counts[];  // [kOrderWarps][E]: a warp's pairs of each expert, then their places
     __shared__ OrderSmem sm;
     cg::cluster_group cluster = cg::this_cluster();
-    const int ctas = static_cast<int>(cluster.num_blocks());
-    const int rank = static_cast<int>(cluster.block_rank());
+    const int ctas = CLUSTER ? static_cast<int>(cluster.num_blocks()) : 1;
+    const int rank = CLUSTER ? static_cast<int>(cluster.block_rank()) : 0;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int bits = 32 - __clz(E - 1);  // of an expert's number
 
     // this warp's run of pairs, a whole number of 32s
     const int per_warp = ((P + ctas * kOrderWarps - 1) / (ctas * kOrderWarps) + 31) / 32 * 32;
     const int64_t lo = static_cast<int64_t>(rank * kOrderWarps + warp) * per_warp;
     const int64_t hi = lo + per_warp < P ? lo + per_warp : P;
+    const auto load = [&](int64_t p0, int (&id)[kBatch]) {
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int64_t p = p0 + b * 32 + lane;
+            id[b] = p < hi ? ld_ro(ids + p) : -1;
+            if (id[b] < 0 || id[b] >= E) id[b] = -1;
+        }
+    };
+    int id[kBatch];  // of the first batch, kept for the second walk
+    load(lo, id);
 
+    for (int i = threadIdx.x; i < kOrderWarps * E; i += kOrderThreads) counts[i] = 0;
+    __syncthreads();
     int* mine = counts + warp * E;
-    for (int e = lane; e < E; e += 32) mine[e] = 0;
-    __syncwarp();
-    for (int64_t p0 = lo; p0 < hi; p0 += 32) {
-        const int64_t p = p0 + lane;
-        const int id = p < hi ? ld_ro(ids + p) : -1;
-        const unsigned same = __match_any_sync(kAll, id);
-        if (id >= 0 && id < E && lane == __ffs(same) - 1) mine[id] += __popc(same);
-        __syncwarp();
+    for (int64_t p0 = lo; p0 < hi; p0 += 32 * kBatch) {
+        int next[kBatch];
+        if (p0 > lo) load(p0, next);
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            if (p0 + b * 32 >= hi) break;
+            const int e = p0 > lo ? next[b] : id[b];
+            if (e >= 0) atomicAdd(&mine[e], 1);
+        }
     }
     __syncthreads();
     // counts[w][e]: pairs of e in the warps before w
-    for (int e = threadIdx.x; e < E; e += kOrderThreads) {
-        int n = 0;
+    const int e = threadIdx.x;  // E <= kOrderThreads
+    int n = 0;
+    if (e < E) {
 #pragma unroll 8
         for (int w = 0; w < kOrderWarps; ++w) {
             const int c = counts[w * E + e];
             counts[w * E + e] = n;
             n += c;
         }
-        sm.total[e] = n;
     }
-    cluster.sync();
-    const int e = threadIdx.x;  // E <= kOrderThreads
-    int rounded = 0;
-    if (e < E) {
-        int below = 0, all = 0;
-        for (int c = 0; c < ctas; ++c) {
-            const int n = *cluster.map_shared_rank(&sm.total[e], c);
-            if (c < rank) below += n;
-            all += n;
-        }
-        sm.below[e] = below;
-        sm.all[e] = all;
-        rounded = (all + align - 1) / align * align;
+    int below = 0, all = n;
+    if constexpr (CLUSTER) {
+        if (e < E) sm.total[e] = n;
+        cluster.sync();
+        all = 0;
+        if (e < E)
+            for (int c = 0; c < ctas; ++c) {
+                const int m = *cluster.map_shared_rank(&sm.total[e], c);
+                if (c < rank) below += m;
+                all += m;
+            }
+        // the other CTAs have read this one's counts before it can leave
+        cluster.sync();
     }
-    // the other CTAs have read this one's counts before it can leave
-    cluster.sync();
+    const int rounded = (all + align - 1) / align * align;
     int scan = rounded;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int n = __shfl_up_sync(kAll, scan, o);
-        if (lane >= o) scan += n;
+        const int m = __shfl_up_sync(kAll, scan, o);
+        if (lane >= o) scan += m;
     }
     if (lane == 31) sm.warp_sum[warp] = scan;
     __syncthreads();
@@ -108,8 +125,8 @@ __global__ void __launch_bounds__(kOrderThreads, 1)
         int v = sm.warp_sum[lane];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int n = __shfl_up_sync(kAll, v, o);
-            if (lane >= o) v += n;
+            const int m = __shfl_up_sync(kAll, v, o);
+            if (lane >= o) v += m;
         }
         sm.warp_sum[lane] = v;
     }
@@ -117,29 +134,38 @@ __global__ void __launch_bounds__(kOrderThreads, 1)
     const int incl = scan + (warp ? sm.warp_sum[warp - 1] : 0);
     if (e < E) {
         sm.start[e] = incl - rounded;
+        sm.below[e] = incl - rounded + below;
+        sm.all[e] = all;
         if (e == E - 1) sm.start[E] = incl;
+        if (rank == 0) {
+            st_plain(offsets + e, incl - rounded);
+            if (e == E - 1) st_plain(offsets + E, incl);
+        }
     }
     __syncthreads();
-    if (rank == 0)
-        for (int i = threadIdx.x; i <= E; i += kOrderThreads) st_plain(offsets + i, sm.start[i]);
 
-    for (int64_t p0 = lo; p0 < hi; p0 += 32) {
-        const int64_t p = p0 + lane;
-        const int id = p < hi ? ld_ro(ids + p) : -1;
-        const bool live = id >= 0 && id < E;
-        const unsigned same = __match_any_sync(kAll, id);
-        int at = 0;
-        if (live) at = mine[id];
-        __syncwarp();
-        if (live && lane == __ffs(same) - 1) mine[id] = at + __popc(same);
-        __syncwarp();
-        if (p < hi) {
-            int slot = -1;
-            if (live) {
-                slot = sm.start[id] + sm.below[id] + at + __popc(same & ((1u << lane) - 1u));
-                st_plain(rows + slot, static_cast<int32_t>(p));
+    for (int64_t p0 = lo; p0 < hi; p0 += 32 * kBatch) {
+        int next[kBatch];
+        if (p0 > lo) load(p0, next);
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int64_t p = p0 + b * 32 + lane;
+            if (p0 + b * 32 >= hi) break;
+            const int x = p0 > lo ? next[b] : id[b];
+            const unsigned same = lanes_of_value(x, bits, __ballot_sync(kAll, x >= 0));
+            int at = 0;
+            if (x >= 0) at = mine[x];
+            __syncwarp();
+            if (x >= 0 && lane == __ffs(same) - 1) mine[x] = at + __popc(same);
+            __syncwarp();
+            if (p < hi) {
+                int slot = -1;
+                if (x >= 0) {
+                    slot = sm.below[x] + at + __popc(same & ((1u << lane) - 1u));
+                    st_plain(rows + slot, static_cast<int32_t>(p));
+                }
+                st_plain(slots + p, slot);
             }
-            st_plain(slots + p, slot);
         }
     }
     // rows without a pair: behind each expert's and behind the last one's
@@ -199,7 +225,7 @@ __device__ __forceinline__ void clear_padding(const int32_t* rows, const int32_t
 }
 
 template <int FORM, int FMT>
-__global__ void __launch_bounds__(kGatherThreads, 4) gather_kernel(const GatherArgs a) {
+__global__ void __launch_bounds__(kGatherThreads, 5) gather_kernel(const GatherArgs a) {
     const int lane = threadIdx.x & 31;
     const int sub = lane >> 3, j8 = lane & 7;
     const int64_t step = static_cast<int64_t>(gridDim.x) * kGatherWarps;
@@ -212,27 +238,46 @@ __global__ void __launch_bounds__(kGatherThreads, 4) gather_kernel(const GatherA
     const int64_t dt = step * 4 / a.G;
     const int dg = static_cast<int>(step * 4 - dt * a.G);
 
+    // a unit's values, and the slots of its tokens: lane j of a group's eight holds those of
+    // experts j, j + 8, ...
     uint4 q[kVecs];
     float sf = 0.0f;
-    const auto load = [&](int64_t u) {
+    int slot = -1;
+    const auto slot_of = [&](int64_t token, int j) {
+        const int s = j < a.k ? ld_ro(a.slots + token * a.k + j) : -1;
+        return static_cast<unsigned>(s) < static_cast<unsigned>(a.R) ? s : -1;
+    };
+    const auto load = [&](int64_t u, int64_t token) {
+        slot = -1;
         if (u < units && u * 4 + sub < a.n_groups) {
 #pragma unroll
             for (int v = 0; v < kVecs; ++v) q[v] = ld_stream(a.x + (u * 32 + lane) * kVecs + v);
             if constexpr (FORM == kGatherCodes) sf = ld_ro(a.x_sf + u * 4 + sub);
+            slot = slot_of(token, j8);
         }
     };
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) q[v] = make_uint4(0, 0, 0, 0);
-    load(first);
+    load(first, t);
     for (int64_t u = first; u < units; u += step) {
         const bool live = u * 4 + sub < a.n_groups;
-        uint4 o[FORM == kGatherBf16 ? 2 : 1];
+        const int64_t token = t;
+        const int group = g;
+        t += dt;
+        g += dg;
+        if (g >= a.G) {
+            g -= a.G;
+            ++t;
+        }
+        int slots8 = slot;
+        constexpr int kOut = FORM == kGatherBf16 ? 2 : 1;
+        uint4 o[kOut];
         float scale = 0.0f;
         if constexpr (FORM == kGatherCast) {
             float v[16];
             unpack8(q[0], v);
             unpack8(q[1], v + 8);
-            load(u + step);
+            load(u + step, t);
             float m = fmaxf(absmax8(v), absmax8(v + 8));
             m = fmaxf(m, __shfl_xor_sync(kAll, m, 1));
             m = fmaxf(m, __shfl_xor_sync(kAll, m, 2));
@@ -245,32 +290,28 @@ __global__ void __launch_bounds__(kGatherThreads, 4) gather_kernel(const GatherA
 #pragma unroll
             for (int v = 0; v < kVecs; ++v) o[v] = q[v];
             scale = sf;
-            load(u + step);
+            load(u + step, t);
         }
-        if (live) {
-            constexpr int kOut = FORM == kGatherBf16 ? 2 : 1;
-            const int32_t* sl = a.slots + t * a.k;
-            for (int j = 0; j < a.k; ++j) {
-                const int s = ld_ro(sl + j);
-                if (static_cast<unsigned>(s) >= static_cast<unsigned>(a.R)) continue;
-                uint4* to = a.out + ((static_cast<int64_t>(s) * a.G + g) * 8 + j8) * kOut;
+        for (int j0 = 0; j0 < a.k; j0 += 8) {
+            if (j0) slots8 = live ? slot_of(token, j0 + j8) : -1;
+            const int most = a.k - j0 < 8 ? a.k - j0 : 8;
 #pragma unroll
-                for (int v = 0; v < kOut; ++v) st_stream(to + v, o[v]);
-                if constexpr (FORM != kGatherBf16)
-                    if (j8 == 0) st_plain(a.out_sf + static_cast<int64_t>(s) * a.G + g, scale);
-            }
-            if (a.row_weights && g == 0)
-                for (int j = j8; j < a.k; j += 8) {
-                    const int s = ld_ro(sl + j);
-                    if (static_cast<unsigned>(s) < static_cast<unsigned>(a.R))
-                        st_plain(a.row_weights + s, ld_ro(a.weights + t * a.k + j));
+            for (int j = 0; j < 8; ++j) {
+                if (j >= most) break;
+                const int s = __shfl_sync(kAll, slots8, (lane & 24) | j);
+                if (s < 0) continue;
+                uint4* to = a.out + ((static_cast<int64_t>(s) * a.G + group) * 8 + j8) * kOut;
+                if constexpr (kOut == 2) {
+                    // whole sectors: two stores of 16 bytes took 167 us where this takes 119 (8192 x 4096, 8 each)
+                    const uint32_t w[8] = {o[0].x, o[0].y, o[0].z, o[0].w, o[1].x, o[1].y, o[1].z, o[1].w};
+                    st_sector(to, w);
+                } else {
+                    st_stream(to, o[0]);
+                    if (j8 == j) st_plain(a.out_sf + static_cast<int64_t>(s) * a.G + group, scale);
                 }
-        }
-        t += dt;
-        g += dg;
-        if (g >= a.G) {
-            g -= a.G;
-            ++t;
+            }
+            if (a.row_weights && group == 0 && slots8 >= 0)
+                st_plain(a.row_weights + slots8, ld_ro(a.weights + token * a.k + j0 + j8));
         }
     }
     float zero_scale = 0.0f, inv;
@@ -487,7 +528,8 @@ cudaError_t launch_expert_order(const int32_t* ids, int32_t* slots, int32_t* row
     int ctas = 1;
     while (ctas < 8 && ctas * per_cta < P) ctas *= 2;
     const size_t smem = static_cast<size_t>(kOrderWarps) * E * sizeof(int);
-    persistent_grid(reinterpret_cast<const void*>(&order_kernel), kOrderThreads, smem, 1);  // allows the shared memory
+    auto* k = ctas > 1 ? &order_kernel<true> : &order_kernel<false>;
+    persistent_grid(reinterpret_cast<const void*>(k), kOrderThreads, smem, 1);  // allows the shared memory
     if (const cudaError_t e = upload_checks(stream)) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
@@ -499,9 +541,9 @@ cudaError_t launch_expert_order(const int32_t* ids, int32_t* slots, int32_t* row
     attr[0].val.clusterDim.x = ctas;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, order_kernel, ids, slots, rows, offsets,
-                                             static_cast<int>(P), E, align, static_cast<int>(R));
+    cfg.numAttrs = ctas > 1 ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k, ids, slots, rows, offsets, static_cast<int>(P), E,
+                                             align, static_cast<int>(R));
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -132,6 +132,7 @@ __device__ void make_plan(Plan<NT>& pl, const Args& a) {
     constexpr int kThreads = Shape<NT>::kThreads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int kPer = kMaxExperts / kThreads;  // experts of a thread, in turn
+    const int bits = 32 - __clz(a.E - 1);         // of an expert's number
     for (int e = tid; e < a.E; e += kThreads) pl.count[e] = 0;
     for (int p = tid; p < a.P; p += kThreads) {
         const int e = a.ids ? ld_ro(a.ids + p) : 0;
@@ -142,7 +143,7 @@ __device__ void make_plan(Plan<NT>& pl, const Args& a) {
         for (int p0 = 0; p0 < a.P; p0 += 32) {
             const int p = p0 + lane;
             const int e = p < a.P ? pl.expert[p] : -1;
-            const unsigned same = __match_any_sync(0xffffffffu, e);
+            const unsigned same = lanes_of_value(e, bits, __ballot_sync(0xffffffffu, e >= 0));
             if (e >= 0 && lane == __ffs(same) - 1) pl.count[e] += __popc(same);
             __syncwarp();
         }
@@ -193,7 +194,7 @@ __device__ void make_plan(Plan<NT>& pl, const Args& a) {
             const int p = p0 + lane;
             const int e = p < a.P ? pl.expert[p] : -1;
             const bool live = e >= 0;
-            const unsigned same = __match_any_sync(0xffffffffu, e);
+            const unsigned same = lanes_of_value(e, bits, __ballot_sync(0xffffffffu, live));
             const int at = live ? pl.first[e] : 0;
             __syncwarp();
             if (live) {
