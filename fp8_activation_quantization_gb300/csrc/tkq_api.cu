@@ -138,6 +138,12 @@ bool encode_u8_2d_swizzled(CUtensorMap* map, const void* base, int64_t cols, int
                      box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+bool encode_bf16_2d_swizzled(CUtensorMap* map, const void* base, int64_t cols, int64_t rows,
+                             uint32_t box_rows) {
+    return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, cols, rows, 64, box_rows,
+                     CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 
 unsigned int* device_status_word() {
     int dev = 0;
