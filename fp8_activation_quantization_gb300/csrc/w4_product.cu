@@ -81,6 +81,7 @@ struct Args {
     const int32_t* ids;      // [P] or null
     uint16_t* out;           // [P, N]
     int P, N, K, E, share;   // x's row of pair p is p / share
+    int ctas;                // the device's own grid, which the order of sums follows
     unsigned int* status;
 };
 
@@ -318,7 +319,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
     const int64_t grid = gridDim.x;
     const int begin = static_cast<int>(items * static_cast<int64_t>(blockIdx.x) / grid);
     const int end = static_cast<int>(items * (static_cast<int64_t>(blockIdx.x) + 1) / grid);
-    const int most = static_cast<int>((items + grid - 1) / grid);
+    const int most = (items + a.ctas - 1) / a.ctas;
     int S = 1;
     while (S < kWarps && 2 * S <= KB) {
         const int teams = kWarps / S;
@@ -461,6 +462,7 @@ cudaError_t launch(const CUtensorMap& map, Args a, int64_t items, cudaStream_t s
                             sizeof(Plan<NT>);
     static_assert(smem <= 227 * 1024, "shared memory");
     const int grid = persistent_grid(reinterpret_cast<const void*>(k), kThreads, smem, items);
+    a.ctas = static_cast<int>(items < device_sms() ? items : device_sms());
     if (const cudaError_t e = upload_checks(stream)) return e;
     k<<<grid, kThreads, smem, stream>>>(map, a);
     return cudaGetLastError();
