@@ -523,8 +523,9 @@ cudaError_t launch_rows(K kernel, int threads, int64_t blocks, const A& a, cudaS
 
 cudaError_t launch_expert_order(const int32_t* ids, int32_t* slots, int32_t* rows, int32_t* offsets,
                                 int64_t P, int E, int align, int64_t R, cudaStream_t stream) {
-    // CTAs of the cluster: a warp walks at least four times 32 pairs
-    const int64_t per_cta = kOrderWarps * 128;
+    // CTAs of the cluster: as many as leave each warp 32 pairs.  (256 experts, four times as
+    // many pairs a CTA: 9.9 instead of 7.9 us for 4096 pairs, 10.6 instead of 7.7 for 8192.)
+    const int64_t per_cta = kOrderWarps * 32;
     int ctas = 1;
     while (ctas < 8 && ctas * per_cta < P) ctas *= 2;
     const size_t smem = static_cast<size_t>(kOrderWarps) * E * sizeof(int);
