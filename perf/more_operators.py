@@ -63,12 +63,10 @@ def listed():
 
 def draw(rng):
     def size(lo, hi):
-        n = max(lo, min(hi, round(math.exp(rng.uniform(math.log(lo), math.log(hi + 0.5))))))
-        return n + 1 if n == 3072 else n
+        return max(lo, min(hi, round(math.exp(rng.uniform(math.log(lo), math.log(hi + 0.5))))))
 
     def width(most):
-        n = size(1, most)
-        return GROUP * (n + 1 if n in (12, 24) else n)
+        return GROUP * size(1, most)
 
     op = rng.choice(["sort", "back", "back_bwd", "product", "weight_grad", "w4"])
     if op in ("sort", "back", "back_bwd"):
