@@ -610,7 +610,9 @@ tkq_status tkq_expert_weight_grad(const void* dy_t, const float* dy_sf, const vo
  *   ids : int32 [T, k];  out : bf16 [T * k, N]
  * T >= 0, 0 < k <= 32, T * k <= 1024 (a larger batch is tkq_expert_product's);
  * 0 < E <= 1024; N, K > 0, multiples of 128, at most 2^20, else TKQ_ERR_SHAPE;
- * w_group: TKQ_ERR_GROUP.  Alignment: x, w, out 16 bytes, else 4.
+ * w_group: TKQ_ERR_GROUP.  Alignment: x, w, out 16 bytes, else 4.  The order of the
+ * sums follows the call's sizes, the experts' numbers of rows and the device's SMs:
+ * results repeat bit for bit on one kind of GPU.
  */
 tkq_status tkq_w4_product(const void* x, const float* x_sf, const void* w, const void* w_sf,
                           const int32_t* ids, void* out, int64_t T, int k, int64_t rows, int64_t E,
