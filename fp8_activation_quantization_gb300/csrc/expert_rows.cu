@@ -181,9 +181,10 @@ __global__ void __launch_bounds__(kOrderThreads, 1)
 // rows to their experts
 // ---------------------------------------------------------------------------
 // The input is one flat sequence of 128-channel groups, as for the plain cast: eight
-// lanes take a group, a lane 16 consecutive values, cast once and stored k times.  The
-// writes bound it: 8192 tokens of 4096 channels cast to 8 rows each in 69 us, 5.0 TB/s,
-// where a fill of memory runs at 4.0.
+// lanes take a group, a lane 16 consecutive values, cast once and stored k times.  Memory
+// bounds it, five bytes in six written: 8192 tokens of 4096 channels cast to 8 rows each
+// in 68 us, 5.1 TB/s (61 us without the rows that pad 64 experts' to groups of 128).  Bulk
+// copies in and, for each row, out of shared memory took 74.
 // Form: what a row is and becomes.
 enum GatherForm { kGatherBf16, kGatherCast, kGatherCodes };
 constexpr int kGatherThreads = 256;
@@ -203,25 +204,36 @@ struct GatherArgs {
     int G, k, E, R;
 };
 
-// Zeros in the rows that have no pair, up to the last expert's last row (one warp per
-// 32 rows); a cast row of zeros has the smallest scale.
+// Zeros in the rows that have no pair: those that pad an expert's, behind its last one; a
+// cast row of zeros has the smallest scale.  kPadParts warps take an expert, each every
+// kPadParts-th of its rows, looking at 32 rows at a time from the end on until none of them
+// is padding.  (All rows looked at in turn, and cleared by the warp that met them, took 12
+// of 73 us for 8192 tokens cast to 8 rows each of 64 experts.)
+constexpr int kPadParts = 8;
 template <int BYTES>
 __device__ __forceinline__ void clear_padding(const int32_t* rows, const int32_t* offsets, int E, int R,
                                               int G, uint4* out, float* out_sf, float zero_scale,
                                               float* row_weights, int64_t warp, int64_t warps) {
     const int lane = threadIdx.x & 31;
-    int end = ld_ro(offsets + E);
-    if (end > R) end = R;
     const int vecs = G * 128 * BYTES / 16;
-    for (int64_t r0 = warp * 32; r0 < end; r0 += warps * 32) {
-        const int64_t r = r0 + lane;
-        const bool pad = r < end && ld_ro(rows + r) < 0;
-        if (pad && row_weights) st_plain(row_weights + r, 0.0f);
-        for (unsigned m = __ballot_sync(kAll, pad); m; m &= m - 1) {
-            const int64_t row = r0 + __ffs(m) - 1;
-            for (int v = lane; v < vecs; v += 32) st_stream(out + row * vecs + v, make_uint4(0, 0, 0, 0));
-            if (out_sf)
-                for (int g = lane; g < G; g += 32) st_plain(out_sf + row * G + g, zero_scale);
+    for (int64_t task = warp; task < static_cast<int64_t>(E) * kPadParts; task += warps) {
+        const int e = static_cast<int>(task / kPadParts), part = static_cast<int>(task % kPadParts);
+        int begin = ld_ro(offsets + e), end = ld_ro(offsets + e + 1);
+        begin = begin < 0 ? 0 : begin;
+        end = end > R ? R : end;
+        for (int64_t r0 = static_cast<int64_t>(end) - 32; r0 > static_cast<int64_t>(begin) - 32; r0 -= 32) {
+            const int64_t r = r0 + lane;
+            const bool pad = r >= begin && ld_ro(rows + r) < 0;
+            const unsigned all = __ballot_sync(kAll, pad);
+            if (!all) break;
+            const bool mine = pad && (r & (kPadParts - 1)) == part;
+            if (mine && row_weights) st_plain(row_weights + r, 0.0f);
+            for (unsigned m = __ballot_sync(kAll, mine); m; m &= m - 1) {
+                const int64_t row = r0 + __ffs(m) - 1;
+                for (int v = lane; v < vecs; v += 32) st_stream(out + row * vecs + v, make_uint4(0, 0, 0, 0));
+                if (out_sf)
+                    for (int g = lane; g < G; g += 32) st_plain(out_sf + row * G + g, zero_scale);
+            }
         }
     }
 }
@@ -261,6 +273,11 @@ __global__ void __launch_bounds__(kGatherThreads, 5) gather_kernel(const GatherA
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) q[v] = make_uint4(0, 0, 0, 0);
     load(first, t);
+    float zero_scale = 0.0f, inv;
+    if constexpr (FORM == kGatherCast) group_scale<FMT>(0.0f, zero_scale, inv);
+    clear_padding<FORM == kGatherBf16 ? 2 : 1>(a.rows, a.offsets, a.E, a.R, a.G, a.out,
+                                               FORM == kGatherBf16 ? nullptr : a.out_sf, zero_scale,
+                                               a.row_weights, first, step);
     for (int64_t u = first; u < units; u += step) {
         const bool live = u * 4 + sub < a.n_groups;
         const int64_t token = t;
@@ -316,11 +333,6 @@ __global__ void __launch_bounds__(kGatherThreads, 5) gather_kernel(const GatherA
                 st_plain(a.row_weights + slots8, ld_ro(a.weights + token * a.k + j0 + j8));
         }
     }
-    float zero_scale = 0.0f, inv;
-    if constexpr (FORM == kGatherCast) group_scale<FMT>(0.0f, zero_scale, inv);
-    clear_padding<FORM == kGatherBf16 ? 2 : 1>(a.rows, a.offsets, a.E, a.R, a.G, a.out,
-                                               FORM == kGatherBf16 ? nullptr : a.out_sf, zero_scale,
-                                               a.row_weights, first, step);
 }
 
 // ---------------------------------------------------------------------------
@@ -409,7 +421,9 @@ __global__ void __launch_bounds__(kReduceThreads) reduce_kernel(const ReduceArgs
 // token's rows is w times dout, and dw of each the sum over the channels of dout times
 // the row.  A lane keeps kGradDepth of those sums while it walks its channels; they are
 // added up within the warp and, in the order of the warps, within the CTA.  8192 tokens
-// of 8 rows of 4096 channels: 202 us, 5.6 TB/s, bound by memory (half of it writes).
+// of 8 rows of 4096 channels: 186 us, 6.1 TB/s, bound by memory (half of it writes); with
+// bf16 rows 122 registers, four CTAs an SM, hold more loads (at most 56: 192 us), with a
+// cast 80, six CTAs (153: 187 us, 80: 149).
 // FMT: an FP8 format, or 2 for bf16 rows.
 constexpr int kGradThreads = 128;
 constexpr int kGradDepth = 8;
@@ -429,7 +443,7 @@ struct GradArgs {
 };
 
 template <int FMT>
-__global__ void __launch_bounds__(kGradThreads) reduce_backward_kernel(const GradArgs a) {
+__global__ void __launch_bounds__(kGradThreads, FMT == 2 ? 1 : 6) reduce_backward_kernel(const GradArgs a) {
     __shared__ float part[kGradThreads / 32][kGradDepth];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int half = threadIdx.x >> 4, l16 = threadIdx.x & 15;
@@ -569,7 +583,7 @@ cudaError_t launch_expert_gather(const ExpertGather& p, cudaStream_t stream) {
     a.R = static_cast<int>(p.R);
     a.n_groups = p.T * a.G;
     const int64_t blocks = ((a.n_groups + 3) / 4 + kGatherWarps - 1) / kGatherWarps +
-                           (p.R / 32 + kGatherWarps - 1) / kGatherWarps;
+                           (p.E * kPadParts + kGatherWarps - 1) / kGatherWarps;
     if (p.form == 0) return launch_rows(&gather_kernel<kGatherBf16, kFmtE4M3>, kGatherThreads, blocks, a, stream);
     if (p.form == 2) return launch_rows(&gather_kernel<kGatherCodes, kFmtE4M3>, kGatherThreads, blocks, a, stream);
     return p.fmt == kFmtE4M3
@@ -615,7 +629,7 @@ cudaError_t launch_expert_reduce_backward(const ExpertReduceGrad& p, cudaStream_
     a.k = p.k;
     a.E = p.E;
     a.R = static_cast<int>(p.R);
-    const int64_t pads = p.R / 32 / (kGradThreads / 32) + 1;
+    const int64_t pads = p.E * kPadParts / (kGradThreads / 32);
     const int64_t blocks = p.T > pads ? p.T : pads;
     if (p.fmt == kFmtE4M3)
         return launch_rows(&reduce_backward_kernel<kFmtE4M3>, kGradThreads, blocks, a, stream);

@@ -509,9 +509,9 @@ tkq_status tkq_expert_order(const int32_t* ids, int32_t* slots, int32_t* rows, i
  *                         the rows of tkq_per_token_cast(x) in fmt, bit for bit
  *   form TKQ_ROWS_CODES : x codes [T, C], x_sf fp32 [T, C/128] -> copies of both
  * With weights (fp32 [T, k]) row_weights[r] (fp32 [R]) is the weight of the row's
- * pair; both or neither are given.  Rows without a pair below offsets[E] are zeros
- * (a cast one has the smallest scale, a copied one the scale 0), their weight 0;
- * rows from offsets[E] on are left as they were.
+ * pair; both or neither are given.  Rows that pad an expert's, behind its last pair,
+ * are zeros (a cast one has the smallest scale, a copied one the scale 0), their
+ * weight 0; rows from offsets[E] on are left as they were.
  *   slots, rows, offsets : as tkq_expert_order gives them; a slot outside [0, R) is
  *   an empty one.  The gradient of this call is tkq_expert_reduce without weights.
  * T >= 0, T * k <= 2^30; C > 0, C % 128 == 0, C <= 2^20; k, E and R as above.
@@ -546,7 +546,7 @@ tkq_status tkq_expert_reduce(const void* y, const int32_t* slots, const float* w
  *   dweights[t, j]  = sum_c dout[t, c] * y[slots[t, j], c]   (binary32, fixed order),
  *                     0 for an empty slot
  * dy is bf16 [R, C] (form TKQ_ROWS_BF16, dy_sf NULL), or its per-token cast in fmt
- * (TKQ_ROWS_CAST, exact quotient).  Rows without a pair are as in
+ * (TKQ_ROWS_CAST, exact quotient).  Rows that pad an expert's are as in
  * tkq_expert_gather.
  *   dout : bf16 [T, C];  y : bf16 [R, C];  weights, dweights : fp32 [T, k]
  */
