@@ -1174,18 +1174,19 @@ def _check_order(order, dev, T=None):
         slots, rows, offsets = order
     except (TypeError, ValueError):
         raise TypeError("order must be an ExpertOrder (slots, rows, offsets)") from None
-    i32 = (torch.int32,)
-    if not (isinstance(slots, torch.Tensor) and slots.dim() == 2 and isinstance(rows, torch.Tensor)
-            and rows.dim() == 1 and isinstance(offsets, torch.Tensor) and offsets.dim() == 1
-            and offsets.numel() >= 2):
-        raise TypeError("order must be an ExpertOrder of slots [T, k], rows [R] and offsets [E + 1]")
-    if T is None:
-        T = slots.shape[0]
-    k, R, E = slots.shape[1], rows.shape[0], offsets.shape[0] - 1
-    _check_like(slots, "order.slots", (T, k), i32, dev)
-    _check_like(rows, "order.rows", (R,), i32, dev)
-    _check_like(offsets, "order.offsets", (E + 1,), i32, dev)
-    return T, k, R, E
+    i32 = torch.int32
+    for t, dim in ((slots, 2), (rows, 1), (offsets, 1)):
+        if not (isinstance(t, torch.Tensor) and t.dtype is i32 and t.dim() == dim and t.device == dev
+                and t.is_contiguous()):
+            raise TypeError("order must be an ExpertOrder of contiguous int32 tensors slots [T, k], rows [R] "
+                            "and offsets [E + 1] on the inputs' device")
+    tokens, k = slots.shape
+    E = offsets.numel() - 1
+    if E < 1:
+        raise TypeError("order.offsets must have E + 1 >= 2 elements")
+    if T is not None and tokens != T:
+        raise ValueError(f"order.slots must have shape [{T}, k]")
+    return tokens, k, rows.numel(), E
 
 
 def _codes_fmt(x, name):
