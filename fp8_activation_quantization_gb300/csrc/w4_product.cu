@@ -14,18 +14,18 @@
 // the eight columns, so the weights go from memory to the tensor core once however many
 // rows there are.  (tcgen05 would want 128 of either, and its operands in shared memory
 // in 8 bits: the weights would have to be widened and stored there first.)
-// A warp takes 32 or 64 rows of a matrix, 128 channels at a time, from a ring of its own
-// in shared memory: one TMA box of rows of 64 bytes and a bulk copy for each row of x.
+// A warp takes 32 or 64 rows of a matrix, 256 channels at a time, from a ring of its own
+// in shared memory: one TMA box of rows of 128 bytes and a bulk copy for each row of x.
 // (Copies of 16 bytes a lane took 134 us for 48 tokens, 8 of 64 matrices of 4096 x 2048,
 // 70 of them without any arithmetic.)  A CTA takes an equal share of all row blocks, one
-// after another; S of its warps share those of a block, each taking every S-th 128
+// after another; S of its warps share those of a block, each taking every S-th 256
 // channels, where otherwise some of the warps would have none left at the end.  No warp
 // waits for another but at the end of shared rows.
-// Measured: those 48 tokens 98 us (2.9 TB/s), one token's 8 matrices of 4096 x 4096 23 us
-// (3.1 TB/s).  Copies alone take 75 and 18: what is left is widening the weights, 7
-// operations for 8, and the latency of a warp's steps (issue slots 57 % in use).  FP8
-// MMAs (m16n8k32) would take codes of x as they are, but are slower here than binary16
-// ones: 190 us where those took 145.
+// Measured: those 48 tokens 85 us (3.4 TB/s), one token's 8 matrices of 4096 x 4096 22 us
+// (3.2 TB/s); 128 channels at a time, in twice as many stages, 98 and 23.  What is left is
+// widening the weights, 7 operations for 8, and the latency of a warp's steps.  FP8 MMAs
+// (m16n8k32) would take codes of x as they are, but are slower here than binary16 ones:
+// 190 us where those took 145.
 #include <cuda_runtime.h>
 
 #include "tkq_async.cuh"
@@ -45,16 +45,17 @@ struct Shape {
 };
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxPairs = 1024;
-constexpr int kDepth = 4;        // stages of a warp's ring: what fits 227 KB with 16 rows of x
-constexpr int kPitch = 144;      // bytes from row to row of x: four rows' equal pieces lie in different banks
+constexpr int kDepth = 2;        // stages of a warp's ring: what fits 227 KB
+constexpr int kPitch = 288;      // bytes from row to row of x: four rows' equal pieces lie in different banks
 
-// One stage of a warp's ring: 128 channels of 32 or 64 rows of weights (64-byte swizzle,
-// aligned to its 512 bytes) and, apart from them, of 8 NT rows of x, and both scales.
+// One stage of a warp's ring: two blocks of 128 channels of 32 or 64 rows of weights
+// (128-byte swizzle, aligned to its 1024 bytes) and, apart from them, of 8 NT rows of x,
+// and both scales.
 template <int NT>
 struct alignas(16) Side {
     uint8_t x[8 * NT * kPitch];
-    uint32_t ws[Shape<NT>::kRows];
-    float xs[8 * NT];
+    uint32_t ws[2][Shape<NT>::kRows];
+    float xs[2][8 * NT];
 };
 
 // What a CTA knows of the rows: the pairs of each expert in turn, cut into runs of at
@@ -125,7 +126,7 @@ __device__ __forceinline__ void decode_ue8m0(uint32_t v, float (&s)[4]) {
     s[3] = bf16_hi(hi);
 }
 
-// A position in a warp's work: run of pairs, 32 rows of its matrix, block of channels.
+// A position in a warp's work: run of pairs, rows of its matrix, pair of blocks.
 struct Cursor {
     int run, block_row, kb;
     int expert, first, rows;
@@ -214,10 +215,10 @@ __device__ void make_plan(Plan<NT>& pl, const Args& a) {
     __syncthreads();
 }
 
-// acc += one stage's products, 8 NV columns of them.
+// acc += the products of a stage's block b, 8 NV columns of them.
 template <int NV, int NT, bool G32, int FMT>
 __device__ __forceinline__ void multiply(const uint8_t* w, const Side<NT>& s,
-                                         float (&acc)[Shape<NT>::kTiles][NT][4], int lane) {
+                                         float (&acc)[Shape<NT>::kTiles][NT][4], int b, int lane) {
     constexpr int kTiles = Shape<NT>::kTiles;
     const int g = lane >> 2, t = lane & 3;
     float blk[kTiles][NV][4];
@@ -231,27 +232,27 @@ __device__ __forceinline__ void multiply(const uint8_t* w, const Side<NT>& s,
 #pragma unroll
     for (int q = 0; q < 2 * kTiles; ++q) {
         if constexpr (G32)
-            decode_ue8m0(s.ws[q * 8 + g], ws[q]);
+            decode_ue8m0(s.ws[b][q * 8 + g], ws[q]);
         else
-            ws[q][0] = __uint_as_float(s.ws[q * 8 + g]);
+            ws[q][0] = __uint_as_float(s.ws[b][q * 8 + g]);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        uint32_t b[NV][4];
+        uint32_t xf[NV][4];
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
-            const uint2 xv = *reinterpret_cast<const uint2*>(s.x + (n * 8 + g) * kPitch + i * 32 + t * 8);
-            b[n][0] = fp8x2_to_f16x2<FMT>(xv.x & 0xFFFFu);
-            b[n][1] = fp8x2_to_f16x2<FMT>(xv.x >> 16);
-            b[n][2] = fp8x2_to_f16x2<FMT>(xv.y & 0xFFFFu);
-            b[n][3] = fp8x2_to_f16x2<FMT>(xv.y >> 16);
+            const uint2 xv = *reinterpret_cast<const uint2*>(s.x + (n * 8 + g) * kPitch + b * 128 + i * 32 + t * 8);
+            xf[n][0] = fp8x2_to_f16x2<FMT>(xv.x & 0xFFFFu);
+            xf[n][1] = fp8x2_to_f16x2<FMT>(xv.x >> 16);
+            xf[n][2] = fp8x2_to_f16x2<FMT>(xv.y & 0xFFFFu);
+            xf[n][3] = fp8x2_to_f16x2<FMT>(xv.y >> 16);
         }
 #pragma unroll
         for (int m2 = 0; m2 < kTiles / 2; ++m2) {
             uint32_t v[4];
             asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                          : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                         : "r"(smem_u32(w + (m2 * 32 + lane) * 64 + ((i ^ ((lane >> 1) & 3)) << 4))));
+                         : "r"(smem_u32(w + (m2 * 32 + lane) * 128 + (((4 * b + i) ^ (lane & 7)) << 4))));
             uint32_t h[4][4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) decode_e2m1(v[q], h[q]);
@@ -268,15 +269,15 @@ __device__ __forceinline__ void multiply(const uint8_t* w, const Side<NT>& s,
                 for (int n = 0; n < NV; ++n) {
                     if constexpr (G32) {
                         float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                        mma_16816(p, lo[0], hi[0], lo[1], hi[1], b[n][0], b[n][1]);
-                        mma_16816(p, lo[2], hi[2], lo[3], hi[3], b[n][2], b[n][3]);
+                        mma_16816(p, lo[0], hi[0], lo[1], hi[1], xf[n][0], xf[n][1]);
+                        mma_16816(p, lo[2], hi[2], lo[3], hi[3], xf[n][2], xf[n][3]);
                         blk[m][n][0] = fmaf(p[0], s0, blk[m][n][0]);
                         blk[m][n][1] = fmaf(p[1], s0, blk[m][n][1]);
                         blk[m][n][2] = fmaf(p[2], s1, blk[m][n][2]);
                         blk[m][n][3] = fmaf(p[3], s1, blk[m][n][3]);
                     } else {
-                        mma_16816(blk[m][n], lo[0], hi[0], lo[1], hi[1], b[n][0], b[n][1]);
-                        mma_16816(blk[m][n], lo[2], hi[2], lo[3], hi[3], b[n][2], b[n][3]);
+                        mma_16816(blk[m][n], lo[0], hi[0], lo[1], hi[1], xf[n][0], xf[n][1]);
+                        mma_16816(blk[m][n], lo[2], hi[2], lo[3], hi[3], xf[n][2], xf[n][3]);
                     }
                 }
             }
@@ -284,7 +285,7 @@ __device__ __forceinline__ void multiply(const uint8_t* w, const Side<NT>& s,
     }
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
-        const float2 xs = *reinterpret_cast<const float2*>(&s.xs[n * 8 + 2 * t]);
+        const float2 xs = *reinterpret_cast<const float2*>(&s.xs[b][n * 8 + 2 * t]);
 #pragma unroll
         for (int m = 0; m < kTiles; ++m) {
             const float s0 = G32 ? 1.0f : ws[2 * m][0];
@@ -300,10 +301,10 @@ __device__ __forceinline__ void multiply(const uint8_t* w, const Side<NT>& s,
 template <int NT, bool G32, int FMT>
 __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
     w4_kernel(const __grid_constant__ CUtensorMap map_w, const Args a) {
-    extern __shared__ __align__(512) uint8_t base[];
+    extern __shared__ __align__(1024) uint8_t base[];
     using St = Side<NT>;
     constexpr int kWarps = Shape<NT>::kWarps, kRows = Shape<NT>::kRows, kTiles = Shape<NT>::kTiles;
-    constexpr int kBytesW = kRows * 64, kPart = Shape<NT>::kPart;
+    constexpr int kBytesW = kRows * 128, kPart = Shape<NT>::kPart;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint8_t* ring_w = base + warp * kDepth * kBytesW;
     St* ring = reinterpret_cast<St*>(base + kWarps * kDepth * kBytesW) + warp * kDepth;
@@ -317,7 +318,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
     fence_barrier_init();
     make_plan<NT>(pl, a);
 
-    const int KB = a.K / 128, NB = a.N / kRows;
+    const int KB = a.K / 128, KP = (KB + 1) / 2, NB = a.N / kRows;
     // this CTA's share of the row blocks, and the warps that share one: the fewest with
     // which at least seven eighths of the warps' time is used, else the most
     const int items = pl.runs * NB;
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
     const int end = static_cast<int>(items * (static_cast<int64_t>(blockIdx.x) + 1) / grid);
     const int most = (items + a.ctas - 1) / a.ctas;
     int S = 1;
-    while (S < kWarps && 2 * S <= KB) {
+    while (S < kWarps && 2 * S <= KP) {
         const int teams = kWarps / S;
         if (8 * most >= 7 * ((most + teams - 1) / teams * teams)) break;
         S *= 2;
@@ -355,10 +356,10 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
         if (load_item >= end) return;
         if (lane < ld.rows) {
             const int64_t r = pl.xrow[ld.first + lane];
-            from_x = a.x + r * a.K + ld.kb * 128;
-            from_xs = a.xs + r * KB + ld.kb;
+            from_x = a.x + r * a.K + ld.kb * 256;
+            from_xs = a.xs + r * KB + 2 * ld.kb;
         }
-        from_ws = a.ws + (static_cast<int64_t>(ld.expert) * a.N + ld.block_row * kRows + lane) * KB + ld.kb;
+        from_ws = a.ws + (static_cast<int64_t>(ld.expert) * a.N + ld.block_row * kRows + lane) * KB + 2 * ld.kb;
     };
     place_load();
     RingPos<kDepth> in, out;
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
 
     // issues the copies of the next block of this warp's work, if there is one
     const auto load_next = [&]() {
-        while (load_item < end && ld.kb >= KB) {
+        while (load_item < end && ld.kb >= KP) {
             load_item += teams;
             place_load();
         }
@@ -375,19 +376,25 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
             St& s = ring[in.stage];
             uint64_t* bar = &full[in.stage];
             const int row0 = ld.expert * a.N + ld.block_row * kRows;
-            if (lane == 0) mbar_arrive_expect_tx(bar, kBytesW + ld.rows * 128);
+            const bool both = 2 * ld.kb + 1 < KB;  // the last pair may be one block
+            const uint32_t bytes = both ? 256 : 128;
+            if (lane == 0) mbar_arrive_expect_tx(bar, kBytesW + ld.rows * bytes);
             __syncwarp();
-            if (lane == 0) tma_load_2d(ring_w + in.stage * kBytesW, &map_w, ld.kb * 64, row0, bar);
+            if (lane == 0) tma_load_2d(ring_w + in.stage * kBytesW, &map_w, ld.kb * 128, row0, bar);
             if (lane < ld.rows) {
-                if (access_ok(from_x, 128, false)) bulk_load(s.x + lane * kPitch, from_x, 128, bar);
-                cp_async4(&s.xs[lane], from_xs);
-                from_x += S * 128;
-                from_xs += S;
+                if (access_ok(from_x, bytes, false)) bulk_load(s.x + lane * kPitch, from_x, bytes, bar);
+                cp_async4(&s.xs[0][lane], from_xs);
+                if (both) cp_async4(&s.xs[1][lane], from_xs + 1);
+                from_x += S * 256;
+                from_xs += 2 * S;
             }
 #pragma unroll
-            for (int i = 0; i < kRows / 32; ++i)
-                cp_async4(&s.ws[i * 32 + lane], from_ws + static_cast<int64_t>(i * 32) * KB);
-            from_ws += S;
+            for (int i = 0; i < kRows / 32; ++i) {
+                const uint32_t* from = from_ws + static_cast<int64_t>(i * 32) * KB;
+                cp_async4(&s.ws[0][i * 32 + lane], from);
+                if (both) cp_async4(&s.ws[1][i * 32 + lane], from + 1);
+            }
+            from_ws += 2 * S;
             ld.kb += S;
             in.advance();
             ++on_way;
@@ -406,7 +413,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
-        for (; at.kb < KB; at.kb += S) {
+        for (; at.kb < KP; at.kb += S) {
             load_next();
             if (!dead) {
                 const bool ok = mbar_wait_bounded(&full[out.stage], out.phase, &pl.abort, a.status);
@@ -421,10 +428,14 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
             out.advance();
             --on_way;
             // columns without rows are left out, eight at a time
-            if (NT == 1 || at.rows <= 8)
-                multiply<1, NT, G32, FMT>(w, s, acc, lane);
-            else
-                multiply<NT, NT, G32, FMT>(w, s, acc, lane);
+            const int blocks = 2 * at.kb + 1 < KB ? 2 : 1;
+#pragma unroll 1
+            for (int b = 0; b < blocks; ++b) {
+                if (NT == 1 || at.rows <= 8)
+                    multiply<1, NT, G32, FMT>(w, s, acc, b, lane);
+                else
+                    multiply<NT, NT, G32, FMT>(w, s, acc, b, lane);
+            }
             // the stage is refilled by the next copies, made in the async proxy
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
@@ -478,7 +489,7 @@ template <int NT, bool G32, int FMT>
 cudaError_t launch(const CUtensorMap& map, Args a, int64_t items, cudaStream_t stream) {
     auto* k = &w4_kernel<NT, G32, FMT>;
     constexpr int kThreads = Shape<NT>::kThreads;
-    constexpr size_t smem = Shape<NT>::kWarps * kDepth * (Shape<NT>::kRows * 64 + sizeof(Side<NT>)) +
+    constexpr size_t smem = Shape<NT>::kWarps * kDepth * (Shape<NT>::kRows * 128 + sizeof(Side<NT>)) +
                             sizeof(Plan<NT>);
     static_assert(smem <= 227 * 1024, "shared memory");
     const int grid = persistent_grid(reinterpret_cast<const void*>(k), kThreads, smem, items);
@@ -492,7 +503,7 @@ template <int NT>
 cudaError_t launch_form(const W4Product& p, const Args& a, int64_t experts, cudaStream_t stream) {
     constexpr int kRows = Shape<NT>::kRows;
     CUtensorMap map;
-    if (!encode_u8_2d_swizzled(&map, p.w, p.K / 2, p.E * p.N, 64, kRows)) return cudaErrorInvalidValue;
+    if (!encode_u8_2d_swizzled(&map, p.w, p.K / 2, p.E * p.N, 128, kRows)) return cudaErrorInvalidValue;
     const bool g32 = p.group == 32;
     const int fmt = p.fmt;
     const int64_t items = experts * (p.N / kRows);
