@@ -21,11 +21,11 @@
 // after another; S of its warps share those of a block, each taking every S-th 256
 // channels, where otherwise some of the warps would have none left at the end.  No warp
 // waits for another but at the end of shared rows.
-// Measured: those 48 tokens 85 us (3.4 TB/s), one token's 8 matrices of 4096 x 4096 22 us
-// (3.2 TB/s); 128 channels at a time, in twice as many stages, 98 and 23.  What is left is
-// widening the weights, 7 operations for 8, and the latency of a warp's steps.  FP8 MMAs
-// (m16n8k32) would take codes of x as they are, but are slower here than binary16 ones:
-// 190 us where those took 145.
+// Measured: those 48 tokens 79 us (3.6 TB/s), one token's 8 matrices of 4096 x 4096 21 us
+// (3.3 TB/s); 128 channels at a time, in twice as many stages, took 13 us more for the 48.  What
+// is left is widening the weights, 7 operations for 8, and the latency of a warp's steps.
+// FP8 MMAs (m16n8k32) would take codes of x as they are, but are slower here than binary16
+// ones: 190 us where those took 145.
 #include <cuda_runtime.h>
 
 #include "tkq_async.cuh"
@@ -72,9 +72,8 @@ struct Plan {
     uint16_t run_expert[kMaxPairs];
     union {
         struct {
-            uint16_t count[kMaxExperts];
-            uint16_t first[kMaxExperts];  // first of its pairs in `pair`
-            int16_t expert[kMaxPairs];    // of each pair, -1 for none
+            int count[kMaxExperts];
+            uint16_t first[kMaxExperts];  // first of its pairs in `pair`, then the next one's place
         };
         float parts[Shape<NT>::kWarps][Shape<NT>::kPart][32];  // sums of shared rows, after the plan is made
     };
@@ -132,28 +131,32 @@ struct Cursor {
     int expert, first, rows;
 };
 
-// The pairs of each expert, cut into runs, by one warp in the order of the pairs, so that
-// every CTA makes the same runs; the scan over the experts by all.
+// The pairs of each expert in rising order, cut into runs: every CTA makes the same ones.
+// Pairs stay in the registers of the lanes that read them, 32 to a warp; the warps place
+// theirs one after another.  (One warp doing all of it took 9 us for 384 pairs.)
 template <int NT>
 __device__ void make_plan(Plan<NT>& pl, const Args& a) {
-    constexpr int kThreads = Shape<NT>::kThreads;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int kThreads = Shape<NT>::kThreads, kWarps = Shape<NT>::kWarps;
     constexpr int kPer = kMaxExperts / kThreads;  // experts of a thread, in turn
+    constexpr int kMine = kMaxPairs / kThreads;   // pairs of a lane, kThreads apart
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int bits = 32 - __clz(a.E - 1);         // of an expert's number
-    for (int e = tid; e < a.E; e += kThreads) pl.count[e] = 0;
-    for (int p = tid; p < a.P; p += kThreads) {
-        const int e = a.ids ? ld_ro(a.ids + p) : 0;
-        pl.expert[p] = static_cast<int16_t>(e >= 0 && e < a.E ? e : -1);
+    int expert[kMine];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const int p = i * kThreads + tid;
+        const int e = p >= a.P ? -1 : a.ids ? ld_ro(a.ids + p) : 0;
+        expert[i] = e >= 0 && e < a.E ? e : -1;
     }
+    for (int e = tid; e < a.E; e += kThreads) pl.count[e] = 0;
     __syncthreads();
-    if (warp == 0)
-        for (int p0 = 0; p0 < a.P; p0 += 32) {
-            const int p = p0 + lane;
-            const int e = p < a.P ? pl.expert[p] : -1;
-            const unsigned same = lanes_of_value(e, bits, __ballot_sync(0xffffffffu, e >= 0));
-            if (e >= 0 && lane == __ffs(same) - 1) pl.count[e] += __popc(same);
-            __syncwarp();
-        }
+    unsigned same[kMine];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        if (i * kThreads + warp * 32 >= a.P) break;
+        same[i] = lanes_of_value(expert[i], bits, __ballot_sync(0xffffffffu, expert[i] >= 0));
+        if (expert[i] >= 0 && lane == __ffs(same[i]) - 1) atomicAdd(&pl.count[expert[i]], __popc(same[i]));
+    }
     __syncthreads();
     int n = 0, r = 0, cnt[kPer];
 #pragma unroll
@@ -176,11 +179,13 @@ __device__ void make_plan(Plan<NT>& pl, const Args& a) {
         pl.sums[1][warp] = r;
     }
     __syncthreads();
-    int at_n = n - n_mine, at_r = r - r_mine;
-    for (int w = 0; w < warp; ++w) {
-        at_n += pl.sums[0][w];
-        at_r += pl.sums[1][w];
+    int before_n = lane < warp ? pl.sums[0][lane] : 0, before_r = lane < warp ? pl.sums[1][lane] : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        before_n += __shfl_xor_sync(0xffffffffu, before_n, o);
+        before_r += __shfl_xor_sync(0xffffffffu, before_r, o);
     }
+    int at_n = before_n + n - n_mine, at_r = before_r + r - r_mine;
     if (tid == kThreads - 1) {
         pl.runs = at_r + r_mine;
         pl.run_first[at_r + r_mine] = static_cast<uint16_t>(at_n + n_mine);
@@ -196,23 +201,24 @@ __device__ void make_plan(Plan<NT>& pl, const Args& a) {
         at_n += cnt[i];
     }
     __syncthreads();
-    if (warp == 0)
-        for (int p0 = 0; p0 < a.P; p0 += 32) {
-            const int p = p0 + lane;
-            const int e = p < a.P ? pl.expert[p] : -1;
-            const bool live = e >= 0;
-            const unsigned same = lanes_of_value(e, bits, __ballot_sync(0xffffffffu, live));
-            const int at = live ? pl.first[e] : 0;
-            __syncwarp();
-            if (live) {
-                const int to = at + __popc(same & ((1u << lane) - 1u));
-                pl.pair[to] = static_cast<uint16_t>(p);
-                pl.xrow[to] = static_cast<uint16_t>(p / a.share);
-                if (lane == __ffs(same) - 1) pl.first[e] = static_cast<uint16_t>(at + __popc(same));
+#pragma unroll
+    for (int i = 0; i < kMine; ++i)
+        for (int w = 0; w < kWarps; ++w) {
+            if (i * kThreads + w * 32 >= a.P) break;
+            if (warp == w) {
+                const bool live = expert[i] >= 0;
+                const int at = live ? pl.first[expert[i]] : 0;
+                __syncwarp();
+                if (live) {
+                    const int to = at + __popc(same[i] & ((1u << lane) - 1u)), p = i * kThreads + tid;
+                    pl.pair[to] = static_cast<uint16_t>(p);
+                    pl.xrow[to] = static_cast<uint16_t>(p / a.share);
+                    if (lane == __ffs(same[i]) - 1)
+                        pl.first[expert[i]] = static_cast<uint16_t>(at + __popc(same[i]));
+                }
             }
-            __syncwarp();
+            __syncthreads();
         }
-    __syncthreads();
 }
 
 // acc += the products of a stage's block b, 8 NV columns of them.
@@ -571,7 +577,7 @@ cudaError_t launch_w4_product(const W4Product& p, cudaStream_t stream) {
     a.status = device_status_word();
     const int64_t experts = p.ids ? (a.P < p.E ? a.P : p.E) : 1;  // at most this many have rows
     // eight columns where an expert has at most eight rows on average (48 tokens, 8 of 64
-    // matrices of 4096 x 2048: 101 us, with 16 columns 115)
+    // matrices of 4096 x 2048: 101 us, with 16 columns 115, both with stages of 128 channels)
     return a.P <= 8 * experts ? launch_form<1>(p, a, experts, stream) : launch_form<2>(p, a, experts, stream);
 }
 
