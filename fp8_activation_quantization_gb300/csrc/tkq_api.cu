@@ -891,7 +891,8 @@ tkq_status tkq_expert_gather(const void* x, const float* x_sf, const int32_t* sl
     const Buffer in[] = {{x, T * C * (codes_in ? 1 : 2), 16}, {x_sf, T * G * 4, 4},
                          {slots, T * k * 4, 4},               {rows, R * 4, 4},
                          {offsets, (E + 1) * 4, 4},           {weights, T * k * 4, 4}};
-    const Buffer outs[] = {{out, R * C * (codes_out ? 1 : 2), 16},
+    // bf16 rows are stored in whole sectors of 32 bytes
+    const Buffer outs[] = {{out, R * C * (codes_out ? 1 : 2), codes_out ? 16u : 32u},
                            {out_sf, R * G * 4, 4},
                            {row_weights, R * 4, 4}};
     if ((st = check_buffers(in, outs)) != TKQ_OK) return st;
@@ -974,7 +975,7 @@ tkq_status tkq_expert_product(const void* a, const float* a_sf, const void* w, c
                          {w, E * N * K, 16},
                          {w_sf, E * (N / 128) * (K / 128) * 4, 4},
                          {offsets, (E + 1) * 4, 4}};
-    const Buffer outs[] = {{out, R * N * 2, 16}};
+    const Buffer outs[] = {{out, R * N * 2, 32}};
     if ((st = check_buffers(in, outs)) != TKQ_OK) return st;
     const tkq::ExpertProduct p = {a, a_sf, w, w_sf, offsets, out, R, N, K, static_cast<int>(E),
                                   fmt_a, fmt_w, false};
@@ -998,7 +999,7 @@ tkq_status tkq_expert_weight_grad(const void* dy_t, const float* dy_sf, const vo
                          {x_t, K * R, 16},
                          {x_sf, K * (R / 128) * 4, 4},
                          {offsets, (E + 1) * 4, 4}};
-    const Buffer outs[] = {{dw, E * N * K * (f32 ? 4 : 2), 16}};
+    const Buffer outs[] = {{dw, E * N * K * (f32 ? 4 : 2), 32}};
     if ((st = check_buffers(in, outs)) != TKQ_OK) return st;
     const tkq::ExpertProduct p = {dy_t, dy_sf, x_t, x_sf, offsets, dw, R, N, K, static_cast<int>(E),
                                   fmt_dy, fmt_x, f32};

@@ -515,7 +515,7 @@ tkq_status tkq_expert_order(const int32_t* ids, int32_t* slots, int32_t* rows, i
  *   slots, rows, offsets : as tkq_expert_order gives them; a slot outside [0, R) is
  *   an empty one.  The gradient of this call is tkq_expert_reduce without weights.
  * T >= 0, T * k <= 2^30; C > 0, C % 128 == 0, C <= 2^20; k, E and R as above.
- * Alignment: x, out 16 bytes, else 4.
+ * Alignment: x, out 16 bytes (bf16 rows of out 32), else 4.
  */
 #define TKQ_ROWS_BF16 0
 #define TKQ_ROWS_CAST 1
@@ -570,7 +570,7 @@ tkq_status tkq_expert_reduce_backward(const void* dout, const void* y, const int
  *   w : codes [E, N, K] in fmt_w;  w_sf : fp32 [E, N/128, K/128] (tkq_per_block_cast)
  *   offsets : int32 [E + 1];  out : bf16 [R, N]
  * R >= 0, R < 2^31; 0 < E <= 1024; N, K > 0, multiples of 128, at most 2^20,
- * E * N < 2^31.  Alignment: a, w, out 16 bytes, else 4.  NaN codes and infinite
+ * E * N < 2^31.  Alignment: a, w 16 bytes, out 32, else 4.  NaN codes and infinite
  * scales give unspecified values in their own rows and columns.
  */
 tkq_status tkq_expert_product(const void* a, const float* a_sf, const void* w, const float* w_sf,
@@ -588,7 +588,8 @@ tkq_status tkq_expert_product(const void* a, const float* a_sf, const void* w, c
  *   dy_t : codes [N, R] in fmt_dy;  dy_sf : fp32 [N, R/128]
  *   x_t  : codes [K, R] in fmt_x;   x_sf : fp32 [K, R/128]
  *   dw   : [E, N, K] of out_dtype (TKQ_OUT_F32 or TKQ_OUT_BF16)
- * R >= 0, a multiple of 128, R < 2^31; N, K, E, alignment as above.
+ * R >= 0, a multiple of 128, R < 2^31; N, K, E as above.  Alignment: dy_t, x_t 16
+ * bytes, dw 32, else 4.
  */
 tkq_status tkq_expert_weight_grad(const void* dy_t, const float* dy_sf, const void* x_t,
                                   const float* x_sf, const int32_t* offsets, void* dw, int64_t R,

@@ -68,6 +68,7 @@ GATHER = dict(x=at(0), x_sf=None, slots=at(1), rows=at(2), offsets=at(3), weight
     (dict(group=64), GROUP), (dict(C=200), SHAPE), (dict(C=0), SHAPE), (dict(C=2 ** 21), SHAPE), (dict(T=-1), SHAPE),
     (dict(k=40), SHAPE), (dict(E=0), SHAPE), (dict(R=-1), SHAPE), (dict(x=at(0, 8)), ALIGN), (dict(out=at(5, 4)), ALIGN),
     (dict(out_sf=at(6, 2)), ALIGN), (dict(out=at(0)), ALIAS), (dict(row_weights=at(4)), ALIAS),
+    (dict(form=0, out_sf=None, out=at(5, 16)), ALIGN),  # bf16 rows go out in sectors of 32 bytes
     (dict(out_sf=at(5, 1024)), ALIAS), (dict(T=0, x=None), 0), (dict(R=0, out=None), 0)])
 def test_gather_refusals(lib, changes, expected):
     assert _call(lib.tkq_expert_gather, GATHER, **changes) == expected
@@ -109,7 +110,8 @@ PRODUCT = dict(a=at(0), a_sf=at(1), w=at(2), w_sf=at(3), offsets=at(4), out=at(5
     (dict(R=2 ** 31 - 1), SHAPE), (dict(E=0), SHAPE), (dict(E=1025), SHAPE), (dict(N=100), SHAPE), (dict(N=0), SHAPE),
     (dict(K=64), SHAPE), (dict(K=2 ** 21), SHAPE), (dict(E=1024, N=2 ** 21), SHAPE), (dict(E=1024, N=2 ** 20, K=2 ** 20), SHAPE),
     (dict(group=64), GROUP), (dict(fmt_a=2), FMT), (dict(fmt_w=-1), FMT), (dict(a=at(0, 8)), ALIGN), (dict(w=at(2, 4)), ALIGN),
-    (dict(out=at(5, 2)), ALIGN), (dict(a_sf=at(1, 2)), ALIGN), (dict(out=at(0, 131072 - 16)), ALIAS),
+    (dict(out=at(5, 2)), ALIGN), (dict(out=at(5, 16)), ALIGN), (dict(a_sf=at(1, 2)), ALIGN),
+    (dict(out=at(0, 131072 - 32)), ALIAS),
     (dict(out=at(4)), ALIAS), (dict(R=0, a=None), 0)])
 def test_product_refusals(lib, changes, expected):
     assert _call(lib.tkq_expert_product, PRODUCT, **changes) == expected
@@ -123,6 +125,7 @@ GRAD = dict(dy_t=at(0), dy_sf=at(1), x_t=at(2), x_sf=at(3), offsets=at(4), dw=at
     *((dict([(n, None)]), NULL) for n in ("dy_t", "dy_sf", "x_t", "x_sf", "offsets", "dw")), (dict(R=100), SHAPE),
     (dict(R=-128), SHAPE), (dict(E=0), SHAPE), (dict(N=130), SHAPE), (dict(K=0), SHAPE), (dict(group=32), GROUP),
     (dict(fmt_dy=2), FMT), (dict(fmt_x=3), FMT), (dict(dtype=2), FMT), (dict(dy_t=at(0, 4)), ALIGN), (dict(dw=at(5, 8)), ALIGN),
+    (dict(dw=at(5, 16)), ALIGN), (dict(dw=at(5, 16), dtype=1), ALIGN),
     (dict(dw=at(2)), ALIAS), (dict(R=0, dy_t=None, offsets=None), NULL)])
 def test_weight_grad_refusals(lib, changes, expected):
     assert _call(lib.tkq_expert_weight_grad, GRAD, **changes) == expected
