@@ -170,9 +170,9 @@ __global__ void __launch_bounds__(kOrderThreads, 1)
     }
     // rows without a pair: behind each expert's and behind the last one's
     for (int x = rank * kOrderWarps + warp; x < E; x += ctas * kOrderWarps)
-        for (int r = sm.start[x] + sm.all[x] + lane; r < sm.start[x + 1]; r += 32)
+        for (int64_t r = static_cast<int64_t>(sm.start[x]) + sm.all[x] + lane; r < sm.start[x + 1]; r += 32)
             st_plain(rows + r, -1);
-    for (int r = sm.start[E] + rank * kOrderThreads + static_cast<int>(threadIdx.x); r < R;
+    for (int64_t r = static_cast<int64_t>(sm.start[E]) + rank * kOrderThreads + threadIdx.x; r < R;
          r += ctas * kOrderThreads)
         st_plain(rows + r, -1);
 }

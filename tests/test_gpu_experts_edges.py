@@ -182,6 +182,20 @@ def test_captured_and_replayed(cuda_device):
     assert tkq.tkq_read_device_status() == 0
 
 
+def test_an_order_of_a_whole_cluster_captured_and_replayed(cuda_device):
+    T, k, E = 5000, 8, 100
+    ids = ids_of(T, k, E, gen(1))
+    order = tkq.expert_order(ids, E)                 # its buffers are the graph's
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        tkq.expert_order(ids, E, 128, *order)
+    for s in (2, 3):
+        ids.copy_(ids_of(T, k, E, gen(s)))
+        graph.replay()
+        for u, v in zip(order, tkq.expert_order(ids, E)):
+            assert torch.equal(u, v)
+
+
 def test_on_a_side_stream_behind_its_work(cuda_device):
     """Calls go to the current stream: inputs are written there just before, late."""
     side = torch.cuda.Stream()
