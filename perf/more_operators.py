@@ -25,48 +25,50 @@ E2M1 = [0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0]
 def listed():
     return [
         # a decoding step of 4 sequences: each token to 8 of 256 experts, cast on the way; latency counts
-        dict(name="sort of 4 tokens", op="sort", T=4, k=8, E=256, C=7168, align=1, form="cast", fmt="e4m3",
+        dict(name="sort, 4 tokens", op="sort", T=4, k=8, E=256, C=7168, align=1, form="cast", fmt="e4m3",
              weighted=True, dropped=False),
         # a training batch of 8192 tokens to 8 of 64 experts, groups of 128 rows for the transposed casts
-        dict(name="sort of 8192 tokens", op="sort", T=8192, k=8, E=64, C=4096, align=128, form="cast",
+        dict(name="sort, 8192 tokens", op="sort", T=8192, k=8, E=64, C=4096, align=128, form="cast",
              fmt="e4m3", weighted=True, dropped=False),
         # the gradient of sorting an odd batch, with tokens that have empty slots, and the gradients of
         # the rows' weights
-        dict(name="back of 1021 tokens", op="back", T=1021, k=6, E=60, C=1408, align=128, weighted=False,
+        dict(name="back, 1021 tokens", op="back", T=1021, k=6, E=60, C=1408, align=128, weighted=False,
              values=True, dropped=True, out="bf16"),
         # the experts' outputs of the training batch, weighted and summed for each token
-        dict(name="back of 8192 tokens", op="back", T=8192, k=8, E=64, C=4096, align=128, weighted=True,
+        dict(name="back, 8192 tokens", op="back", T=8192, k=8, E=64, C=4096, align=128, weighted=True,
              values=False, dropped=False, out="bf16"),
         # the backward of a weighted sum on a small odd batch, gradients cast for the next product
-        dict(name="back backward of 333 tokens", op="back_bwd", T=333, k=4, E=12, C=640, align=128,
+        dict(name="back backward, 333 tokens", op="back_bwd", T=333, k=4, E=12, C=640, align=128,
              form="cast", fmt="e5m2", dropped=True),
         # the same on the training batch: bf16 gradients and those of the weights
-        dict(name="back backward of 8192 tokens", op="back_bwd", T=8192, k=8, E=64, C=4096, align=128,
+        dict(name="back backward, 8192 tokens", op="back_bwd", T=8192, k=8, E=64, C=4096, align=128,
              form="bf16", fmt="e4m3", dropped=False),
         # a short prompt: a few rows for each of 60 experts, where reading the weights counts
-        dict(name="product of 384 rows", op="product", rows=384, E=60, N=2816, K=2048, align=1, fmt="e4m3"),
+        dict(name="product, 384 rows", op="product", rows=384, E=60, N=2816, K=2048, align=1, fmt="e4m3"),
         # the first product of the training batch's experts (gate and up of H = 2048), 32 experts
-        dict(name="product of 65536 rows", op="product", rows=65536, E=32, N=4096, K=4096, align=128,
+        dict(name="product, 65536 rows", op="product", rows=65536, E=32, N=4096, K=4096, align=128,
              fmt="e4m3"),
         # the weight gradient of a small ragged batch, experts without rows among them
-        dict(name="weight gradient of 1100 rows", op="weight_grad", rows=1100, E=12, N=768, K=640,
+        dict(name="weight gradient, 1100 rows", op="weight_grad", rows=1100, E=12, N=768, K=640,
              fmt="e5m2", out="f32"),
         # the weight gradient of the first product, 65536 rows of 8 experts
-        dict(name="weight gradient of 65536 rows", op="weight_grad", rows=65536, E=8, N=4096, K=4096,
+        dict(name="weight gradient, 65536 rows", op="weight_grad", rows=65536, E=8, N=4096, K=4096,
              fmt="e4m3", out="f32"),
         # one token at a time: the first product of its 8 of 64 experts with 4-bit weights
-        dict(name="4-bit product of 1 token", op="w4", T=1, k=8, E=64, N=4096, K=4096, group=32, each=False),
+        dict(name="4-bit product, 1 token", op="w4", T=1, k=8, E=64, N=4096, K=4096, group=32, each=False),
         # 48 sequences decoded together: the second product, each expert's rows with their own input
-        dict(name="4-bit product of 48 tokens", op="w4", T=48, k=8, E=64, N=4096, K=2048, group=32, each=True),
+        dict(name="4-bit product, 48 tokens", op="w4", T=48, k=8, E=64, N=4096, K=2048, group=32, each=True),
     ]
 
 
 def draw(rng):
     def size(lo, hi):
-        return max(lo, min(hi, round(math.exp(rng.uniform(math.log(lo), math.log(hi + 0.5))))))
+        n = max(lo, min(hi, round(math.exp(rng.uniform(math.log(lo), math.log(hi + 0.5))))))
+        return n + 1 if n == 3072 else n
 
     def width(most):
-        return GROUP * size(1, most)
+        n = size(1, most)
+        return GROUP * (n + 1 if n in (12, 24) else n)
 
     op = rng.choice(["sort", "back", "back_bwd", "product", "weight_grad", "w4"])
     if op in ("sort", "back", "back_bwd"):
