@@ -1455,7 +1455,8 @@ def w4_product(x, x_sf, w, w_sf, ids=None, out=None):
 
 def w4_cast(w, group: int = 32):
     """Weights for ``w4_product``: bf16 [N, K] or [E, N, K] -> (E2M1 codes uint8 [..., K/2], scales of
-    ``group`` channels: UE8M0 (uint8 [..., K/32]) for 32, fp32 [..., K/128] for 128)."""
+    ``group`` channels: UE8M0 (uint8 [..., K/32]) for 32, fp32 [..., K/128] for 128).  A group
+    with a NaN or an infinity has the scale NaN (255 as UE8M0): products with it are NaN."""
     import torch
     if (not isinstance(w, torch.Tensor) or not w.is_cuda or w.dtype != torch.bfloat16
             or w.dim() not in (2, 3) or not w.is_contiguous()):

@@ -525,7 +525,15 @@ cudaError_t launch_form(const W4Product& p, const Args& a, int64_t experts, cuda
 // ---------------------------------------------------------------------------
 // A warp takes 128 values of a row, a lane four: the largest magnitude of 8 lanes (32
 // values) or of all, the scale amax / 6 (UE8M0: the power of two not below it), and the
-// codes of the quotient, to nearest, ties to even, by the hardware conversion.
+// codes of the quotient, to nearest, ties to even, by the hardware conversion.  E2M1 has no
+// code for what is no number, so a group with a NaN (which fmaxf would drop) or an infinity
+// says so in its scale, and every product with it is NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 template <bool G32>
 __global__ void __launch_bounds__(256) w4_cast_kernel(const uint2* __restrict__ w, uint16_t* __restrict__ codes,
                                                       void* __restrict__ sf, int64_t groups) {
@@ -534,9 +542,10 @@ __global__ void __launch_bounds__(256) w4_cast_kernel(const uint2* __restrict__ 
          u += static_cast<int64_t>(gridDim.x) * 8) {
         const uint2 q = ld_ro(w + u * 32 + lane);
         const float v[4] = {bf16_lo(q.x), bf16_hi(q.x), bf16_lo(q.y), bf16_hi(q.y)};
-        float m = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+        float m = max_nan(max_nan(fabsf(v[0]), fabsf(v[1])), max_nan(fabsf(v[2]), fabsf(v[3])));
 #pragma unroll
-        for (int o = 1; o < (G32 ? 8 : 32); o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        for (int o = 1; o < (G32 ? 8 : 32); o <<= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const bool finite = m <= 3.402823466e+38f;
         // the smallest scale is 2^-126, so that zeros and tiny groups have one
         float s = fmaxf(__fdiv_rn(m, 6.0f), 1.17549435e-38f);
         if constexpr (G32) {
@@ -544,9 +553,9 @@ __global__ void __launch_bounds__(256) w4_cast_kernel(const uint2* __restrict__ 
             pow2_scale(s, inv);
             if ((lane & 7) == 0)
                 st_plain(static_cast<uint8_t*>(sf) + u * 4 + (lane >> 3),
-                         static_cast<uint8_t>(__float_as_uint(s) >> 23));
+                         finite ? static_cast<uint8_t>(__float_as_uint(s) >> 23) : uint8_t{255});
         } else if (lane == 0) {
-            st_plain(static_cast<float*>(sf) + u, s);
+            st_plain(static_cast<float*>(sf) + u, finite ? s : __uint_as_float(0x7FFFFFFFu));
         }
         uint16_t c;
         asm("{\n\t.reg .b8 lo, hi;\n\t"
@@ -556,7 +565,7 @@ __global__ void __launch_bounds__(256) w4_cast_kernel(const uint2* __restrict__ 
             : "=h"(c)
             : "f"(__fdiv_rn(v[0], s)), "f"(__fdiv_rn(v[1], s)), "f"(__fdiv_rn(v[2], s)),
               "f"(__fdiv_rn(v[3], s)));
-        st_plain(codes + u * 32 + lane, c);
+        st_plain(codes + u * 32 + lane, finite ? c : uint16_t{0});
     }
 }
 

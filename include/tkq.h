@@ -607,7 +607,7 @@ tkq_status tkq_expert_weight_grad(const void* dy_t, const float* dy_sf, const vo
  *   w : E2M1 codes [E, N, K/2], two in a byte, the low four bits the even channel:
  *       sign, two bits of exponent, one of mantissa: 0, 0.5, 1, 1.5, 2, 3, 4, 6
  *   w_sf : s of groups along K, w_group 32: UE8M0 bytes [E, N, K/32], s = 2^(byte -
- *       127) (255 gives unspecified values), or w_group 128: fp32 [E, N, K/128]
+ *       127) (255 is NaN), or w_group 128: fp32 [E, N, K/128]
  *   ids : int32 [T, k];  out : bf16 [T * k, N]
  * T >= 0, 0 < k <= 32, T * k <= 1024 (a larger batch is tkq_expert_product's);
  * 0 < E <= 1024; N, K > 0, multiples of 128, at most 2^20, else TKQ_ERR_SHAPE;
@@ -624,7 +624,9 @@ tkq_status tkq_w4_product(const void* x, const float* x_sf, const void* w, const
  * The weights of tkq_w4_product from bf16 [N, K] (the matrices of several experts as
  * one of E * N rows): for each group of w_group channels
  *   s = max(amax / 6, 2^-126), for w_group 32 rounded up to a power of two,
- * and the codes of fl32(w / s), to nearest, ties to even, saturating.
+ * and the codes of fl32(w / s), to nearest, ties to even, saturating.  A group with a
+ * NaN or an infinity has the scale NaN (255 as UE8M0) and codes of zero: products
+ * with it are NaN.
  *   codes : [N, K/2];  sf : UE8M0 bytes [N, K/32] or fp32 [N, K/128]
  * N >= 0; K > 0, K % 128 == 0.  Alignment: w 16 bytes, else 4.
  */
