@@ -323,6 +323,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         RingPos<kUnits> pos;
         bool ok = true;
         for (; ok && walk.get(a, sm, t); walk.next()) {
+            // lanes part at the end of a tile (one stores a box, or those with a row store it); reads of
+            // tensor memory are the whole warp's
+            __syncwarp();
             uint64_t sum[kCols / 2];  // pairs of binary32
 #pragma unroll
             for (int i = 0; i < kCols / 2; ++i) sum[i] = 0;
