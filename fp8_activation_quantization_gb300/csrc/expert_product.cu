@@ -378,9 +378,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const auto pair = [&](int i) {
                 return pack_bf16x2(__uint_as_float(value(i)), __uint_as_float(value(i + 1)));
             };
-#ifndef TKQ_CHECKED
             if constexpr (!GRAD) {
-                if (t.row + quarter * 32 + 32 <= sm.start[t.e + 1]) {  // the expert has all of the warp's rows
+                // the expert has all of the warp's rows (and, checked build, the output all of them: a box
+                // is refused as a whole, its rows then one by one)
+                if (t.row + quarter * 32 + 32 <= sm.start[t.e + 1] &&
+                    __all_sync(0xffffffffu, access_ok(static_cast<uint16_t*>(a.out) + at, kCols * 2, true))) {
                     uint8_t* box = boxes + warp * 2 * kBytesBox;
                     if (lane == 0) bulk_wait_read();  // the tile before
                     __syncwarp();
@@ -400,7 +402,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     continue;
                 }
             }
-#endif
             // a lane's row in whole sectors of 32 bytes
             if (!live) continue;
             constexpr int kPer = F32 ? 8 : 16;
