@@ -35,7 +35,7 @@
 namespace tkq {
 namespace {
 
-constexpr int kBM = 128, kBN = 256, kBK = 128;
+constexpr int kBM = 128, kBN = 256, kBK = 128;  // kBK: the width of a tensor map's box
 constexpr int kStages = 3;
 constexpr int kEpilogueWarps = 8;
 constexpr int kCols = kBN / (kEpilogueWarps / 4);  // columns of a warp
@@ -427,9 +427,9 @@ template <bool GRAD, bool F32>
 cudaError_t launch(const ExpertProduct& p, int64_t tiles, cudaStream_t stream) {
     CUtensorMap map_a, map_b, map_out = {};
     const bool made =
-        GRAD ? encode_u8_2d_swizzled(&map_a, p.a, p.R, p.N, kBK, kBM) && encode_u8_2d_swizzled(&map_b, p.b, p.R, p.K, kBK, kBN)
-             : encode_u8_2d_swizzled(&map_a, p.a, p.K, p.R, kBK, kBM) &&
-                   encode_u8_2d_swizzled(&map_b, p.b, p.K, p.E * p.N, kBK, kBN);
+        GRAD ? encode_u8_2d_swizzled(&map_a, p.a, p.R, p.N, kBM) && encode_u8_2d_swizzled(&map_b, p.b, p.R, p.K, kBN)
+             : encode_u8_2d_swizzled(&map_a, p.a, p.K, p.R, kBM) &&
+                   encode_u8_2d_swizzled(&map_b, p.b, p.K, p.E * p.N, kBN);
     if (!made || (!GRAD && !encode_bf16_2d_swizzled(&map_out, p.out, p.N, p.R, 32)))
         return cudaErrorInvalidValue;
     Args a = {};

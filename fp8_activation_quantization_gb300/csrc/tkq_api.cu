@@ -133,9 +133,9 @@ bool encode_bf16_2d(CUtensorMap* map, const void* base, int64_t cols, int64_t ro
 }
 
 bool encode_u8_2d_swizzled(CUtensorMap* map, const void* base, int64_t cols, int64_t rows,
-                           uint32_t box_cols, uint32_t box_rows) {
-    return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, cols, rows, box_cols, box_rows,
-                     box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+                           uint32_t box_rows) {
+    return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, cols, rows, 128, box_rows,
+                     CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 bool encode_bf16_2d_swizzled(CUtensorMap* map, const void* base, int64_t cols, int64_t rows,

@@ -276,10 +276,10 @@ cudaError_t launch_w4_product(const W4Product& p, cudaStream_t stream);
 cudaError_t launch_w4_cast(const void* w, void* codes, void* sf, int64_t N, int64_t K, int group,
                            cudaStream_t stream);
 
-// Tensor map of a row-major matrix of bytes [rows, cols] for boxes of box_cols (64 or
-// 128) bytes x box_rows in the swizzle of that width, out-of-range elements read as zero.
+// Tensor map of a row-major matrix of bytes [rows, cols] for boxes of 128 bytes x box_rows
+// in the 128-byte swizzle, out-of-range elements read as zero.
 bool encode_u8_2d_swizzled(CUtensorMap* map, const void* base, int64_t cols, int64_t rows,
-                           uint32_t box_cols, uint32_t box_rows);
+                           uint32_t box_rows);
 // The same of a row-major bf16 matrix, boxes of 64 elements x box_rows.
 bool encode_bf16_2d_swizzled(CUtensorMap* map, const void* base, int64_t cols, int64_t rows,
                              uint32_t box_rows);

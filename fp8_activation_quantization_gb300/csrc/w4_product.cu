@@ -509,7 +509,7 @@ template <int NT>
 cudaError_t launch_form(const W4Product& p, const Args& a, int64_t experts, cudaStream_t stream) {
     constexpr int kRows = Shape<NT>::kRows;
     CUtensorMap map;
-    if (!encode_u8_2d_swizzled(&map, p.w, p.K / 2, p.E * p.N, 128, kRows)) return cudaErrorInvalidValue;
+    if (!encode_u8_2d_swizzled(&map, p.w, p.K / 2, p.E * p.N, kRows)) return cudaErrorInvalidValue;
     const bool g32 = p.group == 32;
     const int fmt = p.fmt;
     const int64_t items = experts * (p.N / kRows);
