@@ -19,12 +19,17 @@
 // own: read by the eight warps themselves, a group before its use, they cost more than
 // the products (2.0 ms against 1.1 with scales that are not read, 65536 rows, 32
 // matrices of 4096 x 4096).
-// Measured on that size: 0.91 ms, 2.4 PFLOP/s; the gradient of 8 matrices 1.53 ms, 1.4
-// PFLOP/s.  Copies and MMAs alone take 0.66 and 0.77 ms.  What bounds it is taking each
-// group's sums out of tensor memory, which contends with the MMAs (0.77 ms with reads
-// and no arithmetic), and the arithmetic, one operation for each sum and in the gradient
-// two.  A few rows for each of many experts are bound by the weights: 384 rows of 60
-// matrices of 2816 x 2048 in 51 us, 6.8 TB/s.
+// Measured on that size: 0.91 ms, 2.4 PFLOP/s, at 2070 MHz, and 0.98 ms, 2.25 PFLOP/s, when it
+// runs for seconds and the power limit holds the clock near 1850 MHz; the gradient of 8
+// matrices 1.49 to 1.53 ms, 1.45 PFLOP/s.  Copies and MMAs alone take 0.66 and 0.77 ms.  No
+// unit is full: a summing warp reads 16 columns of tensor memory, waits for them and does
+// their arithmetic, one operation for each sum and in the gradient two, in turn.  Reads alone,
+// which contend with the MMAs, make it 0.77 ms; the arithmetic comes on top, and in the gradient the
+// stores, which the same warps make.  A few rows for each of many experts are bound by the
+// weights: 384 rows of 60 matrices of 2816 x 2048 in 51 us, 6.8 TB/s.
+// Every tile has 256 columns: the last one of a width that is an odd multiple of 128 reads,
+// multiplies and drops 128 columns that are another matrix's or none (65536 rows, 32 matrices of
+// N x 4096: N = 1408 takes 348 us and 1536 351, 384 takes 126 and 512 129, 128 takes 78 and 256 83).
 #include <cuda_runtime.h>
 
 #include "tkq_async.cuh"

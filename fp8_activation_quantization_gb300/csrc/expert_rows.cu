@@ -27,10 +27,12 @@ constexpr unsigned kAll = 0xffffffffu;
 // of its run of pairs, the warps' counts are added up within the CTA, the CTAs'
 // read through distributed shared memory, and the warp then walks its run again,
 // 32 pairs at a time, the lanes of one expert in pair order, so that equal experts
-// keep the order of their pairs and the result does not depend on the launch.  A cluster of at most eight CTAs (the portable size)
-// replaces the second launch and the workspace that a grid of CTAs would need; it
-// is bound by the latency of its steps, not by the few bytes it moves.  Each lane
-// asks for kBatch of its ids at once.
+// keep the order of their pairs and the result does not depend on the launch.  A cluster
+// of at most eight CTAs (the portable size) replaces the second launch and the workspace
+// that a grid of CTAs would need; it is bound by the latency of its steps, not by the few
+// bytes it moves, and from 8192 pairs on, with all eight CTAs at work, its time grows with
+// their number: 65536 pairs 9 to 11 us, 131072 16, a million 89.  Each lane asks for kBatch
+// of its ids at once.
 constexpr int kOrderThreads = 1024;
 constexpr int kOrderWarps = kOrderThreads / 32;
 constexpr int kOrderMaxExperts = 1024;
@@ -182,9 +184,10 @@ __global__ void __launch_bounds__(kOrderThreads, 1)
 // ---------------------------------------------------------------------------
 // The input is one flat sequence of 128-channel groups, as for the plain cast: eight
 // lanes take a group, a lane 16 consecutive values, cast once and stored k times.  Memory
-// bounds it, five bytes in six written: 8192 tokens of 4096 channels cast to 8 rows each
-// in 68 us, 5.1 TB/s (61 us without the rows that pad 64 experts' to groups of 128).  Bulk
-// copies in and, for each row, out of shared memory took 74.
+// bounds it, four bytes in five written: 8192 tokens of 4096 channels cast to 8 rows each
+// in 66 to 68 us, 5.1 TB/s, 5.4 with the rows that pad 64 experts' to groups of 128 (61 us
+// without those); copied as bf16 115, as codes 59.  Bulk copies in and, for each row, out of
+// shared memory took 74.
 // Form: what a row is and becomes.
 enum GatherForm { kGatherBf16, kGatherCast, kGatherCodes };
 constexpr int kGatherThreads = 256;
@@ -341,7 +344,7 @@ __global__ void __launch_bounds__(kGatherThreads, 5) gather_kernel(const GatherA
 // Half a warp takes 128 channels of a token, a lane eight of them, and adds up the
 // token's rows in the order of its experts, so a sum repeats bit for bit.  The loads
 // of up to eight rows are in flight at once: 8192 tokens of 8 rows of 4096 channels in
-// 94 us, 6.4 TB/s, bound by memory.
+// 90 to 94 us, 6.4 TB/s, bound by memory; to fp32 sums 120 us, 5.6 TB/s.
 constexpr int kReduceThreads = 256;
 constexpr int kReduceDepth = 8;
 

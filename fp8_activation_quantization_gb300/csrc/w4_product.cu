@@ -11,9 +11,11 @@
 //
 // Reading the weights bounds this: a few rows do 2 to 32 operations for each half byte.
 // Weights take the place of the MMA's 16-row operand and up to eight rows of x that of
-// the eight columns, so the weights go from memory to the tensor core once however many
-// rows there are.  (tcgen05 would want 128 of either, and its operands in shared memory
-// in 8 bits: the weights would have to be widened and stored there first.)
+// the eight columns.  An expert's rows are cut into runs of 8 or 16, and the weights are
+// read and widened once for each run: one matrix of 4096 x 4096 takes 8.5 us with one
+// row, 12 with 16, 31 with 64 and 393 with 1024.  (The 5th-generation tensor core takes
+// E2M1 operands beside FP8 ones, in bytes of shared memory that a tensor map of 4-bit
+// elements can lay out, and would take many rows a run; that form has not been built.)
 // A warp takes 32 or 64 rows of a matrix, 256 channels at a time, from a ring of its own
 // in shared memory: one TMA box of rows of 128 bytes and a bulk copy for each row of x.
 // (Copies of 16 bytes a lane took 134 us for 48 tokens, 8 of 64 matrices of 4096 x 2048,
@@ -22,8 +24,10 @@
 // channels, where otherwise some of the warps would have none left at the end.  No warp
 // waits for another but at the end of shared rows.
 // Measured: those 48 tokens 79 us (3.6 TB/s), one token's 8 matrices of 4096 x 4096 21 us
-// (3.3 TB/s); 128 channels at a time, in twice as many stages, took 13 us more for the 48.  What
-// is left is widening the weights, 7 operations for 8, and the latency of a warp's steps.
+// (3.3 TB/s), with fp32 scales 6 to 7 % less; 128 channels at a time, in twice as many stages,
+// took 13 us more for the 48.  Nothing is full there (memory 46 %, the tensor pipe 22 %, issue
+// slots 61 %): what is left is the latency of a warp's own steps, one after another; widening,
+// 7 operations for 8 weights, is over a quarter of their instructions.
 // FP8 MMAs (m16n8k32) would take codes of x as they are, but are slower here than binary16
 // ones: 190 us where those took 145.
 #include <cuda_runtime.h>
@@ -586,7 +590,10 @@ cudaError_t launch_w4_product(const W4Product& p, cudaStream_t stream) {
     a.status = device_status_word();
     const int64_t experts = p.ids ? (a.P < p.E ? a.P : p.E) : 1;  // at most this many have rows
     // eight columns where an expert has at most eight rows on average (48 tokens, 8 of 64
-    // matrices of 4096 x 2048: 101 us, with 16 columns 115, both with stages of 128 channels)
+    // matrices of 4096 x 2048: 101 us, with 16 columns 115, both with stages of 128 channels).
+    // The host knows no more than the average: where routing is uneven the busiest experts'
+    // matrices are read once for every eight of their rows (64 tokens, 8 of 64: 87 us, all of
+    // them to the same 8: 66)
     return a.P <= 8 * experts ? launch_form<1>(p, a, experts, stream) : launch_form<2>(p, a, experts, stream);
 }
 

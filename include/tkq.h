@@ -513,7 +513,9 @@ tkq_status tkq_expert_order(const int32_t* ids, int32_t* slots, int32_t* rows, i
  * are zeros (a cast one has the smallest scale, a copied one the scale 0), their
  * weight 0; rows from offsets[E] on are left as they were.
  *   slots, rows, offsets : as tkq_expert_order gives them; a slot outside [0, R) is
- *   an empty one.  The gradient of this call is tkq_expert_reduce without weights.
+ *   an empty one.  Scales are row-major fp32: the packed and the column-major layouts
+ *   (TKQ_SF_UE8M0_PACKED, TKQ_SF_COL_MAJOR) are neither read nor written.  The gradient
+ *   of this call is tkq_expert_reduce without weights.
  * T >= 0, T * k <= 2^30; C > 0, C % 128 == 0, C <= 2^20; k, E and R as above.
  * Alignment: x, out 16 bytes (bf16 rows of out 32), else 4.
  */
@@ -569,6 +571,9 @@ tkq_status tkq_expert_reduce_backward(const void* dout, const void* y, const int
  *   a : codes [R, K] in fmt_a;  a_sf : fp32 [R, K/128] (tkq_per_token_cast)
  *   w : codes [E, N, K] in fmt_w;  w_sf : fp32 [E, N/128, K/128] (tkq_per_block_cast)
  *   offsets : int32 [E + 1];  out : bf16 [R, N]
+ * Scales are row-major fp32, any values or powers of two (TKQ_SF_ROUND_POW2); the packed
+ * and the column-major layouts (TKQ_SF_UE8M0_PACKED, TKQ_SF_COL_MAJOR) are not read, here
+ * and in the two calls below.
  * R >= 0, R < 2^31; 0 < E <= 1024; N, K > 0, multiples of 128, at most 2^20,
  * E * N < 2^31.  Alignment: a, w 16 bytes, out 32, else 4.  NaN codes and infinite
  * scales give unspecified values in their own rows and columns.
@@ -609,7 +614,8 @@ tkq_status tkq_expert_weight_grad(const void* dy_t, const float* dy_sf, const vo
  *   w_sf : s of groups along K, w_group 32: UE8M0 bytes [E, N, K/32], s = 2^(byte -
  *       127) (255 is NaN), or w_group 128: fp32 [E, N, K/128]
  *   ids : int32 [T, k];  out : bf16 [T * k, N]
- * T >= 0, 0 < k <= 32, T * k <= 1024 (a larger batch is tkq_expert_product's);
+ * T >= 0, 0 < k <= 32, T * k <= 1024 (a larger batch is tkq_expert_product's; a matrix is
+ * read again for every 8 or 16 of its rows, so a few rows each are what this is for);
  * 0 < E <= 1024; N, K > 0, multiples of 128, at most 2^20, else TKQ_ERR_SHAPE;
  * w_group: TKQ_ERR_GROUP.  Alignment: x, w, out 16 bytes, else 4.  The order of the
  * sums follows the call's sizes, the experts' numbers of rows and the device's SMs:
