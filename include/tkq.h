@@ -575,8 +575,8 @@ tkq_status tkq_expert_reduce_backward(const void* dout, const void* y, const int
  * and the column-major layouts (TKQ_SF_UE8M0_PACKED, TKQ_SF_COL_MAJOR) are not read, here
  * and in the two calls below.
  * R >= 0, R < 2^31; 0 < E <= 1024; N, K > 0, multiples of 128, at most 2^20,
- * E * N < 2^31.  Alignment: a, w 16 bytes, out 32, else 4.  NaN codes and infinite
- * scales give unspecified values in their own rows and columns.
+ * E * N < 2^31.  Alignment: a, w 16 bytes, out 32, else 4.  A NaN code or scale makes
+ * NaN of its own row (its expert's column, its block of columns) and of nothing else.
  */
 tkq_status tkq_expert_product(const void* a, const float* a_sf, const void* w, const float* w_sf,
                               const int32_t* offsets, void* out, int64_t R, int64_t E, int64_t N,
